@@ -23,6 +23,10 @@ DTYPE_BF16 = 1
 FLAG_FUSE_REFRESH = 1
 FLAG_REPLAYSSM = 2
 FLAG_AUTO_FLUSH = 4
+FLAG_COPY = 8
+
+PAGE_ARRAYS_MAX = 12
+TOP_MAX = 32
 
 READ_BF16 = 0
 READ_FP8_E4M3 = 1
@@ -39,6 +43,9 @@ EXPORTS = (
     "ers_spec_verify", "ers_commit", "ers_ssu_update", "ers_ssd_scan_fwd_static", "ers_conv1d_fwd",
     "ers_conv1d_update", "ers_gdn_verify", "ers_gdn_commit", "ers_gdn_refresh", "ers_selftest_bounded_wait",
     "ers_spec_verify_exact_workspace_size", "ers_spec_verify_exact", "ers_commit_exact",
+    "ers_linattn_fwd", "ers_linattn_prefill", "ers_linattn_decode", "ers_pages_fork", "ers_pages_own_workspace_size",
+    "ers_pages_own", "ers_pages_free", "ers_pages_compact_workspace_size", "ers_pages_compact", "ers_pages_copy",
+    "ers_token_logprobs",
 )
 
 
@@ -85,6 +92,22 @@ class Cache(ctypes.Structure):
                 ("buf_pages", ctypes.c_void_p), ("page_rows", ctypes.c_int32), ("npages", ctypes.c_int32)]
 
 
+class LinAttnDims(ctypes.Structure):
+    _fields_ = [("nheads", ctypes.c_int32), ("ngroups", ctypes.c_int32), ("dk", ctypes.c_int32),
+                ("dv", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class LinAttnCache(ctypes.Structure):
+    _fields_ = [("state", ctypes.c_void_p), ("table", ctypes.c_void_p), ("nslots", ctypes.c_int32),
+                ("npages", ctypes.c_int32)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("nslots", ctypes.c_int32),
+                ("slot_pages", ctypes.c_int32), ("npages", ctypes.c_int32), ("narrays", ctypes.c_int32),
+                ("array", ctypes.c_void_p * PAGE_ARRAYS_MAX), ("page_bytes", ctypes.c_int64 * PAGE_ARRAYS_MAX)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -96,6 +119,9 @@ _U32 = ctypes.c_uint32
 _DIMS = ctypes.POINTER(Dims)
 _PRM = ctypes.POINTER(Params)
 _CACHE = ctypes.POINTER(Cache)
+_LDIMS = ctypes.POINTER(LinAttnDims)
+_LCACHE = ctypes.POINTER(LinAttnCache)
+_POOL = ctypes.POINTER(PagePool)
 
 _SIGS = {
     "ers_status_str": ([_I32], ctypes.c_char_p),
@@ -121,6 +147,17 @@ _SIGS = {
     "ers_gdn_verify": ([ctypes.POINTER(GdnDims), ctypes.POINTER(GdnCache), _I32, _P, _I32, _P, _P, _P, _P, _P,
                         _U32, _P, _P, _P], _I32),
     "ers_gdn_commit": ([ctypes.POINTER(GdnDims), ctypes.POINTER(GdnCache), _I32, _P, _P, _I32, _U32, _P, _P], _I32),
+    "ers_linattn_fwd": ([_LDIMS, _P, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P], _I32),
+    "ers_linattn_prefill": ([_LDIMS, _P, _LCACHE, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P], _I32),
+    "ers_linattn_decode": ([_LDIMS, _P, _LCACHE, _I32, _P, _P, _P, _P, _P, _P, _P, _P], _I32),
+    "ers_pages_fork": ([_POOL, _I32, _P, _P, _P, _P], _I32),
+    "ers_pages_own_workspace_size": ([_POOL, _I32], _SZ),
+    "ers_pages_own": ([_POOL, _I32, _P, _U32, _P, _P, _SZ, _P, _P], _I32),
+    "ers_pages_free": ([_POOL, _I32, _P, _P, _P], _I32),
+    "ers_pages_compact_workspace_size": ([_POOL], _SZ),
+    "ers_pages_compact": ([_POOL, _P, _P, _P, _SZ, _P, _P], _I32),
+    "ers_pages_copy": ([_POOL, _I32, _P, _P, _P, _P], _I32),
+    "ers_token_logprobs": ([_I32, _I32, _I32, _I64, _P, _P, ctypes.c_float, _I32, _P, _P, _P, _P, _P, _P], _I32),
     "ers_gdn_refresh": ([ctypes.POINTER(GdnDims), ctypes.POINTER(GdnCache), _I32, _P, _I32, _P, _P], _I32),
 }
 

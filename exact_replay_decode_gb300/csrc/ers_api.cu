@@ -5,25 +5,14 @@
 
 #include <mutex>
 
+#include "api_checks.h"
 #include "ers.h"
 #include "ers_internal.h"
 
 using ers::LaunchArgs;
+using ers::check_ptr;
 
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-ers_status check_ptr(const void* p, bool required) {
-  if (p == nullptr) return required ? ERS_EINVAL : ERS_OK;
-  return aligned16(p) ? ERS_OK : ERS_EPTR;
-}
-
-#define ERS_TRY(expr)                  \
-  do {                                 \
-    const ers_status st_ = (expr);     \
-    if (st_ != ERS_OK) return st_;     \
-  } while (0)
 
 ers_status check_dims(const ers_dims* d) {
   if (d == nullptr) return ERS_EINVAL;

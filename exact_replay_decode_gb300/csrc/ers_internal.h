@@ -177,4 +177,69 @@ struct ConvLaunch {
 };
 cudaError_t conv1d(const ConvLaunch& l, cudaStream_t s);
 
+// linear attention with a decay per head, ers_linattn.cu
+struct LinAttnArgs {
+  int H, G, dk, dv, io;
+  float scale;
+  const float* log_decay;   // [H]
+  int nseq, max_len;
+  long long ntokens;
+  const int32_t* cu;        // prompts: [nseq + 1]
+  const void* q;            // [T, G, dk]
+  const void* k;
+  const void* v;            // [T, H, dv]
+  void* o;
+  // states by sequence (init may be null: zeros) ...
+  const float* init;
+  float* final_state;
+  // ... or in the pages of a pool (pool not null)
+  float* pool;              // [npages, H, dv, dk]
+  const int32_t* table;     // [nslots] page of a slot
+  const int32_t* slot;
+  const int32_t* read_page;
+  int nslots, npages;
+  int32_t* status;
+};
+bool linattn_supported(int dk, int dv);
+cudaError_t linattn_fwd(const LinAttnArgs& a, cudaStream_t s);      // prompts
+cudaError_t linattn_decode(const LinAttnArgs& a, cudaStream_t s);   // one token per sequence
+
+// pages of a cache, ers_pages.cu
+constexpr int kMaxPageArrays = ERS_PAGE_ARRAYS_MAX;
+struct PageArgs {
+  int32_t* table;
+  int32_t* refs;
+  int nslots, slot_pages, npages, narrays;
+  char* array[kMaxPageArrays];
+  long long page_bytes[kMaxPageArrays];
+  int n;                    // listed slots (or pages, for the copy)
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t* read_page;
+  int32_t* remap;
+  int32_t* live;
+  int32_t* ws;
+  int32_t* status;
+};
+cudaError_t pages_fork(const PageArgs& a, cudaStream_t s);
+cudaError_t pages_own(const PageArgs& a, bool copy, cudaStream_t s);   // ws: 2 n slot_pages
+cudaError_t pages_free(const PageArgs& a, cudaStream_t s);
+cudaError_t pages_compact(const PageArgs& a, cudaStream_t s);          // ws: 1 + 2 npages
+cudaError_t pages_copy(const PageArgs& a, cudaStream_t s);
+
+// log probabilities of given tokens, ers_logprobs.cu
+struct LogprobArgs {
+  int io, nrows, vocab, top_k;
+  long long stride;
+  float scale;
+  const void* logits;
+  const int32_t* target;
+  float* logprob;
+  float* entropy;
+  int32_t* top_id;
+  float* top_logprob;
+  int32_t* status;
+};
+cudaError_t token_logprobs(const LogprobArgs& a, cudaStream_t s);
+
 }  // namespace ers

@@ -1,0 +1,308 @@
+// Pages of a cache (include/ers.h): counted references under a table of pages per slot.
+//
+// The decisions (which page goes where) are whole numbers with an order, a few thousand of them, so one
+// CTA takes them with prefix sums in shared memory: first everything is checked and counted, then
+// either all of it is carried out or none.  The bytes are moved by a second launch over the whole GPU.
+#include "ers_common.cuh"
+#include "ers_internal.h"
+
+namespace ers {
+namespace {
+
+constexpr int kPlan = 1024;   // threads of a deciding CTA
+
+// Inclusive prefix sum over the CTA's threads; *total receives the sum.  scratch: kPlan / 32 ints.
+__device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int u = __shfl_up_sync(kFull, v, off);
+    if (lane >= off) v += u;
+  }
+  if (lane == 31) scratch[warp] = v;
+  __syncthreads();
+  int w = scratch[lane];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int u = __shfl_up_sync(kFull, w, off);
+    if (lane >= off) w += u;
+  }
+  const int before = __shfl_sync(kFull, w, warp == 0 ? 0 : warp - 1);
+  *total = __shfl_sync(kFull, w, 31);
+  __syncthreads();   // scratch may be written again
+  return v + (warp == 0 ? 0 : before);
+}
+
+// Whether any thread found an error; the smallest code found is reported.
+__device__ __forceinline__ bool failed(int32_t err, int32_t* status) {
+  __shared__ int worst;
+  if (threadIdx.x == 0) worst = 0x7fffffff;
+  __syncthreads();
+  if (err != ERS_OK) atomicMin(&worst, err);
+  __syncthreads();
+  const int w = worst;
+  if (w != 0x7fffffff && threadIdx.x == 0) report(status, w);
+  return w != 0x7fffffff;
+}
+
+// Checks the listed slots: in range, each listed once (seen: one bit per slot, shared memory).
+__device__ __forceinline__ int32_t check_slots(const PageArgs& a, const int32_t* list, uint32_t* seen) {
+  int32_t err = ERS_OK;
+  for (int w = threadIdx.x; w < (a.nslots + 31) / 32; w += kPlan) seen[w] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n; i += kPlan) {
+    const int s = list[i];
+    if (s < 0 || s >= a.nslots) {
+      err = ERS_ESLOT;
+    } else if ((atomicOr(&seen[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u) {
+      err = ERS_EINVAL;
+    }
+  }
+  __syncthreads();
+  return err;
+}
+
+__device__ __forceinline__ bool page_ok(const PageArgs& a, int p) { return p >= -1 && p < a.npages; }
+
+__global__ void __launch_bounds__(kPlan) k_pages_fork(PageArgs a) {
+  extern __shared__ uint32_t seen[];
+  const int m = a.n * a.slot_pages;
+  int32_t err = check_slots(a, a.dst, seen);
+  for (int i = threadIdx.x; i < a.n; i += kPlan) {
+    const int s = a.src[i];
+    if (s < 0 || s >= a.nslots) err = ERS_ESLOT;
+    else if ((seen[s >> 5] >> (s & 31)) & 1u) err = ERS_EINVAL;
+  }
+  if (failed(err, a.status)) return;
+  for (int e = threadIdx.x; e < m; e += kPlan) {
+    const int i = e / a.slot_pages, c = e % a.slot_pages;
+    if (a.table[(size_t)a.dst[i] * a.slot_pages + c] != -1) err = ERS_EINVAL;   // it would be lost
+    if (!page_ok(a, a.table[(size_t)a.src[i] * a.slot_pages + c])) err = ERS_ESLOT;
+  }
+  if (failed(err, a.status)) return;
+  for (int e = threadIdx.x; e < m; e += kPlan) {
+    const int i = e / a.slot_pages, c = e % a.slot_pages;
+    const int p = a.table[(size_t)a.src[i] * a.slot_pages + c];
+    a.table[(size_t)a.dst[i] * a.slot_pages + c] = p;
+    if (p >= 0) atomicAdd(&a.refs[p], 1);
+  }
+}
+
+__global__ void __launch_bounds__(kPlan) k_pages_free(PageArgs a) {
+  extern __shared__ uint32_t seen[];
+  const int m = a.n * a.slot_pages;
+  if (failed(check_slots(a, a.dst, seen), a.status)) return;
+  int32_t err = ERS_OK;
+  for (int e = threadIdx.x; e < m; e += kPlan)
+    if (!page_ok(a, a.table[(size_t)a.dst[e / a.slot_pages] * a.slot_pages + e % a.slot_pages])) err = ERS_ESLOT;
+  if (failed(err, a.status)) return;
+  for (int e = threadIdx.x; e < m; e += kPlan) {
+    int32_t* at = &a.table[(size_t)a.dst[e / a.slot_pages] * a.slot_pages + e % a.slot_pages];
+    const int p = *at;
+    if (p >= 0) atomicSub(&a.refs[p], 1);
+    *at = -1;
+  }
+}
+
+// ws: [m] rank of an entry among those that need a page (-1: it keeps its own), then [m] the free pages
+__global__ void __launch_bounds__(kPlan) k_pages_own(PageArgs a) {
+  extern __shared__ uint32_t seen[];
+  __shared__ int scratch[kPlan / 32];
+  const int m = a.n * a.slot_pages;
+  int32_t* rank = a.ws;
+  int32_t* free_page = a.ws + m;
+  int32_t err = check_slots(a, a.dst, seen);
+  bool bad = failed(err, a.status);
+  int needed = 0, found = 0;
+  if (!bad) {
+    for (int e0 = 0; e0 < m; e0 += kPlan) {
+      const int e = e0 + threadIdx.x;
+      int need = 0, p = -1;
+      if (e < m) {
+        p = a.table[(size_t)a.dst[e / a.slot_pages] * a.slot_pages + e % a.slot_pages];
+        if (!page_ok(a, p)) err = ERS_ESLOT;
+        else need = p < 0 || a.refs[p] > 1;
+      }
+      int total;
+      const int upto = block_scan(need, scratch, &total);
+      if (e < m) {
+        rank[e] = need ? needed + upto - 1 : -1;
+        a.read_page[e] = p;
+      }
+      needed += total;
+    }
+    for (int p0 = 0; p0 < a.npages && found < needed; p0 += kPlan) {
+      const int p = p0 + threadIdx.x;
+      const int is_free = p < a.npages && a.refs[p] <= 0;
+      int total;
+      const int r = found + block_scan(is_free, scratch, &total) - 1;
+      if (is_free && r < needed) free_page[r] = p;
+      found += total;
+    }
+    if (found < needed) err = ERS_EOVERFLOW;
+    bad = failed(err, a.status);
+  }
+  if (bad) {
+    for (int e = threadIdx.x; e < m; e += kPlan) {
+      rank[e] = -1;
+      a.read_page[e] = -2;
+    }
+    return;
+  }
+  for (int e = threadIdx.x; e < m; e += kPlan) {
+    const int r = rank[e], old = a.read_page[e];
+    if (r < 0) continue;
+    const int p = free_page[r];
+    if (old >= 0) atomicSub(&a.refs[old], 1);
+    a.refs[p] = 1;
+    a.table[(size_t)a.dst[e / a.slot_pages] * a.slot_pages + e % a.slot_pages] = p;
+  }
+}
+
+// ws: [0] pages that move, [1, 1 + npages) where from, then [npages] where to
+__global__ void __launch_bounds__(kPlan) k_pages_compact(PageArgs a) {
+  __shared__ int scratch[kPlan / 32];
+  int32_t* from = a.ws + 1;
+  int32_t* to = from + a.npages;
+  int32_t err = ERS_OK;
+  for (long long e = threadIdx.x; e < (long long)a.nslots * a.slot_pages; e += kPlan)
+    if (!page_ok(a, a.table[e])) err = ERS_ESLOT;
+  const bool bad = failed(err, a.status);
+  int live = 0;
+  for (int p0 = 0; p0 < a.npages; p0 += kPlan) {
+    int total;
+    block_scan(p0 + threadIdx.x < a.npages && a.refs[p0 + threadIdx.x] > 0, scratch, &total);
+    live += total;
+  }
+  int holes = 0, movers = 0;
+  for (int p0 = 0; p0 < a.npages; p0 += kPlan) {
+    const int p = p0 + threadIdx.x;
+    const bool in = p < a.npages, used = in && a.refs[p] > 0;
+    const int hole = in && !used && p < live, mover = used && p >= live;
+    int total;
+    int r = block_scan(hole, scratch, &total);
+    if (hole) to[holes + r - 1] = p;
+    holes += total;
+    r = block_scan(mover, scratch, &total);
+    if (mover) from[movers + r - 1] = p;
+    movers += total;
+    if (in) a.remap[p] = used ? p : -1;
+  }
+  __syncthreads();
+  if (bad) movers = 0;
+  for (int r = threadIdx.x; r < movers; r += kPlan) {
+    a.remap[from[r]] = to[r];
+    a.refs[to[r]] = a.refs[from[r]];
+    a.refs[from[r]] = 0;
+  }
+  if (threadIdx.x == 0) {
+    a.ws[0] = movers;
+    *a.live = live;
+  }
+}
+
+// ---- moving the bytes -----------------------------------------------------------------------------------
+// A piece of a page is moved by a CTA in 16-byte words (2-byte ones where the page's size is no multiple).
+constexpr long long kPiece = 32768;
+
+__device__ __forceinline__ void move_piece(char* dst, const char* src, long long bytes, bool wide) {
+  if (wide) {
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    for (long long b = threadIdx.x * 16; b < bytes; b += kThreads * 16)
+      *reinterpret_cast<uint4*>(dst + b) = src != nullptr ? *reinterpret_cast<const uint4*>(src + b) : z;
+  } else {
+    for (long long b = threadIdx.x * 2; b < bytes; b += kThreads * 2)
+      *reinterpret_cast<uint16_t*>(dst + b) = src != nullptr ? *reinterpret_cast<const uint16_t*>(src + b) : uint16_t(0);
+  }
+}
+
+// page `to` of every array <- page `from` (-1: zeros), the pieces w, w + step, ...
+__device__ __forceinline__ void move_page(const PageArgs& a, int to, int from, long long w, long long step) {
+  for (int k = 0; k < a.narrays; ++k) {
+    const long long size = a.page_bytes[k], pieces = (size + kPiece - 1) / kPiece;
+    for (; w < pieces; w += step) {
+      const long long at = w * kPiece, n = size - at < kPiece ? size - at : kPiece;
+      move_piece(a.array[k] + to * size + at, from < 0 ? nullptr : a.array[k] + from * size + at, n, size % 16 == 0);
+    }
+    w -= pieces;
+  }
+}
+
+enum : int { kMoveOwn, kMoveCompact, kMoveList };
+
+template <int kind>
+__global__ void __launch_bounds__(kThreads) k_pages_move(PageArgs a) {
+  if (kind == kMoveCompact) {   // the tables follow
+    const long long entries = (long long)a.nslots * a.slot_pages;
+    const long long id = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+    for (long long e = id; e < entries; e += (long long)gridDim.x * gridDim.y * kThreads) {
+      const int p = a.table[e];
+      if (p >= 0 && p < a.npages) a.table[e] = a.remap[p];   // out of range: found by the plan, nothing moves
+    }
+  }
+  const int count = kind == kMoveCompact ? a.ws[0] : kind == kMoveOwn ? a.n * a.slot_pages : a.n;
+  for (int e = blockIdx.y; e < count; e += gridDim.y) {
+    int to, from;
+    if (kind == kMoveOwn) {
+      if (a.ws[e] < 0) continue;
+      to = a.ws[count + a.ws[e]];
+      from = a.read_page[e];
+    } else if (kind == kMoveCompact) {
+      from = a.ws[1 + e];
+      to = a.ws[1 + a.npages + e];
+    } else {
+      from = a.src[e];
+      to = a.dst[e];
+      if (from < 0 || from >= a.npages || to < 0 || to >= a.npages) {
+        if (threadIdx.x == 0) report(a.status, ERS_ESLOT);
+        continue;
+      }
+    }
+    move_page(a, to, from, blockIdx.x, gridDim.x);
+  }
+}
+
+cudaError_t move(const PageArgs& a, int kind, long long count, cudaStream_t s) {
+  long long pieces = 0;
+  for (int k = 0; k < a.narrays; ++k) pieces += (a.page_bytes[k] + kPiece - 1) / kPiece;
+  if (count == 0 || (pieces == 0 && kind != kMoveCompact)) return cudaSuccess;
+  const dim3 grid((unsigned)(pieces < 1 ? 1 : pieces > 1024 ? 1024 : pieces), (unsigned)(count > 1024 ? 1024 : count));
+  if (kind == kMoveOwn) k_pages_move<kMoveOwn><<<grid, kThreads, 0, s>>>(a);
+  else if (kind == kMoveCompact) k_pages_move<kMoveCompact><<<grid, kThreads, 0, s>>>(a);
+  else k_pages_move<kMoveList><<<grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+size_t seen_bytes(const PageArgs& a) { return (size_t)(a.nslots + 31) / 32 * sizeof(uint32_t); }
+
+template <typename K>
+cudaError_t plan(K kernel, const PageArgs& a, cudaStream_t s) {
+  const size_t smem = seen_bytes(a);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<1, kPlan, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t pages_fork(const PageArgs& a, cudaStream_t s) { return plan(k_pages_fork, a, s); }
+
+cudaError_t pages_free(const PageArgs& a, cudaStream_t s) { return plan(k_pages_free, a, s); }
+
+cudaError_t pages_own(const PageArgs& a, bool copy, cudaStream_t s) {
+  const cudaError_t e = plan(k_pages_own, a, s);
+  return e != cudaSuccess || !copy ? e : move(a, kMoveOwn, (long long)a.n * a.slot_pages, s);
+}
+
+cudaError_t pages_compact(const PageArgs& a, cudaStream_t s) {
+  k_pages_compact<<<1, kPlan, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : move(a, kMoveCompact, a.npages, s);
+}
+
+cudaError_t pages_copy(const PageArgs& a, cudaStream_t s) { return move(a, kMoveList, a.n, s); }
+
+}  // namespace ers

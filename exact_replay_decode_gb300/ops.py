@@ -263,6 +263,17 @@ class ReplayCache:
         self.buf_B = torch.zeros(*lead, ngroups, dstate, dtype=io_dtype, **z)
         self.buf_C = torch.zeros(*lead, ngroups, dstate, dtype=io_dtype, **z)
         self.pos = torch.zeros(nslots, dtype=torch.int32, **z)
+        self._pool = None
+
+    def page_pool(self):
+        """The buffers' pages as a PagePool (paged caches only).  It counts the table's entries when first asked for;
+        from then on pages change hands through it."""
+        if self.buf_pages is None:
+            raise ValueError("page_pool() is for paged buffers (paged=(page_rows, npages))")
+        if self._pool is None:
+            from .serve import PagePool
+            self._pool = PagePool([self.buf_x, self.buf_dt, self.buf_B, self.buf_C], self.buf_pages)
+        return self._pool
 
     @property
     def dims(self) -> _abi.Dims:

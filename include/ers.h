@@ -468,6 +468,137 @@ ERS_API ers_status ers_conv1d_update(const ers_conv_dims* dims, int32_t nseq, co
                                      void* y, ers_stream_t stream, int32_t* dev_status);
 
 /* ---------------------------------------------------------------------------------------------
+ * Linear attention with a decay per head.  Per head h (key group g = h / (H/G)) with a = log_decay[h]:
+ *     S_t = exp(a) S_{t-1} + v_t k_t^T   (S is [dv x dk], fp32),   o_t = scale * S_t q_t
+ * (the output is taken after the update, the state laid out as the GDN anchors are).
+ *
+ *   dims: dk and dv in {64, 128}, nheads % ngroups == 0, io_dtype for q, k, v and o; scale multiplies
+ *     the fp32 output before its one rounding.
+ *   log_decay [H] fp32, <= 0 (-inf: nothing is remembered; a positive value grows without bound).
+ *   q, k [T, G, dk], v, o [T, H, dv] in the io dtype, T = ntokens (packed by cu_seqlens [nseq+1]) or nseq (decode).
+ *   max_seqlen is the length of the longest sequence as the caller knows it (>= 0): it chooses how
+ *     the work is split, never what is computed.  A split changes the order of the state's fp32 sums, so the
+ *     bits of two calls agree when nseq, max_seqlen and dims agree.
+ * ers_linattn_fwd: prompts from init_state [nseq, H, dv, dk] (NULL: zeros); final_state [nseq, H, dv, dk] (may be
+ *   init_state itself).  An empty sequence's final state is its initial one.
+ * ers_linattn_prefill / ers_linattn_decode: the states live in the pages of a pool, cache->state [npages, H,
+ *   dv, dk]; the state of slot s is page cache->table[s], sequence i is slot[i] (NULL: i).  The state is read from
+ *   page read_page[i] (-1: zeros; NULL: the slot's own page) and the new state written to the slot's own
+ *   page, so a sequence that was forked goes on from its parent's page into its own with no copy in between.  Within
+ *   a call no slot's own page may be another sequence's own page or read page.  Decode takes one token per sequence.
+ * A NaN or infinity in a token reaches that token and later ones of its sequence and no others.
+ * Device errors: ERS_ESLOT (slot, or a page outside [0, npages)), ERS_EINVAL (cu_seqlens not ascending within
+ *   [0, ntokens]), ERS_ETIMEOUT; the sequence's outputs are then left unwritten. */
+typedef struct ers_linattn_dims {
+  int32_t nheads;
+  int32_t ngroups;
+  int32_t dk;
+  int32_t dv;
+  int32_t io_dtype;
+  float scale;
+} ers_linattn_dims;
+
+typedef struct ers_linattn_cache {
+  float* state;         /* [npages, H, dv, dk] */
+  const int32_t* table; /* [nslots] page of each slot */
+  int32_t nslots;
+  int32_t npages;
+} ers_linattn_cache;
+
+ERS_API ers_status ers_linattn_fwd(const ers_linattn_dims* dims, const float* log_decay, int32_t nseq,
+                                   int64_t ntokens, int32_t max_seqlen, const int32_t* cu_seqlens, const void* q,
+                                   const void* k, const void* v, const float* init_state, void* o, float* final_state,
+                                   ers_stream_t stream, int32_t* dev_status);
+
+ERS_API ers_status ers_linattn_prefill(const ers_linattn_dims* dims, const float* log_decay,
+                                       const ers_linattn_cache* cache, int32_t nseq, int64_t ntokens,
+                                       int32_t max_seqlen, const int32_t* cu_seqlens, const int32_t* slot,
+                                       const int32_t* read_page, const void* q, const void* k, const void* v, void* o,
+                                       ers_stream_t stream, int32_t* dev_status);
+
+ERS_API ers_status ers_linattn_decode(const ers_linattn_dims* dims, const float* log_decay,
+                                      const ers_linattn_cache* cache, int32_t nseq, const int32_t* slot,
+                                      const int32_t* read_page, const void* q, const void* k, const void* v, void* o,
+                                      ers_stream_t stream, int32_t* dev_status);
+
+/* ---------------------------------------------------------------------------------------------
+ * Pages of a cache: counted references to the pages of a pool, under a table of pages per slot.
+ *
+ *   table [nslots, slot_pages] int32: the pages of a slot, -1 where it has none; refs [npages] int32: how many
+ *   table entries name a page (0: free); array[k]: npages pages of page_bytes[k] bytes each (a multiple of 2), for
+ *   k < narrays.  One page index addresses all arrays.  nslots <= ERS_PAGE_SLOTS_MAX.
+ * Every call but ers_pages_copy is decided on the device in list order, whole or not at all: a call that finds an
+ *   error changes nothing and reports it.  Slots within one list are distinct (ERS_EINVAL).
+ * ers_pages_fork: row dst[i] of the table (all -1 before) takes the pages of row src[i]; src may repeat, a slot is
+ *   not both source and destination.  Nothing is copied.
+ * ers_pages_own: every entry of the listed slots that is -1, or whose page has more than one reference when the call
+ *   starts, gets a page of its own: the lowest free pages, in list order (ERS_EOVERFLOW if too few are free).
+ *   read_page [n, slot_pages] receives the entries as they were (-2 throughout on an error).  A page all of whose
+ *   owners are listed is free afterwards; its contents stay until a later call hands it out.  With ERS_FLAG_COPY the
+ *   new page receives the old one's contents in every array, or zeros where the entry was -1.
+ * ers_pages_free: the listed slots give up their pages.
+ * ers_pages_compact: with n pages in use, those at n and above move, in ascending order, to the free pages below n, also in
+ *   ascending order; contents, refs and table follow.  remap [npages] receives each page's new index
+ *   (-1: it was free), live [1] receives n.
+ * ers_pages_copy: page dst[i] receives page src[i] in every array (table and refs unused, may be NULL); src may repeat; no
+ *   page is both, and dst are distinct.
+ * Workspaces are 16-byte aligned buffers of the size that the query returns.
+ * Device errors: ERS_ESLOT (slot, or a page outside [0, npages)), ERS_EINVAL, ERS_EOVERFLOW. */
+#define ERS_PAGE_ARRAYS_MAX 12
+#define ERS_PAGE_SLOTS_MAX (1 << 20)
+#define ERS_FLAG_COPY 8u
+
+typedef struct ers_page_pool {
+  int32_t* table;
+  int32_t* refs;
+  int32_t nslots;
+  int32_t slot_pages;
+  int32_t npages;
+  int32_t narrays;
+  void* array[ERS_PAGE_ARRAYS_MAX];
+  int64_t page_bytes[ERS_PAGE_ARRAYS_MAX];
+} ers_page_pool;
+
+ERS_API ers_status ers_pages_fork(const ers_page_pool* pool, int32_t n, const int32_t* src, const int32_t* dst,
+                                  ers_stream_t stream, int32_t* dev_status);
+
+ERS_API size_t ers_pages_own_workspace_size(const ers_page_pool* pool, int32_t n);
+ERS_API ers_status ers_pages_own(const ers_page_pool* pool, int32_t n, const int32_t* slot, uint32_t flags,
+                                 int32_t* read_page, void* workspace, size_t workspace_bytes, ers_stream_t stream,
+                                 int32_t* dev_status);
+
+ERS_API ers_status ers_pages_free(const ers_page_pool* pool, int32_t n, const int32_t* slot, ers_stream_t stream,
+                                  int32_t* dev_status);
+
+ERS_API size_t ers_pages_compact_workspace_size(const ers_page_pool* pool);
+ERS_API ers_status ers_pages_compact(const ers_page_pool* pool, int32_t* remap, int32_t* live, void* workspace,
+                                     size_t workspace_bytes, ers_stream_t stream, int32_t* dev_status);
+
+ERS_API ers_status ers_pages_copy(const ers_page_pool* pool, int32_t n, const int32_t* src, const int32_t* dst,
+                                  ers_stream_t stream, int32_t* dev_status);
+
+/* ---------------------------------------------------------------------------------------------
+ * Log probabilities of given tokens, with the distribution's entropy and its top alternatives: what a draft, a
+ * branch or a sample is scored by.  Per row r of logits [nrows, vocab] (row_stride elements apart; bf16 or
+ * fp32), with m = max_j x_j, d_j = scale (x_j - m), z = sum_j exp(d_j), in fp32:
+ *     logprob[r]      = d_target - log z
+ *     entropy[r]      = log z - sum_j exp(d_j) d_j / z                          (nats)
+ *     top_id[r][0..k) = the k highest logits, highest first, the lowest index first among equals
+ *     top_logprob     = theirs
+ * A logit of -inf is masked: never a top alternative (where fewer than k are left, -1 and -inf fill up).  A row of
+ * -inf alone has logprob -inf and entropy 0.  The type's lowest finite value is an ordinary value: a row of it alone is an
+ * even distribution.  A row with a NaN or +inf has no distribution: its floats are NaN, its ids -1.
+ * target [nrows] int32 in [0, vocab), or -1: no target, logprob 0.  A target outside reports ERS_EINVAL and
+ * its logprob is NaN.  target and logprob may both be NULL; entropy may be NULL; top_k in [0,
+ * ERS_TOP_MAX], with top_id and top_logprob [nrows, top_k] NULL when it is 0.  scale > 0 (an inverse temperature),
+ * finite.  logits needs its elements' own alignment only; row_stride >= vocab >= 1. */
+#define ERS_TOP_MAX 32
+ERS_API ers_status ers_token_logprobs(int32_t io_dtype, int32_t nrows, int32_t vocab, int64_t row_stride,
+                                      const void* logits, const int32_t* target, float scale, int32_t top_k,
+                                      float* logprob, float* entropy, int32_t* top_id, float* top_logprob,
+                                      ers_stream_t stream, int32_t* dev_status);
+
+/* ---------------------------------------------------------------------------------------------
  * ers_ssd_scan_fwd with library-owned scratch.  The pages have no counterpart to this call; it
  * exists for callers that cannot hand the scan a workspace: a host program that owns no device
  * allocator (plain C over the runtime, no tensor library), and serving loops that must not
