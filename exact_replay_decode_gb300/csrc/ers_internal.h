@@ -203,6 +203,8 @@ struct LinAttnArgs {
 bool linattn_supported(int dk, int dv);
 cudaError_t linattn_fwd(const LinAttnArgs& a, cudaStream_t s);      // prompts
 cudaError_t linattn_decode(const LinAttnArgs& a, cudaStream_t s);   // one token per sequence
+bool linattn_tc_supported(const LinAttnArgs& a);                    // chunks on the tensor cores, ers_linattn_tc.cu
+cudaError_t linattn_tc(const LinAttnArgs& a, cudaStream_t s);
 
 // pages of a cache, ers_pages.cu
 constexpr int kMaxPageArrays = ERS_PAGE_ARRAYS_MAX;

@@ -101,6 +101,7 @@ cudaError_t decode(const LinAttnArgs& a, cudaStream_t s) {
 bool linattn_supported(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
 
 cudaError_t linattn_fwd(const LinAttnArgs& a, cudaStream_t s) {
+  if (linattn_tc_supported(a)) return linattn_tc(a, s);
   if (a.io == ERS_DTYPE_BF16)
     return a.dk == 64 ? steps<__nv_bfloat16, 64>(a, s) : steps<__nv_bfloat16, 128>(a, s);
   return a.dk == 64 ? steps<float, 64>(a, s) : steps<float, 128>(a, s);
