@@ -1,22 +1,26 @@
 // Linear attention with a decay per head over prompts, on the tensor cores (bf16 io).
 //
 // Chunks of 128 tokens; rows i, j of a chunk of n tokens that starts from state H ([dv x dk]), lambda = exp(a):
-//   P[i,j] = (q_i . k_j) lambda^(i-j)  [j <= i]
-//   O[i]   = scale * (sum_j P[i,j] v_j + lambda^(i+1) H q_i)
-//   H'     = lambda^n H + sum_j (lambda^(n-1-j) v_j) k_j^T
+//   O[i] = scale * (sum_{j <= i} (q_i . k_j) lambda^(i-j) v_j + lambda^(i+1) H q_i)
+//   H'   = lambda^n H + sum_j (lambda^(n-1-j) v_j) k_j^T
 // Four contractions of 128 x 128 x 128 (at dk = dv = 128), tcgen05 kind::f16 with fp32 accumulators:
-//   S = Q K^T                                    A, B from shared memory (TMA tiles)
-//   O = Q H^T, scaled by lambda^(i+1) in place   B = H as bf16 hi + lo (two chains)
-//   O += P V                                     A = P as bf16 hi + lo in tensor memory, over S
-//   H += V'^T K                                  A = V' = lambda^(n-1-j) v_j as hi + mid + lo in tensor memory
+//   S = Q K^T            A, B from shared memory (TMA tiles)
+//   H += V'^T K          A = V' = lambda^(n-1-j) v_j as bf16 hi + mid + lo in tensor memory
+//   O = Q H'^T + P V     B = H' as hi + lo in shared memory, A = P as hi + lo in tensor memory, over S
+// The decays of a row are taken out of the products: with P[i,j] = S[i,j] lambda^(63-j) and H' = lambda^64 H the row's output is
+// scale lambda^(i-63) O[i], and both products go into one accumulator.  All factors lie within lambda^(+-64), which fp32
+// and bf16 hold down to a = -1 (6e+-27).  Below that (kStrong) P carries lambda^(i-j), H' = H, and the accumulator
+// is multiplied by lambda^(i+1) between the two products.
 // Operands made from fp32 values are split so that outputs keep 16 significant bits before their one rounding (a single
 // bf16 term would cost half as much again as that rounding) and states all 24.  The state stays in tensor memory in
 // fp32 from chunk to chunk.
 //
-// What bounds it: at one CTA per SM a chunk moves 128 KB (2.9 us of an SM's share of the memory), 8 MMA chains of
-// 4.2 MFLOP and about 3000 issue slots of operand making per scheduler, in one dependent loop through the state.  So the
-// warps are specialised: warp 8 loads and stores tiles (TMA; two buffers for K and V, one for Q), warp 9 issues every MMA, warps 0-3 own the
-// rows i (scores, outputs), warps 4-7 the rows of the state (V', H), and the two groups run side by side.
+// What bounds it: at one CTA per SM a chunk moves 128 KB (2.9 us of an SM's share of the memory), 64 MMAs of 64 cycles
+// and some 2500 issue slots of operand making per scheduler, in one dependent loop through the state.  So the warps are
+// specialised and run side by side, and the MMAs are ordered S, H, O so that each group's work on one product lies under the
+// others: while H accumulates the scores become P and the last chunk's outputs are stored; while O accumulates the state is
+// handed on.  Four warps make P and own the outputs, eight make V' and hand the state on, one loads the tiles (TMA; two
+// buffers for K and V, one for Q) and one issues every MMA.
 //
 // A long sequence of few heads is split over the CTAs of a cluster, each a run of chunks: every CTA but the
 // last first forms its run's own end state (K and V only), the cluster turns those into start states through
@@ -37,51 +41,69 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 128;                  // tokens of a chunk
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kBlock = 320;
+// warps 0-3 make P and own the outputs, 4-7 and 8-11 (two sets) the state; lane quarter: warp % 4.  14 warps: 128 registers
+// each, for with spills every reload would go to L2 (the first-level cache is all shared memory).
+constexpr int kStateThread = 128, kStateThreads = 256;
+constexpr int kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kBlock = 448;
+constexpr float kStrong = -1.f;
 constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384, kVStage = 48, kTmemCols = 512;
-constexpr uint32_t kBarState = 1;       // named barrier of warps 4-7
+constexpr uint32_t kBarState = 1, kBarRows = 2, kBarSet = 3;   // named barriers of the warps of a kind
 
 struct Hdr {
   alignas(16) float w[2][kC];        // lambda^(n-1-j), 0 from n on: a full chunk, the last chunk (read 16 bytes at a time)
+  alignas(16) float power[kC + 4];   // lambda^(63-j) of the columns j; kStrong: lambda^j
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, q_empty;   // tile buffers
-  uint64_t s_ready, o2_ready, o_ready, kv_done, v_free[2];    // completed by the tensor core
-  uint64_t pv_go, o_free, o_staged, h_ready, v_ready[2];      // by the warpgroups
+  uint64_t s_ready, qh_done, o_ready, kv_done, v_free[2];               // completed by the tensor core
+  uint64_t p_ready, o_scaled, o_free, h_ready, v_ready[2];    // by the warps
   uint32_t tmem;
   int dead;                          // a wait gave up: no further wait waits, no copy or MMA is issued
   float step_hi, step_lo;            // lambda^128 as two floats,
   float last_hi, last_lo;            // lambda^n of the sequence's last chunk
-  float power[kC + 1];               // lambda^j
-  int bad[2][4];                     // a chunk's value columns (by state warp) hold something not finite,
-  uint8_t first_bad[2][kC];          // from this token on (128: nowhere)
+  float mid;                         // lambda^64
+  alignas(8) uint8_t bad[2][8];      // a chunk's value columns (by state warp) hold something not finite,
+  uint8_t first_bad[2][2][kC];       // from this token of the set's quarters on (128: nowhere)
 };
 
 struct Maps {
-  CUtensorMap q, k, v, o;
+  CUtensorMap q, k, v;
 };
 
 template <int DK, int DV>
 struct Shape {
   static constexpr uint32_t ktile = kC * DK * 2, vtile = kC * DV * 2;
   static constexpr uint32_t hterm = DV * DK * 2;       // one bf16 term of the state operand
-  static constexpr uint32_t smem = 1024 + sizeof(Hdr) + 3 * ktile + 2 * vtile + 2 * hterm;
+  static constexpr uint32_t smem = sizeof(Hdr) + 3 * ktile + 2 * vtile + 2 * hterm;
   static_assert(smem <= 227 * 1024, "one CTA's shared memory");
 };
 
 // ---- waits -----------------------------------------------------------------------------------------------
-__device__ __forceinline__ void wait(Hdr& hd, uint64_t* bar, uint32_t parity, int32_t* status) {
-  if (mbar_try(bar, parity)) return;
+// The code of a wait is kept short (six kinds of warps share the instruction caches): the polling loop is one function.
+__device__ __noinline__ void wait_slow(int* dead, uint64_t* bar, uint32_t parity, int32_t* status) {
   const uint64_t t0 = globaltimer();
-  while (!mbar_try(bar, parity)) {
-    if (*(volatile int*)&hd.dead != 0) return;
+  for (;;) {
+#pragma unroll 1
+    for (int n = 0; n < 16; ++n)
+      if (mbar_try(bar, parity)) return;
+    if (*(volatile int*)dead != 0) return;
     if (globaltimer() - t0 > kWaitLimitNs) {
       if (status != nullptr) atomicCAS(status, 0, ERS_ETIMEOUT);
-      *(volatile int*)&hd.dead = 1;
+      *(volatile int*)dead = 1;
       return;
     }
   }
 }
+__device__ __forceinline__ void wait(Hdr& hd, uint64_t* bar, uint32_t parity, int32_t* status) {
+  if (!mbar_try(bar, parity)) wait_slow(&hd.dead, bar, parity, status);
+}
 __device__ __forceinline__ bool dead(const Hdr& hd) { return *(const volatile int*)&hd.dead != 0; }
+
+// one lane of a converged warp
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 
 // ---- PTX that the other engines do not need ------------------------------------------------------------------
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -101,20 +123,60 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) 
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+// A load that goes on while the thread works; arrived() before its values are used.
+__device__ __forceinline__ void tmem_ld32_begin(uint32_t at, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
 }
-__device__ __forceinline__ void tma_store_3d(const void* map, const void* src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
-               "r"(y), "r"(z), "r"(smem_u32(src))
+__device__ __forceinline__ void arrived(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+// f(x, values) for the 32-column groups x, x + 32, ... of [0, n)
+template <typename F>
+__device__ __forceinline__ void tmem_each32(uint32_t at, int n, F f) {
+#pragma unroll 1
+  for (int x = 0; x < n; x += 32) {
+    uint32_t r[32];
+    tmem_ld32_begin(at + x, r);
+    arrived(r);
+    f(x, r);
+  }
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// 16 lanes x 16 columns in the layout of ldmatrix: thread t holds, of column group g (4 columns), row t / 4 in r[2g] and
+// row t / 4 + 8 in r[2g + 1], column t % 4
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void st_global_32(void* to, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -136,18 +198,37 @@ __device__ __forceinline__ void peer_st(uint32_t addr, float4 v) {
                : "memory");
 }
 
-// ---- bf16 terms ------------------------------------------------------------------------------------------------
-// (a, b) -> packed bf16 hi terms (a in the low half), leaving the remainders in a and b
-__device__ __forceinline__ uint32_t take_term(float& a, float& b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
-  a = __fsub_rn(a, __uint_as_float(u << 16));
-  b = __fsub_rn(b, __uint_as_float(u & 0xffff0000u));
-  return u;
+// ---- pairs of floats (one instruction for two) and their bf16 terms -----------------------------------------------
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
-__device__ __forceinline__ uint32_t last_term(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); }
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+__device__ __forceinline__ void unpair(uint64_t v, uint32_t& x, uint32_t& y) { asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v)); }
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// both rounded to bf16, the first in the low half
+__device__ __forceinline__ uint32_t round2(uint64_t v) {
+  float x, y;
+  unpair(v, x, y);
+  return pack_bf16x2(x, y);
+}
+// the bf16 term of both; what it leaves stays in v (exactly)
+__device__ __forceinline__ uint32_t take_term(uint64_t& v) {
+  const uint32_t u = round2(v);
+  v = fma2(pair(u << 16, u & 0xffff0000u), both(-1.f), v);
+  return u;
 }
 
 // A CTA's share of the work.
@@ -168,6 +249,8 @@ struct Cta {
   uint8_t* hop;        // state operand: hi, then lo; between the two passes the fp32 state itself
   uint32_t tb;
   int h, g;
+  float a_h;
+  bool strong;
   Run run;
 
   // Chunks are numbered m = 0, 1, ... over both passes; number m uses K and V buffer m % 2 for the m / 2th time.
@@ -176,8 +259,20 @@ struct Cta {
   __device__ __forceinline__ uint8_t* qbuf() const { return tiles + 2 * Sh::ktile + 2 * Sh::vtile; }
   __device__ __forceinline__ int rows(int c) const { return run.len - c * kC < kC ? run.len - c * kC : kC; }
   __device__ __forceinline__ void wt(uint64_t* bar, uint32_t parity) const { wait(hd, bar, parity & 1u, a.status); }
+  // one warp of a kind polls, the others wait for it
+  __device__ __forceinline__ void wt_rows(uint64_t* bar, uint32_t parity) const {
+    if (threadIdx.x < 32) wt(bar, parity);
+    named_sync(kBarRows, kStateThread);
+    after_sync();
+  }
+  __device__ __forceinline__ int set() const { return (threadIdx.x - kStateThread) / 128; }
+  __device__ __forceinline__ void wt_set(uint64_t* bar, uint32_t parity) const {
+    if (threadIdx.x % 128 < 32) wt(bar, parity);
+    named_sync(kBarSet + set(), 128);
+    after_sync();
+  }
 
-  // ---- warp 8: tiles in, outputs out ------------------------------------------------------------------------
+  // ---- the loading warp ------------------------------------------------------------------------
   __device__ __forceinline__ void load(uint8_t* to, const CUtensorMap* map, int d, int head, int c, uint64_t* bar) const {
     if (dead(hd)) return;
     mbar_arrive_expect_tx(bar, kC * d * 2);
@@ -197,8 +292,7 @@ struct Cta {
       load_v(c - run.c0, c);
     }
   }
-  // In the order in which buffers come free: Q after Q H^T, K after V'^T K, V when the output, which takes its
-  // place after P V, has been stored.  (The rows of a short chunk are stored by their owners.)
+  // In the order in which buffers come free: K after V'^T K, Q after Q H^T, V after P V.
   __device__ __forceinline__ void load_chunks(int m0) const {
     const int n = run.c1 - run.c0;
     load_k(m0, run.c0);
@@ -208,21 +302,12 @@ struct Cta {
       load_k(m0 + 1, run.c0 + 1);
       load_v(m0 + 1, run.c0 + 1);
     }
-    for (int i = 0; i < n; ++i) {
+#pragma unroll 1
+    for (int i = 0; i + 1 < n; ++i) {
       const int c = run.c0 + i;
-      if (i + 1 < n) {
-        wt(&hd.q_empty, i);
-        load(qbuf(), &maps.q, DK, g, c + 1, &hd.q_full);
-      }
       if (i + 2 < n) load_k(m0 + i + 2, c + 2);
-      wt(&hd.o_staged, i);
-      if (!dead(hd) && rows(c) == kC) {
-        for (int x = 0; x < DV; x += 64)
-          tma_store_3d(&maps.o, vbuf(m0 + i) + x / 64 * (kC * 128), x, h, run.t0 + c * kC);
-        bulk_commit();
-        bulk_wait_read();
-      }
-      mbar_arrive(&hd.v_empty[(m0 + i) & 1]);
+      wt(&hd.q_empty, i);
+      load(qbuf(), &maps.q, DK, g, c + 1, &hd.q_full);
       if (i + 2 < n) load_v(m0 + i + 2, c + 2);
     }
   }
@@ -232,341 +317,384 @@ struct Cta {
     while (globaltimer() - t0 < 2000000) {}   // 2 ms: a thousand times what a tile or an MMA takes
   }
 
-  // ---- warp 9: every MMA --------------------------------------------------------------------------------------
+  // ---- the issuing warp: every MMA --------------------------------------------------------------------------------------
+  // The whole warp runs the loops (their operands then live in uniform registers), one lane issues.  Descriptors step by
+  // constants: 16 columns of a tile are 32 bytes on, in units of 16, and 64 columns an atom of `rows` rows on.
+  __device__ __forceinline__ void chain(uint32_t d, uint64_t ad, uint64_t bd, int arows, int brows, int n, uint32_t id,
+                                        bool accumulate, bool leader) const {
+#pragma unroll 1
+    for (int k = 0; k < n; k += 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (leader) mma(d, ad + 2 * j, bd + 2 * j, id, accumulate || k + j > 0);
+      ad += (uint64_t)arows * 8;
+      bd += (uint64_t)brows * 8;
+    }
+  }
   // one quarter (32 tokens) of H += V'^T K
-  __device__ __forceinline__ void state_quarter(uint32_t kt, int quarter, uint32_t stage, bool accumulate) const {
+  __device__ __forceinline__ void state_quarter(uint64_t kd, uint32_t stage, bool accumulate, bool leader) const {
     constexpr uint32_t id = idesc_bf16(128, DK, false, true);
-    for (int term = 0; term < 3; ++term)
-      for (int ks = 0; ks < 2; ++ks)
-        mma_ts(tb + kColH, tb + kColV + stage * kVStage + term * 16 + ks * 8,
-               sdesc(kt + (32 * quarter + 16 * ks) * 128, kC * 128, 1024), id, accumulate || term + ks > 0);
+    uint32_t at = tb + kColV + stage * kVStage;
+#pragma unroll 1
+    for (int term = 0; term < 3; ++term, at += 16) {
+      if (leader) {
+        mma_ts(tb + kColH, at, kd, id, accumulate || term > 0);
+        mma_ts(tb + kColH, at + 8, kd + 16 * 128 / 16, id, 1);
+      }
+    }
+  }
+  __device__ __forceinline__ uint64_t by_token(const uint8_t* tile) const { return sdesc(smem_u32(tile), kC * 128, 1024); }
+  // the quarters of chunk number m; false: a wait gave up
+  __device__ __forceinline__ bool state_chunk(int m, int& quarters, bool accumulate, bool leader) const {
+    uint64_t kd = by_token(kbuf(m));
+#pragma unroll 1
+    for (int quarter = 0; quarter < 4; ++quarter, ++quarters, kd += 32 * 128 / 16) {
+      wt(&hd.v_ready[quarters & 1], quarters >> 1);
+      after_sync();
+      if (dead(hd)) return false;
+      state_quarter(kd, quarters & 1, accumulate || quarter > 0, leader);
+      if (leader) commit(&hd.v_free[quarters & 1]);
+    }
+    return true;
   }
   __device__ __forceinline__ void issue_states(int& quarters) const {
+    const bool leader = elected();
     const int n = run.c1 - run.c0;
     for (int m = 0; m < n; ++m) {
       wt(&hd.k_full[m & 1], m / 2);
       after_sync();
-      for (int quarter = 0; quarter < 4; ++quarter, ++quarters) {
-        wt(&hd.v_ready[quarters & 1], quarters >> 1);
-        after_sync();
-        if (dead(hd)) return;
-        state_quarter(smem_u32(kbuf(m)), quarter, quarters & 1, m > 0 || quarter > 0);
-        commit(&hd.v_free[quarters & 1]);
+      if (!state_chunk(m, quarters, m > 0, leader)) return;
+      if (leader) {
+        commit(&hd.k_empty[m & 1]);
+        commit(&hd.v_empty[m & 1]);
       }
-      commit(&hd.k_empty[m & 1]);
-      commit(&hd.v_empty[m & 1]);
     }
-    commit(&hd.kv_done);
+    if (leader) commit(&hd.kv_done);
   }
   __device__ __forceinline__ void issue_chunks(int m0, int quarters, bool fresh) const {
     constexpr uint32_t id_s = idesc_bf16(128, kC, false, false), id_h = idesc_bf16(128, DV, false, false),
                        id_v = idesc_bf16(128, DV, false, true);
-    const uint32_t qt = smem_u32(qbuf()), ht = smem_u32(hop);
+    const uint64_t qd = sdesc(smem_u32(qbuf()), 16, 1024), h_hi = sdesc(smem_u32(hop), 16, 1024);
+    const bool leader = elected();
+#pragma unroll 1
     for (int i = 0; i < run.c1 - run.c0; ++i) {
       const int m = m0 + i;
-      const uint32_t kt = smem_u32(kbuf(m)), vt = smem_u32(vbuf(m));
       const bool with_h = !(fresh && i == 0);
       wt(&hd.k_full[m & 1], m / 2);
       wt(&hd.q_full, i);
       after_sync();
       if (dead(hd)) return;
-      for (int k = 0; k < DK / 16; ++k) {
-        const uint32_t at = (k >> 2) * (kC * 128) + (k & 3) * 32;
-        mma(tb + kColS, sdesc(qt + at, 16, 1024), sdesc(kt + at, 16, 1024), id_s, k > 0);
-      }
-      commit(&hd.s_ready);
+      chain(tb + kColS, qd, sdesc(smem_u32(kbuf(m)), 16, 1024), kC, kC, DK / 16, id_s, false, leader);
+      if (leader) commit(&hd.s_ready);
       wt(&hd.h_ready, i);
+      after_sync();
+      if (!state_chunk(m, quarters, with_h, leader)) return;
+      if (leader) {
+        commit(&hd.kv_done);
+        commit(&hd.k_empty[m & 1]);
+      }
       if (i > 0) wt(&hd.o_free, i - 1);
       after_sync();
       if (dead(hd)) return;
-      if (with_h)
-        for (int term = 0; term < 2; ++term)
-          for (int k = 0; k < DK / 16; ++k)
-            mma(tb + kColO, sdesc(qt + (k >> 2) * (kC * 128) + (k & 3) * 32, 16, 1024),
-                sdesc(ht + term * Sh::hterm + (k >> 2) * (DV * 128) + (k & 3) * 32, 16, 1024), id_h, term + k > 0);
-      commit(&hd.o2_ready);
-      commit(&hd.q_empty);
-      for (int quarter = 0; quarter < 4; ++quarter, ++quarters) {
-        wt(&hd.v_ready[quarters & 1], quarters >> 1);
-        after_sync();
-        if (dead(hd)) return;
-        state_quarter(kt, quarter, quarters & 1, with_h || quarter > 0);
-        commit(&hd.v_free[quarters & 1]);
-      }
-      commit(&hd.kv_done);
-      commit(&hd.k_empty[m & 1]);
-      wt(&hd.pv_go, i);
-      after_sync();
-      if (dead(hd)) return;
-      for (int k = 0; k < kC / 16; ++k)
-        for (int term = 0; term < 2; ++term)
-          mma_ts(tb + kColO, tb + kColS + (k >> 2) * 64 + term * 32 + (k & 3) * 8, sdesc(vt + 16 * k * 128, kC * 128, 1024),
-                 id_v, with_h || k + term > 0);
-      commit(&hd.o_ready);
-    }
-  }
-
-  // ---- warps 0-3: scores and outputs, a thread per row ----------------------------------------------------------
-  __device__ __forceinline__ void outputs(int m0, bool fresh) const {
-    const int t = threadIdx.x, warp = t / 32;
-    const uint32_t lane0 = tb + ((uint32_t)(32 * warp) << 16);
-    float u[16];                                   // lambda^(15-j)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) u[j] = hd.power[15 - j];
-    const float carry = hd.power[t + 1];           // lambda^(t+1)
-    for (int c = run.c0; c < run.c1; ++c) {
-      const int i = c - run.c0;
-      const bool with_h = !(fresh && i == 0);
-      wt(&hd.s_ready, i);
-      after_sync();
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        uint32_t hi[32], lo[32];
-        float s[64];
-        if (64 * half <= 32 * warp + 31) tmem_ld64(lane0 + kColS + 64 * half, s);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int j0 = 64 * half + 16 * b;        // columns [j0, j0 + 16)
-          if (j0 + 15 <= 32 * warp) {               // all at or below the diagonal
-            const float f = hd.power[t - j0 - 15];
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              float x = s[16 * b + j] * u[j] * f, y = s[16 * b + j + 1] * u[j + 1] * f;
-              hi[8 * b + j / 2] = take_term(x, y);
-              lo[8 * b + j / 2] = last_term(x, y);
-            }
-          } else if (j0 <= 32 * warp + 31) {        // on the diagonal
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              float x = j0 + j <= t ? s[16 * b + j] * hd.power[t - j0 - j] : 0.f;
-              float y = j0 + j + 1 <= t ? s[16 * b + j + 1] * hd.power[t - j0 - j - 1] : 0.f;
-              hi[8 * b + j / 2] = take_term(x, y);
-              lo[8 * b + j / 2] = last_term(x, y);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) hi[8 * b + j] = lo[8 * b + j] = 0;
-          }
-        }
-        tmem_st32(lane0 + kColS + 64 * half, hi);
-        tmem_st32(lane0 + kColS + 64 * half + 32, lo);
-      }
-      wt(&hd.o2_ready, i);
-      after_sync();
       if (with_h) {
 #pragma unroll 1
-        for (int x = 0; x < DV; x += 32) {
-          float o[32];
-          uint32_t r[32];
-          tmem_ld32(lane0 + kColO + x, o);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(o[j] * carry);
-          tmem_st32(lane0 + kColO + x, r);
-        }
+        for (int term = 0; term < 2; ++term)
+          chain(tb + kColO, qd, h_hi + (Sh::hterm >> 4) * term, kC, DV, DK / 16, id_h, term > 0, leader);
       }
-      tmem_wait_st();
-      before_sync();
-      mbar_arrive(&hd.pv_go);
-      wt(&hd.o_ready, i);
+      if (leader) {
+        commit(&hd.qh_done);
+        commit(&hd.q_empty);
+      }
+      if (strong) wt(&hd.o_scaled, i);
+      wt(&hd.p_ready, i);
       after_sync();
-      const int live = rows(c);
-      const int* bad4 = hd.bad[i & 1];
-      const bool bad = (bad4[0] | bad4[1] | bad4[2] | bad4[3]) != 0;
-      uint8_t* stage = vbuf(m0 + i);           // P V is done with it
-      bf16* out = (bf16*)a.o + ((size_t)(run.t0 + c * kC + t) * a.H + h) * DV;
+      if (dead(hd)) return;
+      uint64_t vd = by_token(vbuf(m));
+      uint32_t pt = tb + kColS;
 #pragma unroll 1
-      for (int x = 0; x < DV; x += 32) {
-        float o[32];
-        tmem_ld32(lane0 + kColO + x, o);
-        if (bad) {
+      for (int k = 0; k < kC / 16; k += 2) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (t >= hd.first_bad[i & 1][x + j]) o[j] = __int_as_float(0x7fffffff);
-        }
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint4 v;
-          v.x = last_term(o[j] * a.scale, o[j + 1] * a.scale);
-          v.y = last_term(o[j + 2] * a.scale, o[j + 3] * a.scale);
-          v.z = last_term(o[j + 4] * a.scale, o[j + 5] * a.scale);
-          v.w = last_term(o[j + 6] * a.scale, o[j + 7] * a.scale);
-          if (live == kC) *reinterpret_cast<uint4*>(stage + sw128(kC, t, x + j)) = v;
-          else if (t < live && !dead(hd)) *reinterpret_cast<uint4*>(out + x + j) = v;
+        for (int j = 0; j < 2; ++j, vd += 16 * 128 / 16, pt += 16) {
+          if (leader) {
+            mma_ts(tb + kColO, pt, vd, id_v, with_h || k + j > 0);
+            mma_ts(tb + kColO, pt + 8, vd, id_v, 1);
+          }
         }
       }
-      before_sync();
-      mbar_arrive(&hd.o_free);
-      fence_async_smem();
-      mbar_arrive(&hd.o_staged);
+      if (leader) {
+        commit(&hd.o_ready);
+        commit(&hd.v_empty[m & 1]);
+      }
     }
   }
 
-  // ---- warps 4-7: V' and the state, a thread per state row --------------------------------------------------------
-  // quarter `quarter` of V' of a chunk: 32 tokens as three terms into tensor memory.  f multiplies the weights.
-  // nan collects whether anything was not finite.
-  __device__ __forceinline__ void make_quarter(const uint8_t* vt, const float* w, float f, int quarter, int& quarters,
-                                               float& nan) const {
-    const int d = threadIdx.x - 128;
-    if (quarters >= 2) {
-      wt(&hd.v_free[quarters & 1], (quarters >> 1) - 1);
-      after_sync();
+  // ---- warps 0-3: P over S, and the outputs, a thread per row ------------------------------------------------------------------
+  __device__ __forceinline__ void rows_of_chunks(bool fresh) const {
+    for (int c = run.c0; c < run.c1; ++c) {
+      const int i = c - run.c0;
+      wt_rows(&hd.s_ready, i);
+      scores();
+      mbar_arrive(&hd.p_ready);
+      if (strong) {
+        wt_rows(&hd.qh_done, i);
+        if (!(fresh && i == 0)) scale_rows();
+        mbar_arrive(&hd.o_scaled);
+      }
+      wt_rows(&hd.o_ready, i);
+      outputs(c);
+      mbar_arrive(&hd.o_free);
     }
-    if (d < DV) {
-      uint32_t r[3][16];
+  }
+  // Columns [16 b, 16 b + 16) of S become the hi terms of P in the first 8 columns of the block and the lo terms in the others.
+  __device__ __forceinline__ void scores() const {
+    const int t = threadIdx.x, quarter = t / 32;
+    const uint32_t at = tb + ((uint32_t)(32 * quarter) << 16) + kColS;
+    tmem_each32(at, 32 * (quarter + 1), [&](int x, uint32_t (&s)[32]) {
+      const bool below = x < 32 * quarter;       // the diagonal, in all of the warp's rows
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const int s = 32 * quarter + j;
-        const float4 w4 = *reinterpret_cast<const float4*>(w + s);
-        const float ws[4] = {w4.x * f, w4.y * f, w4.z * f, w4.w * f};
-        float x[4];
+      for (int b = 0; b < 32; b += 16) {
+        uint32_t r[16];
+        if (!strong) {
+          const ulonglong2* w = reinterpret_cast<const ulonglong2*>(hd.power + x + b);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = __bfloat162float(*reinterpret_cast<const bf16*>(vt + sw128(kC, s + e, d)));
-          nan = fmaf(v, 0.f, nan);
-          x[e] = v * ws[e];
+          for (int j = 0; j < 4; ++j) {
+            const ulonglong2 w4 = w[j];
+            uint64_t p = mul2(pair(s[b + 4 * j], s[b + 4 * j + 1]), w4.x), q = mul2(pair(s[b + 4 * j + 2], s[b + 4 * j + 3]), w4.y);
+            if (!below) {                        // selected, not multiplied: a masked score may be anything
+              uint32_t y, z;
+              const int e = t - x - b - 4 * j;
+              unpair(p, y, z);
+              p = pair(e >= 0 ? y : 0u, e >= 1 ? z : 0u);
+              unpair(q, y, z);
+              q = pair(e >= 2 ? y : 0u, e >= 3 ? z : 0u);
+            }
+            r[2 * j] = take_term(p);
+            r[8 + 2 * j] = round2(p);
+            r[2 * j + 1] = take_term(q);
+            r[9 + 2 * j] = round2(q);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int e = t - x - b - 2 * j;
+            uint64_t p = pair(e >= 0 ? __uint_as_float(s[b + 2 * j]) * hd.power[e] : 0.f,
+                              e >= 1 ? __uint_as_float(s[b + 2 * j + 1]) * hd.power[e - 1] : 0.f);
+            r[j] = take_term(p);
+            r[8 + j] = round2(p);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          r[0][(j + e) / 2] = take_term(x[e], x[e + 1]);
-          r[1][(j + e) / 2] = take_term(x[e], x[e + 1]);
-          r[2][(j + e) / 2] = last_term(x[e], x[e + 1]);
+        for (int j = 0; j < 16; ++j) s[b + j] = r[j];
+      }
+      tmem_st32(at + x, s);
+    });
+#pragma unroll 1
+    for (int x = 32 * (quarter + 1); x < kC; x += 32) {   // above the diagonal
+      const uint32_t zero[32] = {};
+      tmem_st32(at + x, zero);
+    }
+    tmem_wait_st();
+    before_sync();
+  }
+  // kStrong: the state's part of the outputs, times lambda^(i+1)
+  __device__ __forceinline__ void scale_rows() const {
+    const int t = threadIdx.x;
+    const uint32_t at = tb + ((uint32_t)(t & ~31) << 16) + kColO;
+    const uint64_t carry = both(hd.power[t + 1]);
+    tmem_each32(at, DV, [&](int x, uint32_t (&o)[32]) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) unpair(mul2(pair(o[j], o[j + 1]), carry), o[j], o[j + 1]);
+      tmem_st32(at + x, o);
+    });
+    tmem_wait_st();
+    before_sync();
+  }
+  __device__ __forceinline__ void outputs(int c) const {
+    const int t = threadIdx.x, i = c - run.c0;
+    const uint32_t at = tb + ((uint32_t)(t & ~31) << 16) + kColO;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
+    const uint64_t factor = both(strong ? a.scale : a.scale * expf(a_h * (float)(t - 63)));
+    const bool bad = *reinterpret_cast<const uint64_t*>(hd.bad[i & 1]) != 0;
+    bf16* out = (bf16*)a.o + ((size_t)(run.t0 + c * kC + t) * a.H + h) * DV;
+    const bool mine = t < rows(c) && !dead(hd);
+    tmem_each32(at, DV, [&](int x, uint32_t (&o)[32]) {
+      if (bad) {
+#pragma unroll 1
+        for (int j = 0; j < 32; ++j) {
+          const bool hit = t >= hd.first_bad[i & 1][0][x + j] || t >= hd.first_bad[i & 1][1][x + j];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e == j && hit) o[e] = 0x7fffffff;
         }
       }
-      const uint32_t at = tb + ((uint32_t)(32 * (d / 32)) << 16) + kColV + (quarters & 1) * kVStage;
-      tmem_st16(at, r[0]);
-      tmem_st16(at + 16, r[1]);
-      tmem_st16(at + 32, r[2]);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) o[j / 2] = round2(mul2(pair(o[j], o[j + 1]), factor));
+      if (mine) {
+        if (wide) {                              // whole sectors
+          st_global_32(out + x, o);
+          st_global_32(out + x + 16, o + 8);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) *reinterpret_cast<uint4*>(out + x + 2 * j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        }
+      }
+    });
+    before_sync();
+  }
+
+  // ---- warps 4-11: V' and the state ------------------------------------------------------------------------------------------------
+  // Quarter `quarter` of a chunk's V', its n-th in all: 32 tokens as three terms into tensor memory, 32 rows d per warp.
+  // Even quarters are the first set's and go to stage 0, odd ones the second's and stage 1.  The tile's rows are tokens:
+  // ldmatrix turns 8 x 8 blocks of it as tcgen05.st takes them.  nan collects whether anything was not finite.
+  template <bool scaled>
+  __device__ __forceinline__ void make_quarter(const uint8_t* vt, const float* w, float f, int quarter, int n,
+                                               __nv_bfloat162& nan) const {
+    const int lane = threadIdx.x % 32, row = threadIdx.x % 128 & ~31;
+    uint64_t w2[4];                                // the weights of tokens 8 b + 2 (lane % 4) + {0, 1}
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      w2[b] = *reinterpret_cast<const uint64_t*>(w + 32 * quarter + 8 * b + 2 * (lane % 4));
+      if (scaled) w2[b] = mul2(w2[b], both(f));
+    }
+    if (n >= 2) wt_set(&hd.v_free[n & 1], (n >> 1) - 1);
+    if (row < DV) {
+      const uint32_t at = tb + ((uint32_t)row << 16) + kColV + (n & 1) * kVStage;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {       // 16 rows
+        uint32_t r[3][8], v[2][4];                 // (token group b, rows 0-7), (b, 8-15), (b + 1, 0-7), (b + 1, 8-15)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          ldmatrix_x4_trans(v[b], smem_u32(vt) + sw128(kC, 32 * quarter + 8 * (2 * b + lane / 16) + lane % 8,
+                                                       row + 16 * half + 8 * (lane / 8 % 2)));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t u = v[e / 4][e % 4];
+          nan = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), __nv_bfloat162(0.f, 0.f), nan);
+          uint64_t x = mul2(pair(u << 16, u & 0xffff0000u), w2[e / 2]);
+          r[0][e] = take_term(x);
+          r[1][e] = take_term(x);
+          r[2][e] = round2(x);
+        }
+#pragma unroll
+        for (int term = 0; term < 3; ++term) tmem_st_16x128b_x4(at + ((uint32_t)(16 * half) << 16) + 16 * term, r[term]);
+      }
       tmem_wait_st();
     }
     before_sync();
-    ++quarters;
   }
-  __device__ __forceinline__ void quarter_done(int quarters) const { mbar_arrive(&hd.v_ready[(quarters - 1) & 1]); }
 
   // rows from n on of the chunk's K and V tiles belong to the next sequence (or to nobody): zeros
   __device__ __forceinline__ void clear_tail(int n_rows, uint8_t* kt, uint8_t* vt) const {
     constexpr int parts = (DK + DV) / 8;
-    for (int e = threadIdx.x - 128; e < (kC - n_rows) * parts; e += 128) {
+    for (int e = threadIdx.x - kStateThread; e < (kC - n_rows) * parts; e += kStateThreads) {
       const int r = n_rows + e / parts, x = e % parts * 8;
       uint8_t* at = x < DK ? kt + sw128(kC, r, x) : vt + sw128(kC, r, x - DK);
       *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
     }
     fence_async_smem();
-    named_sync(kBarState, 128);
+    named_sync(kBarState, kStateThreads);
   }
-
-  // the state before a chunk: its operand terms to shared memory, and lambda^n of it back for the accumulation
-  __device__ __forceinline__ void hand_state(float step_hi, float step_lo) const {
-    const int d = threadIdx.x - 128;
-    if (d < DV) {
-      const uint32_t at = tb + ((uint32_t)(32 * (d / 32)) << 16) + kColH;
+  // Where a value column holds something that is not finite, a masked product with it would spoil the outputs of
+  // earlier tokens (0 times infinity).  Such values are taken out of the tile (the state has them), and
+  // the outputs of their column from their token on are set when they are stored.
+  // `first` carries over the set's two quarters of the chunk.
+  __device__ __forceinline__ void settle(uint8_t* vt, int i, int quarter, __nv_bfloat162 nan, int& first) const {
+    const int lane = threadIdx.x % 32, d = threadIdx.x % 128;
+    if (quarter < 2) first = kC;
+    if (__any_sync(kFull, !(__low2float(nan) == 0.f && __high2float(nan) == 0.f)) && d < DV) {
 #pragma unroll 1
-      for (int x = 0; x < DK; x += 32) {
-        float s[32];
-        uint32_t r[32];
-        tmem_ld32(at + x, s);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(fmaf(step_hi, s[j], step_lo * s[j]));
-        tmem_st32(at + x, r);
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint4 hi, lo;
-          hi.x = take_term(s[j], s[j + 1]);
-          hi.y = take_term(s[j + 2], s[j + 3]);
-          hi.z = take_term(s[j + 4], s[j + 5]);
-          hi.w = take_term(s[j + 6], s[j + 7]);
-          lo.x = last_term(s[j], s[j + 1]);
-          lo.y = last_term(s[j + 2], s[j + 3]);
-          lo.z = last_term(s[j + 4], s[j + 5]);
-          lo.w = last_term(s[j + 6], s[j + 7]);
-          *reinterpret_cast<uint4*>(hop + sw128(DV, d, x + j)) = hi;
-          *reinterpret_cast<uint4*>(hop + Sh::hterm + sw128(DV, d, x + j)) = lo;
+      for (int s = 32 * quarter + 31; s >= 32 * quarter; --s) {
+        bf16* at = reinterpret_cast<bf16*>(vt + sw128(kC, s, d));
+        if (!isfinite(__bfloat162float(*at))) {
+          first = first < s ? first : s;
+          *at = __float2bfloat16_rn(0.f);
         }
       }
+      fence_async_smem();
+    }
+    if (quarter >= 2) {
+      hd.first_bad[i & 1][set()][d] = (uint8_t)first;
+      const bool any = __any_sync(kFull, first < kC);
+      if (lane == 0) hd.bad[i & 1][(threadIdx.x - kStateThread) / 32] = any;
+    }
+  }
+
+  // The state before a chunk, a thread per half row: its operand terms to shared memory, and lambda^n of it back for the
+  // accumulation.
+  __device__ __forceinline__ void hand_state(float step_hi, float step_lo, uint64_t* free_bar, uint32_t free_parity) const {
+    const int d = threadIdx.x % 128, x0 = set() * (DK / 2);
+    const uint32_t at = tb + ((uint32_t)(d & ~31) << 16) + kColH + x0;
+    const uint64_t by_hi = both(step_hi), by_lo = both(step_lo), by_mid = both(strong ? 1.f : hd.mid);
+    if (free_bar != nullptr) wt_set(free_bar, free_parity);   // the operand may be written again
+    if (d < DV) {
+      tmem_each32(at, DK / 2, [&](int x, uint32_t (&s)[32]) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t &y = s[j + 2 * e], &z = s[j + 2 * e + 1];
+            const uint64_t v = pair(y, z);
+            uint64_t p = mul2(v, by_mid);
+            hi[e] = take_term(p);
+            lo[e] = round2(p);
+            unpair(fma2(by_hi, v, mul2(by_lo, v)), y, z);
+          }
+          *reinterpret_cast<uint4*>(hop + sw128(DV, d, x0 + x + j)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(hop + Sh::hterm + sw128(DV, d, x0 + x + j)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        tmem_st32(at + x, s);
+      });
       tmem_wait_st();
     }
     fence_async_smem();
     before_sync();
   }
 
-  // first pass: the run's own end state, from nothing
-  __device__ __forceinline__ void states_only(int& quarters, float a_h) const {
-    float nan = 0.f;
+  // first pass: weights up to the run's end
+  __device__ __forceinline__ void run_values(float a_h) const {
+    __nv_bfloat162 nan(0.f, 0.f);
     for (int c = run.c0; c < run.c1; ++c) {
       const int m = c - run.c0;
-      wt(&hd.v_full[m & 1], m / 2);
+      wt_set(&hd.v_full[m & 1], m / 2);
       const float f = c + 1 < run.c1 ? expf(a_h * (float)((run.c1 - 1 - c) * kC)) : 1.f;
-      for (int quarter = 0; quarter < 4; ++quarter) {
-        make_quarter(vbuf(m), hd.w[0], f, quarter, quarters, nan);
-        quarter_done(quarters);
+#pragma unroll 1
+      for (int quarter = set(); quarter < 4; quarter += 2) {
+        make_quarter<true>(vbuf(m), hd.w[0], f, quarter, 4 * m + quarter, nan);
+        mbar_arrive(&hd.v_ready[set()]);
       }
     }
-    wt(&hd.kv_done, 0);
-    after_sync();
+    wt_set(&hd.kv_done, 0);
   }
-
-  __device__ __forceinline__ void states(int m0, int quarters, uint32_t kv_phase, bool fresh) const {
-    const int d = threadIdx.x - 128, warp = d / 32;
-    float nan = 0.f;
-    const int c_end = (run.len + kC - 1) / kC;    // of the sequence
-    auto prepare = [&](int c, int m) {             // chunk c's tiles have arrived
-      wt(&hd.v_full[m & 1], m / 2);
-      if (rows(c) < kC) {
-        wt(&hd.k_full[m & 1], m / 2);
-        clear_tail(rows(c), kbuf(m), vbuf(m));
-      }
-      nan = 0.f;
-    };
-    auto weights = [&](int c) -> const float* { return hd.w[c + 1 == c_end ? 1 : 0]; };
-    for (int c = run.c0; c < run.c1; ++c) {
-      const int i = c - run.c0, m = m0 + i;
-      uint8_t* vt = vbuf(m);
-      if (i == 0) {
-        if (!fresh) hand_state(c + 1 == c_end ? hd.last_hi : hd.step_hi, c + 1 == c_end ? hd.last_lo : hd.step_lo);
-        mbar_arrive(&hd.h_ready);
-        prepare(c, m);
-      }
-      for (int quarter = i == 0 ? 0 : 2; quarter < 4; ++quarter) {
-        make_quarter(vt, weights(c), 1.f, quarter, quarters, nan);
-        if (quarter == 3) settle(vt, i, warp, d, nan);
-        quarter_done(quarters);
-      }
-      if (c + 1 < run.c1) {                        // the next chunk's first half, while the tensor core works
-        prepare(c + 1, m + 1);
-        for (int quarter = 0; quarter < 2; ++quarter) {
-          make_quarter(vbuf(m + 1), weights(c + 1), 1.f, quarter, quarters, nan);
-          quarter_done(quarters);
-        }
-      }
-      wt(&hd.kv_done, kv_phase + i);
-      after_sync();
-      if (c + 1 < run.c1) {
-        const bool last = c + 2 == c_end;
-        hand_state(last ? hd.last_hi : hd.step_hi, last ? hd.last_lo : hd.step_lo);
+  __device__ __forceinline__ void states(int m0, uint32_t kv_phase, bool fresh) const {
+    const int c_end = (run.len + kC - 1) / kC;     // of the sequence
+    const int all = 2 * (run.c1 - run.c0);
+    int first = kC;
+    // Each set's quarters one after the other; the state is handed on before the first, and then halfway through each chunk's:
+    // as much of V' as there is room for is made before the state is there.
+#pragma unroll 1
+    for (int n = 0; n < all; ++n) {
+      const int i = n >> 1, quarter = 2 * (n & 1) + set(), c = run.c0 + i, m = m0 + i;
+      const bool last = c + 1 == c_end;
+      if (n == 0 || (i > 0 && quarter >= 2)) {
+        if (i > 0) wt_set(&hd.kv_done, kv_phase + i - 1);
+        if (i > 0 || !fresh)
+          hand_state(last ? hd.last_hi : hd.step_hi, last ? hd.last_lo : hd.step_lo, i > 0 ? &hd.qh_done : nullptr, i - 1);
         mbar_arrive(&hd.h_ready);
       }
-    }
-  }
-  // Where a value column holds something that is not finite, a masked product with it would spoil the outputs of
-  // earlier tokens (0 times infinity).  Such values are taken out of the tile (the state has them), and
-  // the outputs of their column from their token on are set when they are stored.
-  __device__ __forceinline__ void settle(uint8_t* vt, int i, int warp, int d, float nan) const {
-    const bool any = __any_sync(kFull, !(nan == 0.f));
-    if (d < DV) {
-      int first = kC;
-      if (any) {
-        for (int s = kC - 1; s >= 0; --s) {
-          bf16* at = reinterpret_cast<bf16*>(vt + sw128(kC, s, d));
-          if (!isfinite(__bfloat162float(*at))) {
-            first = s;
-            *at = __float2bfloat16_rn(0.f);
-          }
+      if (quarter < 2) {
+        wt_set(&hd.v_full[m & 1], m / 2);
+        if (rows(c) < kC) {
+          wt_set(&hd.k_full[m & 1], m / 2);
+          clear_tail(rows(c), kbuf(m), vbuf(m));
         }
-        fence_async_smem();
       }
-      hd.first_bad[i & 1][d] = (uint8_t)first;
+      __nv_bfloat162 nan(0.f, 0.f);
+      make_quarter<false>(vbuf(m), hd.w[last ? 1 : 0], 1.f, quarter, 4 * m + quarter, nan);
+      settle(vbuf(m), i, quarter, nan, first);
+      mbar_arrive(&hd.v_ready[set()]);
     }
-    if (d % 32 == 0) hd.bad[i & 1][warp] = any;
+    wt_set(&hd.kv_done, kv_phase + run.c1 - run.c0 - 1);
   }
 
   // ---- the fp32 state between tensor memory and elsewhere, a thread per row ----------------------------------------
@@ -574,10 +702,10 @@ struct Cta {
     return (uint32_t)d * (DK * 4) + (uint32_t)(((x / 4) ^ (d & 7)) * 16);
   }
   __device__ __forceinline__ void state_in(const float* src, bool shared) const {
-    const int d = threadIdx.x - 128;
+    const int d = threadIdx.x % 128, x0 = set() * (DK / 2);
     if (d < DV) {
 #pragma unroll 1
-      for (int x = 0; x < DK; x += 32) {
+      for (int x = x0; x < x0 + DK / 2; x += 32) {
         uint32_t r[32];
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
@@ -588,26 +716,23 @@ struct Cta {
           r[j + 2] = __float_as_uint(v.z);
           r[j + 3] = __float_as_uint(v.w);
         }
-        tmem_st32(tb + ((uint32_t)(32 * (d / 32)) << 16) + kColH + x, r);
+        tmem_st32(tb + ((uint32_t)(d & ~31) << 16) + kColH + x, r);
       }
       tmem_wait_st();
     }
-    named_sync(kBarState, 128);   // hop may be overwritten
+    named_sync(kBarState, kStateThreads);   // hop may be overwritten
   }
   __device__ __forceinline__ void state_out(float* dst, bool shared) const {
-    const int d = threadIdx.x - 128;
+    const int d = threadIdx.x % 128, x0 = set() * (DK / 2);
     if (d >= DV) return;
-#pragma unroll 1
-    for (int x = 0; x < DK; x += 32) {
-      float s[32];
-      tmem_ld32(tb + ((uint32_t)(32 * (d / 32)) << 16) + kColH + x, s);
+    tmem_each32(tb + ((uint32_t)(d & ~31) << 16) + kColH + x0, DK / 2, [&](int x, uint32_t (&s)[32]) {
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
-        const float4 v = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
-        if (shared) *reinterpret_cast<float4*>(hop + cell(d, x + j)) = v;
-        else *reinterpret_cast<float4*>(dst + (size_t)d * DK + x + j) = v;
+        const uint4 v = make_uint4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+        if (shared) *reinterpret_cast<uint4*>(hop + cell(d, x0 + x + j)) = v;
+        else *reinterpret_cast<uint4*>(dst + (size_t)d * DK + x0 + x + j) = v;
       }
-    }
+    });
   }
 
   // Start states from the runs' own end states, in place: this CTA turns DV / split rows of every run's.
@@ -637,7 +762,7 @@ struct Cta {
   }
 };
 
-extern __shared__ uint8_t linattn_smem[];
+extern __shared__ __align__(1024) uint8_t linattn_smem[];   // whole 1024-byte swizzle groups
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kBlock, 1)
@@ -647,7 +772,7 @@ __global__ void __launch_bounds__(kBlock, 1)
   const int i = unit / a.H, h = unit % a.H;
   LinAttnSeq seq;
   if (!linattn_seq(a, i, h, &seq)) return;   // the same for every CTA of the cluster
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0), lane = tid % 32;
   if (seq.len == 0) {
     if (rank == 0)
       for (int e = tid; e < DV * DK; e += kBlock) seq.out[e] = seq.in != nullptr ? seq.in[e] : 0.f;
@@ -663,17 +788,22 @@ __global__ void __launch_bounds__(kBlock, 1)
   run.c0 = min(rank * run.per, chunks);
   run.c1 = min(run.c0 + run.per, chunks);
 
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(linattn_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t* base = linattn_smem;
   uint8_t* hop = base + 3 * Sh::ktile + 2 * Sh::vtile;
   Hdr& hd = *reinterpret_cast<Hdr*>(hop + 2 * Sh::hterm);
+  if ((smem_u32(base) & 1023u) != 0) {   // the tiles' swizzle counts on it
+    if (tid == 0) report(a.status, ERS_ECUDA);
+    return;
+  }
   if (warp == kMmaWarp) tmem_alloc(&hd.tmem, kTmemCols);
   if (tid == 0) {
     uint64_t* by_one[] = {&hd.k_full[0], &hd.k_full[1], &hd.k_empty[0], &hd.k_empty[1], &hd.v_full[0], &hd.v_full[1],
-                          &hd.v_empty[0], &hd.v_empty[1], &hd.q_full, &hd.q_empty,
-                          &hd.s_ready, &hd.o2_ready, &hd.o_ready, &hd.kv_done, &hd.v_free[0], &hd.v_free[1]};
+                          &hd.v_empty[0], &hd.v_empty[1], &hd.q_full, &hd.q_empty, &hd.s_ready, &hd.qh_done, &hd.o_ready,
+                          &hd.kv_done, &hd.v_free[0], &hd.v_free[1]};
     for (uint64_t* b : by_one) mbar_init(b, 1);
-    uint64_t* by_group[] = {&hd.pv_go, &hd.o_free, &hd.o_staged, &hd.h_ready, &hd.v_ready[0], &hd.v_ready[1]};
-    for (uint64_t* b : by_group) mbar_init(b, 128);
+    uint64_t* by_four[] = {&hd.p_ready, &hd.o_scaled, &hd.o_free, &hd.v_ready[0], &hd.v_ready[1]};
+    for (uint64_t* b : by_four) mbar_init(b, 128);
+    mbar_init(&hd.h_ready, 256);
     fence_mbar_init();
     hd.dead = 0;
   }
@@ -681,21 +811,25 @@ __global__ void __launch_bounds__(kBlock, 1)
   if (tid >= 128 && tid < 128 + kC) {
     const int j = tid - 128;
     // lambda^0 = 1 whatever lambda
-    hd.power[j] = j == 0 ? 1.f : expf(a_h * (float)j);
-    if (j == 0) hd.power[kC] = expf(a_h * (float)kC);
+    const bool strong = a_h < kStrong;
+    hd.power[j] = strong ? (j == 0 ? 1.f : expf(a_h * (float)j)) : expf(a_h * (float)(63 - j));
+    if (j == 0) {
+      hd.power[kC] = expf(a_h * (float)kC);   // of the strong ones
+      hd.mid = expf(a_h * 64.f);
+    }
     hd.w[0][j] = j == kC - 1 ? 1.f : expf(a_h * (float)(kC - 1 - j));
     hd.w[1][j] = j >= n_last ? 0.f : j == n_last - 1 ? 1.f : expf(a_h * (float)(n_last - 1 - j));
-  } else if (tid == 288 || tid == 256) {           // multiplied once a chunk over the whole sequence: as two floats
-    const int n = tid == 288 ? kC : n_last;
+  } else if (tid == 32 * kLoadWarp || tid == 32 * kMmaWarp) {           // multiplied once a chunk over the whole sequence: as two floats
+    const int n = tid == 32 * kLoadWarp ? kC : n_last;
     const double e = exp((double)a_h * n);
     const float hi = (float)e, lo = (float)(e - (double)hi);
-    (tid == 288 ? hd.step_hi : hd.last_hi) = hi;
-    (tid == 288 ? hd.step_lo : hd.last_lo) = lo;
+    (tid == 32 * kLoadWarp ? hd.step_hi : hd.last_hi) = hi;
+    (tid == 32 * kLoadWarp ? hd.step_lo : hd.last_lo) = lo;
   }
   before_sync();
   __syncthreads();
   after_sync();
-  Cta<DK, DV> cta{a, maps, hd, base, hop, hd.tmem, h, h / (a.H / a.G), run};
+  Cta<DK, DV> cta{a, maps, hd, base, hop, __shfl_sync(kFull, hd.tmem, 0), h, h / (a.H / a.G), a_h, a_h < kStrong, run};
 
   // ---- first pass -----------------------------------------------------------------------------------------
   const bool first = run.last_run > 0 && rank < run.last_run;
@@ -707,9 +841,9 @@ __global__ void __launch_bounds__(kBlock, 1)
     if (warp == kLoadWarp) {
       if (lane == 0) cta.load_states();
     } else if (warp == kMmaWarp) {
-      if (lane == 0) cta.issue_states(quarters);
-    } else if (warp >= 4) {
-      cta.states_only(quarters, a_h);
+      cta.issue_states(quarters);
+    } else if (tid >= kStateThread) {
+      cta.run_values(a_h);
       cta.state_out(nullptr, true);
     }
     quarters = 4 * (run.c1 - run.c0);
@@ -729,13 +863,13 @@ __global__ void __launch_bounds__(kBlock, 1)
     if (warp == kLoadWarp) {
       if (lane == 0) cta.load_chunks(m0);
     } else if (warp == kMmaWarp) {
-      if (lane == 0) cta.issue_chunks(m0, quarters, !given);
-    } else if (warp >= 4) {
+      cta.issue_chunks(m0, quarters, !given);
+    } else if (tid >= kStateThread) {
       if (given) cta.state_in(seq.in, run.last_run > 0);
-      cta.states(m0, quarters, kv_phase, !given);
+      cta.states(m0, kv_phase, !given);
       if (rank == run.last_run && !dead(hd)) cta.state_out(seq.out, false);
     } else {
-      cta.outputs(m0, !given);
+      cta.rows_of_chunks(!given);
     }
   }
   __syncwarp();
@@ -802,7 +936,7 @@ bool linattn_tc_supported(const LinAttnArgs& a) {
 cudaError_t linattn_tc(const LinAttnArgs& a, cudaStream_t s) {
   Maps maps;
   if (!encode(&maps.q, a.q, a.ntokens, a.G, a.dk) || !encode(&maps.k, a.k, a.ntokens, a.G, a.dk) ||
-      !encode(&maps.v, a.v, a.ntokens, a.H, a.dv) || !encode(&maps.o, a.o, a.ntokens, a.H, a.dv))
+      !encode(&maps.v, a.v, a.ntokens, a.H, a.dv))
     return cudaErrorInvalidValue;
   // Runs of a sequence: as many as fill the SMs, of two chunks at least.
   const int chunks = (int)((a.max_len + kC - 1) / kC);
