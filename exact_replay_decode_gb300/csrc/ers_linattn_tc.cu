@@ -19,7 +19,7 @@
 // and some 2500 issue slots of operand making per scheduler, in one dependent loop through the state.  So the warps are
 // specialised and run side by side, and the MMAs are ordered S, H, O so that each group's work on one product lies under the
 // others: while H accumulates the scores become P and the last chunk's outputs are stored; while O accumulates the state is
-// handed on.  Four warps make P and own the outputs, eight make V' and hand the state on, one loads the tiles (TMA; two
+// handed on.  Four warps make P, four own the outputs, eight make V' and hand the state on, one loads the tiles (TMA; two
 // buffers for K and V, one for Q) and one issues every MMA.
 //
 // A long sequence of few heads is split over the CTAs of a cluster, each a run of chunks: every CTA but the
@@ -41,21 +41,24 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 128;                  // tokens of a chunk
-// warps 0-3 make P and own the outputs, 4-7 and 8-11 (two sets) the state; lane quarter: warp % 4.  14 warps: 128 registers
-// each, for with spills every reload would go to L2 (the first-level cache is all shared memory).
-constexpr int kStateThread = 128, kStateThreads = 256;
-constexpr int kLoadWarp = 12, kMmaWarp = 13;
-constexpr int kBlock = 448;
+// Five warpgroups: warps 0-3 make P, 4-7 own the outputs, 8-11 and 12-15 (two sets) the state, 16 loads and 17 issues (18 and 19
+// fill the group up); lane quarter: warp % 4.  They share out the registers of the launch, 96 a thread: reloads of spilled
+// ones would go to L2, for the first-level cache is all shared memory.
+constexpr int kOutThread = 128, kStateThread = 256, kStateThreads = 256, kControlThread = 512;
+constexpr int kLoadWarp = 16, kMmaWarp = 17;
+constexpr int kBlock = 640;
+constexpr int kLaunchRegs = 96, kScoreRegs = 104, kOutRegs = 64, kStateRegs = 128, kControlRegs = 40;
+static_assert(kScoreRegs + kOutRegs + 2 * kStateRegs + kControlRegs <= 5 * kLaunchRegs, "what the launch brings");
 constexpr float kStrong = -1.f;
 constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384, kVStage = 48, kTmemCols = 512;
-constexpr uint32_t kBarState = 1, kBarRows = 2, kBarSet = 3;   // named barriers of the warps of a kind
+constexpr uint32_t kBarState = 1, kBarScores = 2, kBarOut = 3, kBarSet = 4;   // named barriers of the warps of a kind
 
 struct Hdr {
   alignas(16) float w[2][kC];        // lambda^(n-1-j), 0 from n on: a full chunk, the last chunk (read 16 bytes at a time)
   alignas(16) float power[kC + 4];   // lambda^(63-j) of the columns j; kStrong: lambda^j
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, q_empty;   // tile buffers
   uint64_t s_ready, qh_done, o_ready, kv_done, v_free[2];               // completed by the tensor core
-  uint64_t p_ready, o_scaled, o_free, h_ready, v_ready[2];    // by the warps
+  uint64_t p_ready, o_scaled, o_free, o_staged, h_scaled, h_ready, v_ready[2];    // by the warps
   uint32_t tmem;
   int dead;                          // a wait gave up: no further wait waits, no copy or MMA is issued
   float step_hi, step_lo;            // lambda^128 as two floats,
@@ -66,14 +69,15 @@ struct Hdr {
 };
 
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
 };
 
 template <int DK, int DV>
 struct Shape {
   static constexpr uint32_t ktile = kC * DK * 2, vtile = kC * DV * 2;
   static constexpr uint32_t hterm = DV * DK * 2;       // one bf16 term of the state operand
-  static constexpr uint32_t smem = sizeof(Hdr) + 3 * ktile + 2 * vtile + 2 * hterm;
+  static constexpr uint32_t stage = vtile > ktile ? vtile : 0;   // outputs on their way out: in a K tile where they fit
+  static constexpr uint32_t smem = sizeof(Hdr) + 3 * ktile + 2 * vtile + 2 * hterm + stage;
   static_assert(smem <= 227 * 1024, "one CTA's shared memory");
 };
 
@@ -98,6 +102,11 @@ __device__ __forceinline__ void wait(Hdr& hd, uint64_t* bar, uint32_t parity, in
 }
 __device__ __forceinline__ bool dead(const Hdr& hd) { return *(const volatile int*)&hd.dead != 0; }
 
+// a warpgroup's share of the registers
+template <int n>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
+template <int n>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n)); }
 // one lane of a converged warp
 __device__ __forceinline__ bool elected() {
   uint32_t r;
@@ -172,11 +181,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t at)
                : "r"(at)
                : "memory");
 }
-__device__ __forceinline__ void st_global_32(void* to, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void tma_store_3d(const void* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(smem_u32(src))
                : "memory");
 }
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -231,6 +242,20 @@ __device__ __forceinline__ uint32_t take_term(uint64_t& v) {
   return u;
 }
 
+// Row t of 32 output columns, from the tokens first[] (of either set) on not finite.
+__device__ __noinline__ void spoil_mask(uint32_t* hit, const uint8_t* first0, const uint8_t* first1, int t) {
+  uint32_t m = 0;
+  for (int j = 0; j < 32; ++j) m |= (uint32_t)(t >= first0[j] || t >= first1[j]) << j;
+  *hit = m;
+}
+__device__ __forceinline__ void spoil(uint32_t (&o)[32], const uint8_t* first0, const uint8_t* first1, int t) {
+  uint32_t m;
+  spoil_mask(&m, first0, first1, t);
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (m >> j & 1u) o[j] = 0x7fffffff;
+}
+
 // A CTA's share of the work.
 struct Run {
   int t0, len;         // the sequence's tokens
@@ -257,20 +282,19 @@ struct Cta {
   __device__ __forceinline__ uint8_t* kbuf(int m) const { return tiles + (m & 1) * Sh::ktile; }
   __device__ __forceinline__ uint8_t* vbuf(int m) const { return tiles + 2 * Sh::ktile + (m & 1) * Sh::vtile; }
   __device__ __forceinline__ uint8_t* qbuf() const { return tiles + 2 * Sh::ktile + 2 * Sh::vtile; }
+  __device__ __forceinline__ uint8_t* obuf(int m) const {
+    return Sh::stage > 0 ? tiles + 3 * Sh::ktile + 2 * Sh::vtile : kbuf(m);
+  }
   __device__ __forceinline__ int rows(int c) const { return run.len - c * kC < kC ? run.len - c * kC : kC; }
   __device__ __forceinline__ void wt(uint64_t* bar, uint32_t parity) const { wait(hd, bar, parity & 1u, a.status); }
   // one warp of a kind polls, the others wait for it
-  __device__ __forceinline__ void wt_rows(uint64_t* bar, uint32_t parity) const {
-    if (threadIdx.x < 32) wt(bar, parity);
-    named_sync(kBarRows, kStateThread);
+  __device__ __forceinline__ void wt_group(int id, uint64_t* bar, uint32_t parity) const {
+    if (threadIdx.x % 128 < 32) wt(bar, parity);
+    named_sync(id, 128);
     after_sync();
   }
   __device__ __forceinline__ int set() const { return (threadIdx.x - kStateThread) / 128; }
-  __device__ __forceinline__ void wt_set(uint64_t* bar, uint32_t parity) const {
-    if (threadIdx.x % 128 < 32) wt(bar, parity);
-    named_sync(kBarSet + set(), 128);
-    after_sync();
-  }
+  __device__ __forceinline__ void wt_set(uint64_t* bar, uint32_t parity) const { wt_group(kBarSet + set(), bar, parity); }
 
   // ---- the loading warp ------------------------------------------------------------------------
   __device__ __forceinline__ void load(uint8_t* to, const CUtensorMap* map, int d, int head, int c, uint64_t* bar) const {
@@ -292,7 +316,9 @@ struct Cta {
       load_v(c - run.c0, c);
     }
   }
-  // In the order in which buffers come free: K after V'^T K, Q after Q H^T, V after P V.
+  // In the order in which buffers come free: Q after Q H^T, V after P V, and K, long done with then, when the output that
+  // takes its place has been stored: it is the tile that is needed last.  (The rows of a short chunk are stored by their
+  // owners.)
   __device__ __forceinline__ void load_chunks(int m0) const {
     const int n = run.c1 - run.c0;
     load_k(m0, run.c0);
@@ -303,12 +329,22 @@ struct Cta {
       load_v(m0 + 1, run.c0 + 1);
     }
 #pragma unroll 1
-    for (int i = 0; i + 1 < n; ++i) {
+    for (int i = 0; i < n; ++i) {
       const int c = run.c0 + i;
-      if (i + 2 < n) load_k(m0 + i + 2, c + 2);
-      wt(&hd.q_empty, i);
-      load(qbuf(), &maps.q, DK, g, c + 1, &hd.q_full);
+      if (i + 1 < n) {
+        wt(&hd.q_empty, i);
+        load(qbuf(), &maps.q, DK, g, c + 1, &hd.q_full);
+      }
       if (i + 2 < n) load_v(m0 + i + 2, c + 2);
+      wt(&hd.o_staged, i);
+      if (!dead(hd) && rows(c) == kC) {
+        for (int x = 0; x < DV; x += 64)
+          tma_store_3d(&maps.o, obuf(m0 + i) + x / 64 * (kC * 128), x, h, run.t0 + c * kC);
+        bulk_commit();
+        bulk_wait_read();
+      }
+      mbar_arrive(&hd.k_empty[(m0 + i) & 1]);
+      if (i + 2 < n) load_k(m0 + i + 2, c + 2);
     }
   }
   // After a wait gave up: no copy or MMA may be left in flight when the CTA ends.
@@ -386,14 +422,12 @@ struct Cta {
       if (dead(hd)) return;
       chain(tb + kColS, qd, sdesc(smem_u32(kbuf(m)), 16, 1024), kC, kC, DK / 16, id_s, false, leader);
       if (leader) commit(&hd.s_ready);
-      wt(&hd.h_ready, i);
+      wt(&hd.h_scaled, i);
       after_sync();
       if (!state_chunk(m, quarters, with_h, leader)) return;
-      if (leader) {
-        commit(&hd.kv_done);
-        commit(&hd.k_empty[m & 1]);
-      }
+      if (leader) commit(&hd.kv_done);
       if (i > 0) wt(&hd.o_free, i - 1);
+      wt(&hd.h_ready, i);
       after_sync();
       if (dead(hd)) return;
       if (with_h) {
@@ -428,63 +462,46 @@ struct Cta {
     }
   }
 
-  // ---- warps 0-3: P over S, and the outputs, a thread per row ------------------------------------------------------------------
-  __device__ __forceinline__ void rows_of_chunks(bool fresh) const {
-    for (int c = run.c0; c < run.c1; ++c) {
-      const int i = c - run.c0;
-      wt_rows(&hd.s_ready, i);
-      scores();
+  // ---- warps 0-3: P over S, a thread per row ----------------------------------------------------------------------------------
+  __device__ __forceinline__ void scores_of_chunks() const {
+    uint64_t u[16];                                // lambda^-j
+#pragma unroll
+    for (int j = 0; j < 16; ++j) u[j] = strong ? 0ull : pair(expf(a_h * (float)(-2 * j)), expf(a_h * (float)(-2 * j - 1)));
+    for (int i = 0; i < run.c1 - run.c0; ++i) {
+      wt_group(kBarScores, &hd.s_ready, i);
+      scores(u);
       mbar_arrive(&hd.p_ready);
-      if (strong) {
-        wt_rows(&hd.qh_done, i);
-        if (!(fresh && i == 0)) scale_rows();
-        mbar_arrive(&hd.o_scaled);
-      }
-      wt_rows(&hd.o_ready, i);
-      outputs(c);
-      mbar_arrive(&hd.o_free);
     }
   }
   // Columns [16 b, 16 b + 16) of S become the hi terms of P in the first 8 columns of the block and the lo terms in the others.
-  __device__ __forceinline__ void scores() const {
+  // The weights lambda^(63-j) are products of u and one factor per 32 columns: loads from shared memory, which the tensor
+  // core's operands keep busy, would cost more than the second multiplication.
+  __device__ __forceinline__ void scores(const uint64_t (&u)[16]) const {
     const int t = threadIdx.x, quarter = t / 32;
     const uint32_t at = tb + ((uint32_t)(32 * quarter) << 16) + kColS;
     tmem_each32(at, 32 * (quarter + 1), [&](int x, uint32_t (&s)[32]) {
-      const bool below = x < 32 * quarter;       // the diagonal, in all of the warp's rows
+      // whole blocks of code for each kind: branches inside would cost more than all of this
+      if (strong) {
 #pragma unroll
-      for (int b = 0; b < 32; b += 16) {
-        uint32_t r[16];
-        if (!strong) {
-          const ulonglong2* w = reinterpret_cast<const ulonglong2*>(hd.power + x + b);
+        for (int j = 0; j < 32; ++j) {
+          const int e = t - x - j;
+          s[j] = e >= 0 ? __float_as_uint(__uint_as_float(s[j]) * hd.power[e]) : 0u;
+        }
+        to_terms(s);
+      } else {
+        const uint64_t f = both(hd.power[x]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const ulonglong2 w4 = w[j];
-            uint64_t p = mul2(pair(s[b + 4 * j], s[b + 4 * j + 1]), w4.x), q = mul2(pair(s[b + 4 * j + 2], s[b + 4 * j + 3]), w4.y);
-            if (!below) {                        // selected, not multiplied: a masked score may be anything
-              uint32_t y, z;
-              const int e = t - x - b - 4 * j;
-              unpair(p, y, z);
-              p = pair(e >= 0 ? y : 0u, e >= 1 ? z : 0u);
-              unpair(q, y, z);
-              q = pair(e >= 2 ? y : 0u, e >= 3 ? z : 0u);
-            }
-            r[2 * j] = take_term(p);
-            r[8 + 2 * j] = round2(p);
-            r[2 * j + 1] = take_term(q);
-            r[9 + 2 * j] = round2(q);
-          }
-        } else {
+        for (int j = 0; j < 16; ++j) unpair(mul2(mul2(pair(s[2 * j], s[2 * j + 1]), f), u[j]), s[2 * j], s[2 * j + 1]);
+        to_terms(s);
+        if (x == 32 * quarter) {                   // the diagonal: a mask, for a masked score may be anything
+          const int lane = t % 32;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int e = t - x - b - 2 * j;
-            uint64_t p = pair(e >= 0 ? __uint_as_float(s[b + 2 * j]) * hd.power[e] : 0.f,
-                              e >= 1 ? __uint_as_float(s[b + 2 * j + 1]) * hd.power[e - 1] : 0.f);
-            r[j] = take_term(p);
-            r[8 + j] = round2(p);
+          for (int j = 0; j < 16; ++j) {
+            const uint32_t keep = lane > 2 * j ? 0xffffffffu : lane == 2 * j ? 0xffffu : 0u;
+            s[16 * (j / 8) + j % 8] &= keep;
+            s[16 * (j / 8) + 8 + j % 8] &= keep;
           }
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s[b + j] = r[j];
       }
       tmem_st32(at + x, s);
     });
@@ -496,9 +513,41 @@ struct Cta {
     tmem_wait_st();
     before_sync();
   }
+  // 32 scores in place to the terms of P's two blocks of 16
+  static __device__ __forceinline__ void to_terms(uint32_t (&s)[32]) {
+#pragma unroll
+    for (int b = 0; b < 32; b += 16) {
+      uint32_t r[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint64_t p = pair(s[b + 2 * j], s[b + 2 * j + 1]);
+        r[j] = take_term(p);
+        r[8 + j] = round2(p);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[b + j] = r[j];
+    }
+  }
+
+  // ---- warps 4-7: outputs, a thread per row -------------------------------------------------------------------------------------
+  __device__ __forceinline__ void outputs_of_chunks(int m0, bool fresh) const {
+    for (int c = run.c0; c < run.c1; ++c) {
+      const int i = c - run.c0;
+      if (strong) {
+        wt_group(kBarOut, &hd.qh_done, i);
+        if (!(fresh && i == 0)) scale_rows();
+        mbar_arrive(&hd.o_scaled);
+      }
+      wt_group(kBarOut, &hd.o_ready, i);
+      outputs(c, obuf(m0 + i));
+      mbar_arrive(&hd.o_free);
+      if (i > 0) wt_group(kBarOut, &hd.k_empty[(m0 + i - 1) & 1], (m0 + i - 1) / 2);   // the loader has taken the last one
+      mbar_arrive(&hd.o_staged);
+    }
+  }
   // kStrong: the state's part of the outputs, times lambda^(i+1)
   __device__ __forceinline__ void scale_rows() const {
-    const int t = threadIdx.x;
+    const int t = threadIdx.x - kOutThread;
     const uint32_t at = tb + ((uint32_t)(t & ~31) << 16) + kColO;
     const uint64_t carry = both(hd.power[t + 1]);
     tmem_each32(at, DV, [&](int x, uint32_t (&o)[32]) {
@@ -509,40 +558,28 @@ struct Cta {
     tmem_wait_st();
     before_sync();
   }
-  __device__ __forceinline__ void outputs(int c) const {
-    const int t = threadIdx.x, i = c - run.c0;
+  __device__ __forceinline__ void outputs(int c, uint8_t* stage) const {
+    const int t = threadIdx.x - kOutThread, i = c - run.c0;
     const uint32_t at = tb + ((uint32_t)(t & ~31) << 16) + kColO;
-    const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
     const uint64_t factor = both(strong ? a.scale : a.scale * expf(a_h * (float)(t - 63)));
     const bool bad = *reinterpret_cast<const uint64_t*>(hd.bad[i & 1]) != 0;
+    const int live = rows(c);
     bf16* out = (bf16*)a.o + ((size_t)(run.t0 + c * kC + t) * a.H + h) * DV;
-    const bool mine = t < rows(c) && !dead(hd);
     tmem_each32(at, DV, [&](int x, uint32_t (&o)[32]) {
-      if (bad) {
-#pragma unroll 1
-        for (int j = 0; j < 32; ++j) {
-          const bool hit = t >= hd.first_bad[i & 1][0][x + j] || t >= hd.first_bad[i & 1][1][x + j];
+      if (bad) spoil(o, hd.first_bad[i & 1][0] + x, hd.first_bad[i & 1][1] + x, t);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e == j && hit) o[e] = 0x7fffffff;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) o[j / 2] = round2(mul2(pair(o[j], o[j + 1]), factor));
-      if (mine) {
-        if (wide) {                              // whole sectors
-          st_global_32(out + x, o);
-          st_global_32(out + x + 16, o + 8);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) *reinterpret_cast<uint4*>(out + x + 2 * j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-        }
+      for (int j = 0; j < 32; j += 8) {
+        const uint4 v = make_uint4(round2(mul2(pair(o[j], o[j + 1]), factor)), round2(mul2(pair(o[j + 2], o[j + 3]), factor)),
+                                   round2(mul2(pair(o[j + 4], o[j + 5]), factor)), round2(mul2(pair(o[j + 6], o[j + 7]), factor)));
+        if (live == kC) *reinterpret_cast<uint4*>(stage + sw128(kC, t, x + j)) = v;
+        else if (t < live && !dead(hd)) *reinterpret_cast<uint4*>(out + x + j) = v;
       }
     });
     before_sync();
+    fence_async_smem();
   }
 
-  // ---- warps 4-11: V' and the state ------------------------------------------------------------------------------------------------
+  // ---- warps 8-15: V' and the state ------------------------------------------------------------------------------------------------
   // Quarter `quarter` of a chunk's V', its n-th in all: 32 tokens as three terms into tensor memory, 32 rows d per warp.
   // Even quarters are the first set's and go to stage 0, odd ones the second's and stage 1.  The tile's rows are tokens:
   // ldmatrix turns 8 x 8 blocks of it as tcgen05.st takes them.  nan collects whether anything was not finite.
@@ -556,12 +593,11 @@ struct Cta {
       w2[b] = *reinterpret_cast<const uint64_t*>(w + 32 * quarter + 8 * b + 2 * (lane % 4));
       if (scaled) w2[b] = mul2(w2[b], both(f));
     }
-    if (n >= 2) wt_set(&hd.v_free[n & 1], (n >> 1) - 1);
+    uint32_t r[2][3][8];
     if (row < DV) {
-      const uint32_t at = tb + ((uint32_t)row << 16) + kColV + (n & 1) * kVStage;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {       // 16 rows
-        uint32_t r[3][8], v[2][4];                 // (token group b, rows 0-7), (b, 8-15), (b + 1, 0-7), (b + 1, 8-15)
+        uint32_t v[2][4];                          // (token group b, rows 0-7), (b, 8-15), (b + 1, 0-7), (b + 1, 8-15)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
           ldmatrix_x4_trans(v[b], smem_u32(vt) + sw128(kC, 32 * quarter + 8 * (2 * b + lane / 16) + lane % 8,
@@ -571,13 +607,20 @@ struct Cta {
           const uint32_t u = v[e / 4][e % 4];
           nan = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), __nv_bfloat162(0.f, 0.f), nan);
           uint64_t x = mul2(pair(u << 16, u & 0xffff0000u), w2[e / 2]);
-          r[0][e] = take_term(x);
-          r[1][e] = take_term(x);
-          r[2][e] = round2(x);
+          r[half][0][e] = take_term(x);
+          r[half][1][e] = take_term(x);
+          r[half][2][e] = round2(x);
         }
-#pragma unroll
-        for (int term = 0; term < 3; ++term) tmem_st_16x128b_x4(at + ((uint32_t)(16 * half) << 16) + 16 * term, r[term]);
       }
+    }
+    if (n >= 2) wt_set(&hd.v_free[n & 1], (n >> 1) - 1);   // only now: the terms were made under the stage's last product
+    if (row < DV) {
+      const uint32_t at = tb + ((uint32_t)row << 16) + kColV + (n & 1) * kVStage;
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int term = 0; term < 3; ++term)
+          tmem_st_16x128b_x4(at + ((uint32_t)(16 * half) << 16) + 16 * term, r[half][term]);
       tmem_wait_st();
     }
     before_sync();
@@ -619,36 +662,43 @@ struct Cta {
     }
   }
 
-  // The state before a chunk, a thread per half row: its operand terms to shared memory, and lambda^n of it back for the
-  // accumulation.
-  __device__ __forceinline__ void hand_state(float step_hi, float step_lo, uint64_t* free_bar, uint32_t free_parity) const {
+  // The state before a chunk, a thread per half row: lambda^n of it goes back at once for the next accumulation; its operand
+  // terms go to shared memory when the last chunk's Q H^T (the i-1st) is done with the previous ones.
+  __device__ __forceinline__ void hand_state(float step_hi, float step_lo, int i) const {
     const int d = threadIdx.x % 128, x0 = set() * (DK / 2);
     const uint32_t at = tb + ((uint32_t)(d & ~31) << 16) + kColH + x0;
     const uint64_t by_hi = both(step_hi), by_lo = both(step_lo), by_mid = both(strong ? 1.f : hd.mid);
-    if (free_bar != nullptr) wt_set(free_bar, free_parity);   // the operand may be written again
+    uint32_t hi[DK / 4], lo[DK / 4];
     if (d < DV) {
-      tmem_each32(at, DK / 2, [&](int x, uint32_t (&s)[32]) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint32_t hi[4], lo[4];
+      for (int x = 0; x < DK / 2; x += 32) {
+        uint32_t s[32];
+        tmem_ld32_begin(at + x, s);
+        arrived(s);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t &y = s[j + 2 * e], &z = s[j + 2 * e + 1];
-            const uint64_t v = pair(y, z);
-            uint64_t p = mul2(v, by_mid);
-            hi[e] = take_term(p);
-            lo[e] = round2(p);
-            unpair(fma2(by_hi, v, mul2(by_lo, v)), y, z);
-          }
-          *reinterpret_cast<uint4*>(hop + sw128(DV, d, x0 + x + j)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(hop + Sh::hterm + sw128(DV, d, x0 + x + j)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int j = 0; j < 16; ++j) {
+          const uint64_t v = pair(s[2 * j], s[2 * j + 1]);
+          uint64_t p = mul2(v, by_mid);
+          hi[x / 2 + j] = take_term(p);
+          lo[x / 2 + j] = round2(p);
+          unpair(fma2(by_hi, v, mul2(by_lo, v)), s[2 * j], s[2 * j + 1]);
         }
         tmem_st32(at + x, s);
-      });
+      }
       tmem_wait_st();
     }
-    fence_async_smem();
     before_sync();
+    mbar_arrive(&hd.h_scaled);
+    if (i > 0) wt_set(&hd.qh_done, i - 1);
+    if (d < DV) {
+#pragma unroll
+      for (int j = 0; j < DK / 4; j += 4) {
+        *reinterpret_cast<uint4*>(hop + sw128(DV, d, x0 + 2 * j)) = make_uint4(hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
+        *reinterpret_cast<uint4*>(hop + Sh::hterm + sw128(DV, d, x0 + 2 * j)) = make_uint4(lo[j], lo[j + 1], lo[j + 2], lo[j + 3]);
+      }
+    }
+    fence_async_smem();
+    mbar_arrive(&hd.h_ready);
   }
 
   // first pass: weights up to the run's end
@@ -678,9 +728,12 @@ struct Cta {
       const bool last = c + 1 == c_end;
       if (n == 0 || (i > 0 && quarter >= 2)) {
         if (i > 0) wt_set(&hd.kv_done, kv_phase + i - 1);
-        if (i > 0 || !fresh)
-          hand_state(last ? hd.last_hi : hd.step_hi, last ? hd.last_lo : hd.step_lo, i > 0 ? &hd.qh_done : nullptr, i - 1);
-        mbar_arrive(&hd.h_ready);
+        if (i > 0 || !fresh) {
+          hand_state(last ? hd.last_hi : hd.step_hi, last ? hd.last_lo : hd.step_lo, i);
+        } else {
+          mbar_arrive(&hd.h_scaled);
+          mbar_arrive(&hd.h_ready);
+        }
       }
       if (quarter < 2) {
         wt_set(&hd.v_full[m & 1], m / 2);
@@ -789,7 +842,7 @@ __global__ void __launch_bounds__(kBlock, 1)
   run.c1 = min(run.c0 + run.per, chunks);
 
   uint8_t* base = linattn_smem;
-  uint8_t* hop = base + 3 * Sh::ktile + 2 * Sh::vtile;
+  uint8_t* hop = base + 3 * Sh::ktile + 2 * Sh::vtile + Sh::stage;
   Hdr& hd = *reinterpret_cast<Hdr*>(hop + 2 * Sh::hterm);
   if ((smem_u32(base) & 1023u) != 0) {   // the tiles' swizzle counts on it
     if (tid == 0) report(a.status, ERS_ECUDA);
@@ -801,8 +854,9 @@ __global__ void __launch_bounds__(kBlock, 1)
                           &hd.v_empty[0], &hd.v_empty[1], &hd.q_full, &hd.q_empty, &hd.s_ready, &hd.qh_done, &hd.o_ready,
                           &hd.kv_done, &hd.v_free[0], &hd.v_free[1]};
     for (uint64_t* b : by_one) mbar_init(b, 1);
-    uint64_t* by_four[] = {&hd.p_ready, &hd.o_scaled, &hd.o_free, &hd.v_ready[0], &hd.v_ready[1]};
+    uint64_t* by_four[] = {&hd.p_ready, &hd.o_scaled, &hd.o_free, &hd.o_staged, &hd.v_ready[0], &hd.v_ready[1]};
     for (uint64_t* b : by_four) mbar_init(b, 128);
+    mbar_init(&hd.h_scaled, 256);
     mbar_init(&hd.h_ready, 256);
     fence_mbar_init();
     hd.dead = 0;
@@ -829,6 +883,10 @@ __global__ void __launch_bounds__(kBlock, 1)
   before_sync();
   __syncthreads();
   after_sync();
+  if (tid >= kControlThread) regs_down<kControlRegs>();
+  else if (tid >= kStateThread) regs_up<kStateRegs>();
+  else if (tid >= kOutThread) regs_down<kOutRegs>();
+  else regs_up<kScoreRegs>();
   Cta<DK, DV> cta{a, maps, hd, base, hop, __shfl_sync(kFull, hd.tmem, 0), h, h / (a.H / a.G), a_h, a_h < kStrong, run};
 
   // ---- first pass -----------------------------------------------------------------------------------------
@@ -842,7 +900,7 @@ __global__ void __launch_bounds__(kBlock, 1)
       if (lane == 0) cta.load_states();
     } else if (warp == kMmaWarp) {
       cta.issue_states(quarters);
-    } else if (tid >= kStateThread) {
+    } else if (tid >= kStateThread && tid < kControlThread) {
       cta.run_values(a_h);
       cta.state_out(nullptr, true);
     }
@@ -864,12 +922,15 @@ __global__ void __launch_bounds__(kBlock, 1)
       if (lane == 0) cta.load_chunks(m0);
     } else if (warp == kMmaWarp) {
       cta.issue_chunks(m0, quarters, !given);
+    } else if (tid >= kControlThread) {
     } else if (tid >= kStateThread) {
       if (given) cta.state_in(seq.in, run.last_run > 0);
       cta.states(m0, kv_phase, !given);
       if (rank == run.last_run && !dead(hd)) cta.state_out(seq.out, false);
+    } else if (tid >= kOutThread) {
+      cta.outputs_of_chunks(m0, !given);
     } else {
-      cta.rows_of_chunks(!given);
+      cta.scores_of_chunks();
     }
   }
   __syncwarp();
@@ -936,7 +997,7 @@ bool linattn_tc_supported(const LinAttnArgs& a) {
 cudaError_t linattn_tc(const LinAttnArgs& a, cudaStream_t s) {
   Maps maps;
   if (!encode(&maps.q, a.q, a.ntokens, a.G, a.dk) || !encode(&maps.k, a.k, a.ntokens, a.G, a.dk) ||
-      !encode(&maps.v, a.v, a.ntokens, a.H, a.dv))
+      !encode(&maps.v, a.v, a.ntokens, a.H, a.dv) || !encode(&maps.o, a.o, a.ntokens, a.H, a.dv))
     return cudaErrorInvalidValue;
   // Runs of a sequence: as many as fill the SMs, of two chunks at least.
   const int chunks = (int)((a.max_len + kC - 1) / kC);
