@@ -19,7 +19,8 @@
 // and some 2500 issue slots of operand making per scheduler, in one dependent loop through the state.  So the warps are
 // specialised and run side by side, and the MMAs are ordered S, H, O so that each group's work on one product lies under the
 // others: while H accumulates the scores become P and the last chunk's outputs are stored; while O accumulates the state is
-// handed on.  Four warps make P, four own the outputs, eight make V' and hand the state on, one loads the tiles (TMA; two
+// handed on.  Four warps make P and own the outputs (on warps of their own the outputs made every product slower: more
+// tensor-memory traffic at once), eight make V' and hand the state on, one loads the tiles (TMA; two
 // buffers for K and V, one for Q) and one issues every MMA.
 //
 // A long sequence of few heads is split over the CTAs of a cluster, each a run of chunks: every CTA but the
@@ -41,17 +42,14 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 128;                  // tokens of a chunk
-// Five warpgroups: warps 0-3 make P, 4-7 own the outputs, 8-11 and 12-15 (two sets) the state, 16 loads and 17 issues (18 and 19
-// fill the group up); lane quarter: warp % 4.  They share out the registers of the launch, 96 a thread: reloads of spilled
-// ones would go to L2, for the first-level cache is all shared memory.
-constexpr int kOutThread = 128, kStateThread = 256, kStateThreads = 256, kControlThread = 512;
-constexpr int kLoadWarp = 16, kMmaWarp = 17;
-constexpr int kBlock = 640;
-constexpr int kLaunchRegs = 96, kScoreRegs = 104, kOutRegs = 64, kStateRegs = 128, kControlRegs = 40;
-static_assert(kScoreRegs + kOutRegs + 2 * kStateRegs + kControlRegs <= 5 * kLaunchRegs, "what the launch brings");
+// warps 0-3 make P and own the outputs, 4-7 and 8-11 (two sets) the state; lane quarter: warp % 4.  14 warps: 128 registers
+// each, for with spills every reload would go to L2 (the first-level cache is all shared memory).
+constexpr int kStateThread = 128, kStateThreads = 256, kControlThread = 384;
+constexpr int kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kBlock = 448;
 constexpr float kStrong = -1.f;
 constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384, kVStage = 48, kTmemCols = 512;
-constexpr uint32_t kBarState = 1, kBarScores = 2, kBarOut = 3, kBarSet = 4;   // named barriers of the warps of a kind
+constexpr uint32_t kBarState = 1, kBarRows = 2, kBarSet = 3;   // named barriers of the warps of a kind
 
 struct Hdr {
   alignas(16) float w[2][kC];        // lambda^(n-1-j), 0 from n on: a full chunk, the last chunk (read 16 bytes at a time)
@@ -82,31 +80,22 @@ struct Shape {
 };
 
 // ---- waits -----------------------------------------------------------------------------------------------
-// The code of a wait is kept short (six kinds of warps share the instruction caches): the polling loop is one function.
-__device__ __noinline__ void wait_slow(int* dead, uint64_t* bar, uint32_t parity, int32_t* status) {
-  const uint64_t t0 = globaltimer();
-  for (;;) {
+// Short, and no function call: a call would bind the registers of every caller.
+__device__ __forceinline__ void wait(Hdr& hd, uint64_t* bar, uint32_t parity, int32_t* status) {
+  uint64_t t0 = 0;
 #pragma unroll 1
-    for (int n = 0; n < 16; ++n)
-      if (mbar_try(bar, parity)) return;
-    if (*(volatile int*)dead != 0) return;
-    if (globaltimer() - t0 > kWaitLimitNs) {
+  while (!mbar_try(bar, parity)) {
+    const uint64_t now = globaltimer();
+    if (*(volatile int*)&hd.dead != 0) return;
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
       if (status != nullptr) atomicCAS(status, 0, ERS_ETIMEOUT);
-      *(volatile int*)dead = 1;
-      return;
+      *(volatile int*)&hd.dead = 1;
     }
   }
 }
-__device__ __forceinline__ void wait(Hdr& hd, uint64_t* bar, uint32_t parity, int32_t* status) {
-  if (!mbar_try(bar, parity)) wait_slow(&hd.dead, bar, parity, status);
-}
 __device__ __forceinline__ bool dead(const Hdr& hd) { return *(const volatile int*)&hd.dead != 0; }
 
-// a warpgroup's share of the registers
-template <int n>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
-template <int n>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n)); }
 // one lane of a converged warp
 __device__ __forceinline__ bool elected() {
   uint32_t r;
@@ -243,14 +232,10 @@ __device__ __forceinline__ uint32_t take_term(uint64_t& v) {
 }
 
 // Row t of 32 output columns, from the tokens first[] (of either set) on not finite.
-__device__ __noinline__ void spoil_mask(uint32_t* hit, const uint8_t* first0, const uint8_t* first1, int t) {
-  uint32_t m = 0;
-  for (int j = 0; j < 32; ++j) m |= (uint32_t)(t >= first0[j] || t >= first1[j]) << j;
-  *hit = m;
-}
 __device__ __forceinline__ void spoil(uint32_t (&o)[32], const uint8_t* first0, const uint8_t* first1, int t) {
-  uint32_t m;
-  spoil_mask(&m, first0, first1, t);
+  uint32_t m = 0;
+#pragma unroll 1
+  for (int j = 0; j < 32; ++j) m |= (uint32_t)(t >= first0[j] || t >= first1[j]) << j;
 #pragma unroll
   for (int j = 0; j < 32; ++j)
     if (m >> j & 1u) o[j] = 0x7fffffff;
@@ -462,15 +447,26 @@ struct Cta {
     }
   }
 
-  // ---- warps 0-3: P over S, a thread per row ----------------------------------------------------------------------------------
-  __device__ __forceinline__ void scores_of_chunks() const {
+  // ---- warps 0-3: P over S, and the outputs, a thread per row ------------------------------------------------------------------
+  __device__ __forceinline__ void rows_of_chunks(int m0, bool fresh) const {
     uint64_t u[16];                                // lambda^-j
 #pragma unroll
     for (int j = 0; j < 16; ++j) u[j] = strong ? 0ull : pair(expf(a_h * (float)(-2 * j)), expf(a_h * (float)(-2 * j - 1)));
-    for (int i = 0; i < run.c1 - run.c0; ++i) {
-      wt_group(kBarScores, &hd.s_ready, i);
+    for (int c = run.c0; c < run.c1; ++c) {
+      const int i = c - run.c0;
+      wt_group(kBarRows, &hd.s_ready, i);
       scores(u);
       mbar_arrive(&hd.p_ready);
+      if (strong) {
+        wt_group(kBarRows, &hd.qh_done, i);
+        if (!(fresh && i == 0)) scale_rows();
+        mbar_arrive(&hd.o_scaled);
+      }
+      wt_group(kBarRows, &hd.o_ready, i);
+      outputs(c, obuf(m0 + i));
+      mbar_arrive(&hd.o_free);
+      if (i > 0) wt_group(kBarRows, &hd.k_empty[(m0 + i - 1) & 1], (m0 + i - 1) / 2);   // the loader has taken the last one
+      mbar_arrive(&hd.o_staged);
     }
   }
   // Columns [16 b, 16 b + 16) of S become the hi terms of P in the first 8 columns of the block and the lo terms in the others.
@@ -529,25 +525,9 @@ struct Cta {
     }
   }
 
-  // ---- warps 4-7: outputs, a thread per row -------------------------------------------------------------------------------------
-  __device__ __forceinline__ void outputs_of_chunks(int m0, bool fresh) const {
-    for (int c = run.c0; c < run.c1; ++c) {
-      const int i = c - run.c0;
-      if (strong) {
-        wt_group(kBarOut, &hd.qh_done, i);
-        if (!(fresh && i == 0)) scale_rows();
-        mbar_arrive(&hd.o_scaled);
-      }
-      wt_group(kBarOut, &hd.o_ready, i);
-      outputs(c, obuf(m0 + i));
-      mbar_arrive(&hd.o_free);
-      if (i > 0) wt_group(kBarOut, &hd.k_empty[(m0 + i - 1) & 1], (m0 + i - 1) / 2);   // the loader has taken the last one
-      mbar_arrive(&hd.o_staged);
-    }
-  }
   // kStrong: the state's part of the outputs, times lambda^(i+1)
   __device__ __forceinline__ void scale_rows() const {
-    const int t = threadIdx.x - kOutThread;
+    const int t = threadIdx.x;
     const uint32_t at = tb + ((uint32_t)(t & ~31) << 16) + kColO;
     const uint64_t carry = both(hd.power[t + 1]);
     tmem_each32(at, DV, [&](int x, uint32_t (&o)[32]) {
@@ -559,7 +539,7 @@ struct Cta {
     before_sync();
   }
   __device__ __forceinline__ void outputs(int c, uint8_t* stage) const {
-    const int t = threadIdx.x - kOutThread, i = c - run.c0;
+    const int t = threadIdx.x, i = c - run.c0;
     const uint32_t at = tb + ((uint32_t)(t & ~31) << 16) + kColO;
     const uint64_t factor = both(strong ? a.scale : a.scale * expf(a_h * (float)(t - 63)));
     const bool bad = *reinterpret_cast<const uint64_t*>(hd.bad[i & 1]) != 0;
@@ -579,7 +559,7 @@ struct Cta {
     fence_async_smem();
   }
 
-  // ---- warps 8-15: V' and the state ------------------------------------------------------------------------------------------------
+  // ---- warps 4-11: V' and the state ------------------------------------------------------------------------------------------------
   // Quarter `quarter` of a chunk's V', its n-th in all: 32 tokens as three terms into tensor memory, 32 rows d per warp.
   // Even quarters are the first set's and go to stage 0, odd ones the second's and stage 1.  The tile's rows are tokens:
   // ldmatrix turns 8 x 8 blocks of it as tcgen05.st takes them.  nan collects whether anything was not finite.
@@ -702,7 +682,7 @@ struct Cta {
   }
 
   // first pass: weights up to the run's end
-  __device__ __forceinline__ void run_values(float a_h) const {
+  __device__ __forceinline__ void run_values() const {
     __nv_bfloat162 nan(0.f, 0.f);
     for (int c = run.c0; c < run.c1; ++c) {
       const int m = c - run.c0;
@@ -789,7 +769,7 @@ struct Cta {
   }
 
   // Start states from the runs' own end states, in place: this CTA turns DV / split rows of every run's.
-  __device__ __forceinline__ void join(const float* init, float a_h, int rank, int split) const {
+  __device__ __forceinline__ void join(const float* init, int rank, int split) const {
     const int rows_each = DV / split;
     const float f = expf(a_h * (float)(run.per * kC));
     for (int e = threadIdx.x; e < rows_each * (DK / 4); e += kBlock) {
@@ -883,13 +863,9 @@ __global__ void __launch_bounds__(kBlock, 1)
   before_sync();
   __syncthreads();
   after_sync();
-  if (tid >= kControlThread) regs_down<kControlRegs>();
-  else if (tid >= kStateThread) regs_up<kStateRegs>();
-  else if (tid >= kOutThread) regs_down<kOutRegs>();
-  else regs_up<kScoreRegs>();
   Cta<DK, DV> cta{a, maps, hd, base, hop, __shfl_sync(kFull, hd.tmem, 0), h, h / (a.H / a.G), a_h, a_h < kStrong, run};
 
-  // ---- first pass -----------------------------------------------------------------------------------------
+  // Of a split sequence, all runs but the last first form their own end states (K and V only); the cluster joins them.
   const bool first = run.last_run > 0 && rank < run.last_run;
   int quarters = 0;
   uint32_t kv_phase = 0;
@@ -900,8 +876,8 @@ __global__ void __launch_bounds__(kBlock, 1)
       if (lane == 0) cta.load_states();
     } else if (warp == kMmaWarp) {
       cta.issue_states(quarters);
-    } else if (tid >= kStateThread && tid < kControlThread) {
-      cta.run_values(a_h);
+    } else if (tid >= kStateThread) {
+      cta.run_values();
       cta.state_out(nullptr, true);
     }
     quarters = 4 * (run.c1 - run.c0);
@@ -910,27 +886,22 @@ __global__ void __launch_bounds__(kBlock, 1)
   if (split > 1) {
     before_sync();
     cluster_sync();
-    if (run.last_run > 0) cta.join(seq.in, a_h, rank, split);
+    if (run.last_run > 0) cta.join(seq.in, rank, split);
     cluster_sync();
     after_sync();
   }
   const bool given = run.last_run > 0 ? (rank > 0 || seq.in != nullptr) : seq.in != nullptr;
-
-  // ---- the chunks -------------------------------------------------------------------------------------------
   if (run.c0 < run.c1) {
     if (warp == kLoadWarp) {
       if (lane == 0) cta.load_chunks(m0);
     } else if (warp == kMmaWarp) {
       cta.issue_chunks(m0, quarters, !given);
-    } else if (tid >= kControlThread) {
     } else if (tid >= kStateThread) {
       if (given) cta.state_in(seq.in, run.last_run > 0);
       cta.states(m0, kv_phase, !given);
       if (rank == run.last_run && !dead(hd)) cta.state_out(seq.out, false);
-    } else if (tid >= kOutThread) {
-      cta.outputs_of_chunks(m0, !given);
     } else {
-      cta.scores_of_chunks();
+      cta.rows_of_chunks(m0, !given);
     }
   }
   __syncwarp();
