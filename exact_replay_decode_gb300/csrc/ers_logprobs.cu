@@ -2,14 +2,17 @@
 // m = max_j x_j, d_j = scale (x_j - m), z = sum_j exp(d_j):
 //   logprob = d_target - log z,  entropy = log z - sum_j exp(d_j) d_j / z
 //
-// One pass over the logits.  A thread keeps a running maximum and, relative to it, the sums of exp(d) and exp(d) d; threads,
-// and the CTAs of a row's cluster where rows are few, are joined at the end.  For the alternatives the pass only notes the
-// maximum of each segment (a warp's 512 bytes): the k-th largest of 256 maxima over disjoint parts is a lower bound of the
-// k-th best logit, so the segments that reach it, little more than k of them, are read again (from L2) and what reaches it
-// is ranked.  Should the candidates overflow, the k-th best of those found is a better bound, and the segments are read once
-// more.
+// One pass over the logits.  A thread keeps a running maximum m and, relative to r = m c (c = scale log2 e), the sums of
+// 2^(x c - r) and of that times its exponent, two logits an instruction; threads, and the CTAs of a row's cluster where
+// rows are few, are joined at the end.  For the alternatives the pass notes the maximum of each segment (a warp's 512
+// bytes): the k-th largest of the maxima of 64 disjoint parts is a lower bound of the k-th best logit, so the segments that
+// reach it, about 1.2 k of them, are read again (from L2) and what reaches it is ranked.  Should the candidates overflow, the
+// k-th best of those found is a better bound, and the segments are read once more.
 //
-// What bounds it: 2 (4) bytes a logit from memory; 152 SMs at 6.8 TB/s leave 10.9 issue slots a bf16 logit, of which it takes 7.
+// Logits below kFloor count as kFloor in that pass (-inf times a weight of nothing would be NaN): a row whose maximum is
+// not far above it, or so large that x c would overflow, is read once more and summed with x - m in place of x c - r.
+//
+// What bounds it: 2 (4) bytes a logit from memory; 152 SMs at 6.8 TB/s leave 10.9 issue slots a bf16 logit, of which it takes 6.
 #include <limits.h>
 #include <math.h>
 #include <string.h>
@@ -24,9 +27,9 @@ namespace {
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;           // segments a warp has under way
 constexpr int kSegs = 2048;          // segment maxima of a CTA
-constexpr int kCandidates = 512;
+constexpr int kCandidates = 256;
 constexpr int kMaxSplit = 8;         // CTAs of a row
-constexpr float kLog2e = 1.44269504f;
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 // values in order as whole numbers; -0 and +0 are equal
 __device__ __forceinline__ int order_of(float x) {
@@ -47,6 +50,31 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 units in the last p
   return y;
 }
 
+// pairs of floats, one instruction for two
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN stays one
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kFloor = -1.2676506e30f;   // -2^100: a bf16 number
+
 template <typename T> struct Vec;   // 16 bytes of logits
 template <> struct Vec<float> {
   static constexpr int n = 4;
@@ -55,6 +83,17 @@ template <> struct Vec<float> {
     x[1] = __uint_as_float(r.y);
     x[2] = __uint_as_float(r.z);
     x[3] = __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ float top(const uint4& r) {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
+  // at least kFloor, in pairs
+  static __device__ __forceinline__ void raised(const uint4& r, uint64_t (&x)[2]) {
+    x[0] = pair(max_nan(__uint_as_float(r.x), kFloor), max_nan(__uint_as_float(r.y), kFloor));
+    x[1] = pair(max_nan(__uint_as_float(r.z), kFloor), max_nan(__uint_as_float(r.w), kFloor));
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
 };
 template <> struct Vec<__nv_bfloat16> {
@@ -67,6 +106,27 @@ template <> struct Vec<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+  static __device__ __forceinline__ float top(const uint4& r) {
+    const __nv_bfloat162 m = __hmax2(__hmax2(two(r.x), two(r.y)), __hmax2(two(r.z), two(r.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ void raised(const uint4& r, uint64_t (&x)[4]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    const __nv_bfloat162 least = __floats2bfloat162_rn(kFloor, kFloor);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __hmax2_nan(two(w[i]), least);
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
+      x[i] = pair(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {   // of values that are bf16 already
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(x[2 * i]) >> 16 | (__float_as_uint(x[2 * i + 1]) & 0xffff0000u);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
 
 // A row as 16-byte vectors from the last aligned address at or before its start: element e of vector v is logit
@@ -75,10 +135,15 @@ template <typename T>
 struct Row {
   const T* base;
   int shift, vocab;
-  __device__ __forceinline__ int vectors() const { return (int)(((long long)vocab + shift + Vec<T>::n - 1) / Vec<T>::n); }
-  __device__ __forceinline__ bool whole(int v) const {
-    return (v > 0 || shift == 0) && ((long long)v + 1) * Vec<T>::n <= (long long)vocab + shift;
+  int whole0, whole1;   // vectors [whole0, whole1) lie within the row
+  __device__ __forceinline__ Row(const T* x, int vocab_) : vocab(vocab_) {
+    shift = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    base = x - shift;
+    whole0 = shift == 0 ? 0 : 1;
+    whole1 = (int)(((long long)vocab + shift) / Vec<T>::n);
   }
+  __device__ __forceinline__ int vectors() const { return (int)(((long long)vocab + shift + Vec<T>::n - 1) / Vec<T>::n); }
+  __device__ __forceinline__ bool whole(int v) const { return v >= whole0 && v < whole1; }
   __device__ __forceinline__ uint4 load(int v) const {
     uint4 r;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -87,47 +152,49 @@ struct Row {
     return r;
   }
   // a vector that the row does not fill: -inf outside
-  __device__ __forceinline__ void edge(int v, float (&x)[Vec<T>::n]) const {
+  __device__ __forceinline__ uint4 edge(int v) const {
+    float x[Vec<T>::n];
 #pragma unroll
     for (int e = 0; e < Vec<T>::n; ++e) {
       const long long j = (long long)v * Vec<T>::n + e - shift;
       x[e] = j >= 0 && j < vocab ? to_f(base[j + shift]) : -INFINITY;
     }
+    return Vec<T>::pack(x);
   }
-  __device__ __forceinline__ void get(int v, float (&x)[Vec<T>::n]) const {
-    if (whole(v)) Vec<T>::unpack(load(v), x);
-    else edge(v, x);
-  }
+  __device__ __forceinline__ uint4 get(int v) const { return whole(v) ? load(v) : edge(v); }
 };
 
-// exp(d) and exp(d) d relative to m, in the units of x (d = c (x - m) is taken to base 2: c = scale log2 e)
+// z = sum 2^(u) and zu = sum 2^(u) u, u = x c - r (or, of the rows that are read again, (x - m) c with r = 0)
 struct Sums {
-  float m, z, zd;
-  __device__ __forceinline__ void raise(float to, float c) {
-    if (z != 0.f) {
-      const float f = exp2_fast((m - to) * c);
-      zd = f > 0.f ? f * fmaf(z, m - to, zd) : 0.f;
-      z *= f;
-    }
-    m = to;
+  float r, z, zu;
+  __device__ __forceinline__ void raise(float to) {
+    const float f = exp2_fast(r - to);
+    zu = f > 0.f ? f * fmaf(z, r - to, zu) : 0.f;
+    z *= f;
+    r = to;
   }
-  __device__ __forceinline__ void join(const Sums& o, float c) {
+  __device__ __forceinline__ void join(const Sums& o) {
     Sums u = o;
-    if (u.m > m) raise(u.m, c);
-    else u.raise(m, c);
+    if (u.r > r) raise(u.r);
+    else u.raise(r);
     z += u.z;
-    zd += u.zd;
+    zu += u.zu;
+  }
+  __device__ __forceinline__ Sums across(int off) const {
+    return {__shfl_xor_sync(kFull, r, off), __shfl_xor_sync(kFull, z, off), __shfl_xor_sync(kFull, zu, off)};
   }
 };
 
 struct Shared {
   Sums sums[kWarps];
-  int part_max[kThreads];
+  float top[kWarps];
+  int part[64];              // maxima of the parts: four threads each
   unsigned long long candidates[kCandidates];
   int count;
   unsigned long long best[ERS_TOP_MAX];
   // of the row's first CTA: what all of them found
-  Sums all_sums[kMaxSplit];
+  Sums all_sums[kMaxSplit], again[kMaxSplit];
+  float all_top[kMaxSplit];   // of every CTA
   unsigned long long all_best[kMaxSplit * ERS_TOP_MAX];
   int seg_max[kSegs];
 };
@@ -136,16 +203,16 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 template <typename V>
-__device__ __forceinline__ V* at_first(V* p) {   // the same object of the cluster's first CTA
+__device__ __forceinline__ V* at_cta(V* p, int rank) {   // the same object of the cluster's rank-th CTA
   uint64_t r;
-  asm("mapa.u64 %0, %1, 0;" : "=l"(r) : "l"(p));
+  asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
   return reinterpret_cast<V*>(r);
 }
+template <typename V>
+__device__ __forceinline__ V* at_first(V* p) { return at_cta(p, 0); }
 
-// The k best of n distinct keys in place of rank order into best[0..k), 0 beyond n.  All threads.
+// best[0..k), zeros before: the k best of n distinct keys, best first (zeros count as none).  All threads; ends with a barrier.
 __device__ __forceinline__ void rank_keys(const unsigned long long* keys, int n, unsigned long long* best, int k) {
-  if (threadIdx.x < k) best[threadIdx.x] = 0;
-  __syncthreads();
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const unsigned long long mine = keys[i];
     int rank = 0;
@@ -153,6 +220,13 @@ __device__ __forceinline__ void rank_keys(const unsigned long long* keys, int n,
     if (rank < k && mine != 0) best[rank] = mine;
   }
   __syncthreads();
+}
+// The sums of all warps, in the first one's threads.
+__device__ __forceinline__ Sums join_warps(const Sums* sums) {
+  Sums s = sums[threadIdx.x % kWarps];
+#pragma unroll
+  for (int off = kWarps / 2; off >= 1; off >>= 1) s.join(s.across(off));
+  return s;
 }
 
 template <typename T, bool tops>
@@ -162,11 +236,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   const int row = blockIdx.x / split, rank = blockIdx.x % split;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const T* x0 = (const T*)a.logits + (long long)row * a.stride;
-  Row<T> x;
-  x.shift = (int)((reinterpret_cast<uintptr_t>(x0) & 15u) / sizeof(T));
-  x.base = x0 - x.shift;
-  x.vocab = a.vocab;
-  const int vectors = x.vectors(), segs = (vectors + 31) / 32;
+  const Row<T> x(x0, a.vocab);
+  const int segs = (x.vectors() + 31) / 32;
   const int per = (segs + split - 1) / split;
   const int s0 = min(rank * per, segs), s1 = min(s0 + per, segs);
   const int group = (per + kSegs - 1) / kSegs;   // segments behind one noted maximum
@@ -178,35 +249,49 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   }
 
   // ---- one pass ------------------------------------------------------------------------------------------------------
-  Sums s = {-3.402823466e38f, 0.f, 0.f};
+  const float r0 = kFloor * c;
+  float top = -INFINITY;                    // the thread's maximum
+  float r = r0;
+  uint64_t z2 = 0, zu2 = 0;                 // two zeros each
+  const uint64_t c2 = pair(c, c);
   for (int g = s0 + warp; g < s1; g += kWarps * kUnroll) {
     uint4 raw[kUnroll];
-    bool whole[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int seg = g + u * kWarps, v = seg * 32 + lane;
-      whole[u] = seg < s1 && x.whole(v);
-      if (whole[u]) raw[u] = x.load(v);
+      const int seg = g + u * kWarps;
+      if (seg < s1) raw[u] = x.get(seg * 32 + lane);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int seg = g + u * kWarps, v = seg * 32 + lane;
+      const int seg = g + u * kWarps;
       if (seg >= s1) break;
-      float y[n];
-      if (whole[u]) Vec<T>::unpack(raw[u], y);
-      else x.edge(v, y);
-      float top = y[0];
+      const float t = Vec<T>::top(raw[u]);
+      if (t > top) {
+        top = t;
+        const float to = fmaxf(t, kFloor) * c;
+        float za, zb, ua, ub;
+        unpair(z2, za, zb);
+        unpair(zu2, ua, ub);
+        Sums s = {r, za + zb, ua + ub};
+        s.raise(to);
+        r = to;
+        z2 = pair(s.z, 0.f);
+        zu2 = pair(s.zu, 0.f);
+      }
+      uint64_t y[n / 2];
+      Vec<T>::raised(raw[u], y);
+      const uint64_t r2 = pair(-r, -r);
 #pragma unroll
-      for (int e = 1; e < n; ++e) top = fmaxf(top, y[e]);
-      if (top > s.m) s.raise(top, c);
-#pragma unroll
-      for (int e = 0; e < n; ++e) {
-        const float d = y[e] - s.m, t = exp2_fast(d * c);
-        s.z += t;
-        s.zd = fmaf(t, fmaxf(d, -1e30f), s.zd);   // exp(-inf) times -inf is nothing
+      for (int e = 0; e < n / 2; ++e) {
+        const uint64_t w = fma2(y[e], c2, r2);
+        float wa, wb;
+        unpair(w, wa, wb);
+        const uint64_t p = pair(exp2_fast(wa), exp2_fast(wb));
+        z2 = add2(z2, p);
+        zu2 = fma2(p, w, zu2);
       }
       if (tops) {
-        const int o = __reduce_max_sync(kFull, order_of(top));
+        const int o = __reduce_max_sync(kFull, order_of(t));
         if (lane == 0) {
           if (group == 1) sh.seg_max[seg - s0] = o;
           else atomicMax(&sh.seg_max[(seg - s0) / group], o);
@@ -214,55 +299,61 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
       }
     }
   }
+  float za, zb, ua, ub;
+  unpair(z2, za, zb);
+  unpair(zu2, ua, ub);
+  Sums s = {r, za + zb, ua + ub};
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    const Sums o = {__shfl_xor_sync(kFull, s.m, off), __shfl_xor_sync(kFull, s.z, off), __shfl_xor_sync(kFull, s.zd, off)};
-    s.join(o, c);
+  for (int off = 1; off < 32; off <<= 1) {
+    s.join(s.across(off));
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+    if (tops && off == 2 && lane % 4 == 0) sh.part[threadIdx.x / 4] = order_of(top);
   }
-  if (lane == 0) sh.sums[warp] = s;
+  if (lane == 0) {
+    sh.sums[warp] = s;
+    sh.top[warp] = top;
+  }
+  if (tops && threadIdx.x < ERS_TOP_MAX) sh.best[threadIdx.x] = 0;
+  if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
-  s = sh.sums[0];
+  top = sh.top[0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) s.join(sh.sums[w], c);
+  for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh.top[w]);
+  if (warp == 0) s = join_warps(sh.sums);
 
   // ---- this CTA's best -------------------------------------------------------------------------------------------------
   if (tops) {
-    const int k = a.top_k;
-    int part = INT_MIN;
-    for (int i = threadIdx.x; i < noted; i += kThreads) part = max(part, sh.seg_max[i]);
-    sh.part_max[threadIdx.x] = part;
-    if (threadIdx.x == 0) sh.best[0] = 0;
-    __syncthreads();
-    int above = 0;
-    for (int i = 0; i < kThreads; ++i) {
-      const int o = sh.part_max[i];
-      above += o > part || (o == part && i < threadIdx.x);
-    }
-    // a bound in key order: (k-th part's maximum, any index)
-    if (above == k - 1) sh.best[0] = (unsigned long long)((unsigned)part ^ 0x80000000u) << 32;
-    __syncthreads();
-    unsigned long long bound = sh.best[0];
-    const int nothing = order_of(-INFINITY);
-    for (;;) {
-      __syncthreads();
-      if (threadIdx.x == 0) sh.count = 0;
-      __syncthreads();
-      const int least = key_order(bound);
-      for (int i = warp; i < noted; i += kWarps) {
-        if (sh.seg_max[i] < least || sh.seg_max[i] <= nothing) continue;
-        for (int seg = s0 + i * group; seg < min(s0 + (i + 1) * group, s1); ++seg) {
-          const int v = seg * 32 + lane;
-          if (v >= vectors) continue;
-          float y[n];
-          x.get(v, y);
+    const int k = a.top_k, nothing = order_of(-INFINITY);
+    // a bound: the upper 16 bits of the k-th largest of the parts' maxima
+    const unsigned upper0 = ((unsigned)sh.part[lane] ^ 0x80000000u) >> 16, upper1 = ((unsigned)sh.part[32 + lane] ^ 0x80000000u) >> 16;
+    unsigned least = 0;
 #pragma unroll
-          for (int e = 0; e < n; ++e) {
-            const int o = order_of(y[e]);
-            if (o < least || !(y[e] > -INFINITY)) continue;
-            const unsigned long long key = key_of(o, v * n + e - x.shift);
-            if (key >= bound) {
-              const int at = atomicAdd(&sh.count, 1);
-              if (at < kCandidates) sh.candidates[at] = key;
+    for (int b = 15; b >= 0; --b) {
+      const unsigned with = least | 1u << b;
+      if (__popc(__ballot_sync(kFull, upper0 >= with)) + __popc(__ballot_sync(kFull, upper1 >= with)) >= k) least = with;
+    }
+    unsigned long long bound = (unsigned long long)least << 48;
+    for (;;) {
+      const int from = max(key_order(bound), nothing + 1);
+      for (int i0 = warp; i0 < noted; i0 += kThreads) {   // a lane per noted maximum, warps taking turns
+        const int i = i0 + lane * kWarps;
+        unsigned hits = __ballot_sync(kFull, i < noted && sh.seg_max[i] >= from);
+        while (hits != 0) {
+          const int first = s0 + (i0 + (__ffs(hits) - 1) * kWarps) * group;
+          hits &= hits - 1;
+          for (int seg = first; seg < min(first + group, s1); ++seg) {
+            if (*(volatile int*)&sh.count > kCandidates) break;   // there will be another time
+            float y[n];
+            Vec<T>::unpack(x.get(seg * 32 + lane), y);
+#pragma unroll
+            for (int e = 0; e < n; ++e) {
+              const int o = order_of(y[e]);
+              if (o < from || !(y[e] > -INFINITY)) continue;
+              const unsigned long long key = key_of(o, (seg * 32 + lane) * n + e - x.shift);
+              if (key >= bound) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kCandidates) sh.candidates[at] = key;
+              }
             }
           }
         }
@@ -272,23 +363,68 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
       rank_keys(sh.candidates, min(found, kCandidates), sh.best, k);
       if (found <= kCandidates) break;
       bound = sh.best[k - 1];
+      __syncthreads();
+      if (threadIdx.x < ERS_TOP_MAX) sh.best[threadIdx.x] = 0;
+      if (threadIdx.x == 0) sh.count = 0;
+      __syncthreads();
     }
   }
 
   // ---- the row ---------------------------------------------------------------------------------------------------------
-  const unsigned long long* best = sh.best;
   if (split > 1) {
+    if (threadIdx.x < split) at_cta(sh.all_top, threadIdx.x)[rank] = top;
     if (threadIdx.x == 0) at_first(sh.all_sums)[rank] = s;
-    if (tops && threadIdx.x < ERS_TOP_MAX)
-      at_first(sh.all_best)[rank * ERS_TOP_MAX + threadIdx.x] = threadIdx.x < a.top_k ? sh.best[threadIdx.x] : 0;
+    if (tops && threadIdx.x < a.top_k) at_first(sh.all_best)[rank * a.top_k + threadIdx.x] = sh.best[threadIdx.x];
     cluster_sync();
-    if (rank != 0) return;
-    s = sh.all_sums[0];
-    for (int r = 1; r < split; ++r) s.join(sh.all_sums[r], c);
-    if (tops) rank_keys(sh.all_best, split * ERS_TOP_MAX, sh.best, a.top_k);
+    for (int q = 0; q < split; ++q) top = fmaxf(top, sh.all_top[q]);
   }
-  const bool none = !(s.z < INFINITY), empty = s.z == 0.f;   // z is at least 1 where anything is left
-  const float log_z = logf(s.z);
+  const bool again = fabsf(top) >= 1e29f && fabsf(top) < INFINITY;
+  if (again) {
+    s = {0.f, 0.f, 0.f};
+    for (int v = s0 * 32 + threadIdx.x; v < s1 * 32; v += kThreads * kUnroll) {
+      uint4 raw[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) raw[u] = x.get(v + u * kThreads);
+#pragma unroll 1
+      for (int u = 0; u < kUnroll && v + u * kThreads < s1 * 32; ++u) {
+        float y[n];
+        Vec<T>::unpack(u == 0 ? raw[0] : u == 1 ? raw[1] : u == 2 ? raw[2] : raw[3], y);
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+          const float w = (y[e] - top) * c, p = exp2_fast(w);
+          s.z += p;
+          if (!(p == 0.f)) s.zu = fmaf(p, w, s.zu);
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) s.join(s.across(off));
+    __syncthreads();
+    if (lane == 0) sh.sums[warp] = s;
+    __syncthreads();
+    if (warp == 0) s = join_warps(sh.sums);
+    if (split > 1) {
+      if (threadIdx.x == 0) at_first(sh.again)[rank] = s;
+      cluster_sync();
+    }
+  }
+  if (rank != 0) return;
+  if (split > 1) {
+    const Sums* all = again ? sh.again : sh.all_sums;
+    s = all[0];
+    for (int q = 1; q < split; ++q) s.join(all[q]);
+    if (tops) {
+      __syncthreads();
+      if (threadIdx.x < ERS_TOP_MAX) sh.best[threadIdx.x] = 0;
+      __syncthreads();
+      rank_keys(sh.all_best, split * a.top_k, sh.best, a.top_k);
+    }
+  }
+  if (warp != 0) return;
+  const bool none = !(s.z < INFINITY) || top == INFINITY, empty = top == -INFINITY && !none;
+  // r is the maximum's x c but for its rounding
+  const float log_z = logf(s.z), most = (again ? 0.f : fmaf(top, c, -s.r) * kLn2) - log_z;
+  const auto logprob = [&](float v) { return fmaf(v - top, a.scale, most); };
   if (threadIdx.x == 0) {
     if (a.logprob != nullptr) {
       const int t = a.target[row];
@@ -297,18 +433,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
         report(a.status, ERS_EINVAL);
         lp = NAN;
       } else if (t >= 0) {
-        lp = none ? NAN : empty ? -INFINITY : a.scale * (to_f(x0[t]) - s.m) - log_z;
+        lp = none ? NAN : empty ? -INFINITY : logprob(to_f(x0[t]));
       }
       a.logprob[row] = lp;
     }
-    if (a.entropy != nullptr) a.entropy[row] = none ? NAN : empty ? 0.f : log_z - a.scale * s.zd / s.z;
+    if (a.entropy != nullptr) a.entropy[row] = none ? NAN : empty ? 0.f : log_z - kLn2 * s.zu / s.z;
   }
   if (tops && threadIdx.x < a.top_k) {
-    const unsigned long long key = best[threadIdx.x];
+    const unsigned long long key = sh.best[threadIdx.x];
     const bool gone = none || key == 0;
     const size_t at = (size_t)row * a.top_k + threadIdx.x;
     a.top_id[at] = gone ? -1 : key_index(key);
-    a.top_logprob[at] = none ? NAN : gone ? -INFINITY : a.scale * (value_of(key_order(key)) - s.m) - log_z;
+    a.top_logprob[at] = none ? NAN : gone ? -INFINITY : logprob(value_of(key_order(key)));
   }
 }
 
