@@ -23,7 +23,8 @@ def __getattr__(name):
         return getattr(ops, name)
     if name in _SERVE:
         from . import serve
-        return getattr(serve, name)
+        globals()[name] = value = getattr(serve, name)   # the next look-up finds it here
+        return value
     if name in ("ErsError",):
         from . import _abi
         return _abi.ErsError

@@ -2,7 +2,8 @@
 attention with a decay per head, the pages of a cache, and log probabilities of given tokens.
 
 Marshalling only, as in ops.py: shape, dtype and contiguity checks, outputs and workspaces from torch,
-the caller's stream."""
+the caller's stream.  A decode step's call is a few microseconds of kernel, so the checks of a call that passes
+them are kept to one comparison each."""
 from __future__ import annotations
 
 import ctypes
@@ -12,7 +13,10 @@ from typing import List, Optional, Sequence, Tuple
 import torch
 
 from . import _abi
-from .ops import ReplayCache, Status, _finish, _io_from, _IO, _need, _ptr, _slot_arg, _stream
+from .ops import ReplayCache, Status, _finish, _io_from, _IO, _need, _ptr
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _on_stream(f):
@@ -28,6 +32,18 @@ def _on_stream(f):
 
 def _status(status: Optional[Status], check: bool, device) -> Optional[Status]:
     return status if status is not None else (Status(device) if check else None)
+
+
+def _tensor(t: torch.Tensor, dtype, name: str, shape) -> int:
+    """The data pointer of a dense CUDA tensor of that type and shape; otherwise _need's error."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
+        _need(t, dtype, name, shape)
+    return t.data_ptr()
+
+
+def _where(device: torch.device, st: Optional[Status]):
+    """The launch's stream and status word."""
+    return _raw_stream(device.index), None if st is None else st.t.data_ptr()
 
 
 # ---- pages of a cache --------------------------------------------------------------------------
@@ -59,7 +75,12 @@ class PagePool:
                 raise ValueError(f"arrays[{k}]: {x.shape[0]} pages, expected {npages}")
         self.table, self.refs = table, refs
         self.npages, (self.nslots, self.slot_pages) = npages, table.shape
-        self._c = _pool_c(self.arrays, table, refs)
+        self._c = ctypes.byref(_pool_c(self.arrays, table, refs))
+        # scratch of the calls on this pool, which have to follow one another anyway
+        L = _abi.lib()
+        self._work = torch.empty(max(L.ers_pages_own_workspace_size(self._c, self.nslots),
+                                     L.ers_pages_compact_workspace_size(self._c), 16),
+                                 dtype=torch.uint8, device=table.device)
 
 
 def _pool_c(arrays: Sequence[torch.Tensor], table: Optional[torch.Tensor], refs: Optional[torch.Tensor]):
@@ -75,10 +96,9 @@ def _pool_c(arrays: Sequence[torch.Tensor], table: Optional[torch.Tensor], refs:
 
 
 def _list_arg(t: torch.Tensor, name: str, n: Optional[int] = None) -> int:
-    _need(t, torch.int32, name, None if n is None else (n,))
-    if t.dim() != 1:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected a list")
-    return t.data_ptr()
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name}: expected a one-dimensional tensor")
+    return _tensor(t, torch.int32, name, (t.numel() if n is None else n,))
 
 
 @_on_stream
@@ -88,7 +108,7 @@ def pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, status: Opt
     n = dst.numel()
     s, d = _list_arg(src, "src", n), _list_arg(dst, "dst", n)
     st = _status(status, check, dst.device)
-    code = _abi.lib().ers_pages_fork(ctypes.byref(pool._c), n, s, d, _stream(stream), _ptr(st.t) if st else None)
+    code = _abi.lib().ers_pages_fork(pool._c, n, s, d, *_where(dst.device, st))
     _finish(code, "ers_pages_fork", st, check)
 
 
@@ -101,11 +121,9 @@ def pages_own(pool: PagePool, slot: torch.Tensor, copy: bool = True, status: Opt
     n = slot.numel()
     sp = _list_arg(slot, "slot")
     read = torch.empty(n, pool.slot_pages, dtype=torch.int32, device=slot.device)
-    L = _abi.lib()
-    work = torch.empty(L.ers_pages_own_workspace_size(ctypes.byref(pool._c), n), dtype=torch.uint8, device=slot.device)
     st = _status(status, check, slot.device)
-    code = L.ers_pages_own(ctypes.byref(pool._c), n, sp, _abi.FLAG_COPY if copy else 0, read.data_ptr(),
-                           work.data_ptr(), work.numel(), _stream(stream), _ptr(st.t) if st else None)
+    code = _abi.lib().ers_pages_own(pool._c, n, sp, _abi.FLAG_COPY if copy else 0, read.data_ptr(),
+                                    pool._work.data_ptr(), pool._work.numel(), *_where(slot.device, st))
     _finish(code, "ers_pages_own", st, check)
     return read
 
@@ -116,8 +134,7 @@ def pages_free(pool: PagePool, slot: torch.Tensor, status: Optional[Status] = No
     """The listed slots give up their pages (ers_pages_free)."""
     sp = _list_arg(slot, "slot")
     st = _status(status, check, slot.device)
-    code = _abi.lib().ers_pages_free(ctypes.byref(pool._c), slot.numel(), sp, _stream(stream),
-                                     _ptr(st.t) if st else None)
+    code = _abi.lib().ers_pages_free(pool._c, slot.numel(), sp, *_where(slot.device, st))
     _finish(code, "ers_pages_free", st, check)
 
 
@@ -129,11 +146,9 @@ def pages_compact(pool: PagePool, status: Optional[Status] = None, check: bool =
     dev = pool.table.device
     remap = torch.empty(pool.npages, dtype=torch.int32, device=dev)
     live = torch.empty(1, dtype=torch.int32, device=dev)
-    L = _abi.lib()
-    work = torch.empty(L.ers_pages_compact_workspace_size(ctypes.byref(pool._c)), dtype=torch.uint8, device=dev)
     st = _status(status, check, dev)
-    code = L.ers_pages_compact(ctypes.byref(pool._c), remap.data_ptr(), live.data_ptr(), work.data_ptr(),
-                               work.numel(), _stream(stream), _ptr(st.t) if st else None)
+    code = _abi.lib().ers_pages_compact(pool._c, remap.data_ptr(), live.data_ptr(), pool._work.data_ptr(),
+                                        pool._work.numel(), *_where(dev, st))
     _finish(code, "ers_pages_compact", st, check)
     return remap, live
 
@@ -152,8 +167,7 @@ def pages_copy(arrays: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.Ten
     n = dst.numel()
     s, d = _list_arg(src, "src", n), _list_arg(dst, "dst", n)
     st = _status(status, check, dst.device)
-    code = _abi.lib().ers_pages_copy(ctypes.byref(_pool_c(arrays, None, None)), n, s, d, _stream(stream),
-                                     _ptr(st.t) if st else None)
+    code = _abi.lib().ers_pages_copy(ctypes.byref(_pool_c(arrays, None, None)), n, s, d, *_where(dst.device, st))
     _finish(code, "ers_pages_copy", st, check)
 
 
@@ -196,7 +210,7 @@ class LinAttnCache:
         else:
             table = torch.full((nslots, 1), -1, dtype=torch.int32, device=state.device)
         self.pages = PagePool([state], table, None)
-        self._c = _abi.LinAttnCache(state.data_ptr(), table.data_ptr(), nslots, self.npages)
+        self._c = ctypes.byref(_abi.LinAttnCache(state.data_ptr(), table.data_ptr(), nslots, self.npages))
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.state, self.pages.table, self.pages.refs))
@@ -208,15 +222,24 @@ def _linattn_dims(H: int, G: int, dk: int, dv: int, io: torch.dtype, scale: floa
     return _abi.LinAttnDims(H, G, dk, dv, _IO[io], float(scale))
 
 
-def _qkv(q, k, v, log_decay, io, T, H, G, dk, dv) -> None:
-    _need(q, io, "q", (T, G, dk)); _need(k, io, "k", (T, G, dk)); _need(v, io, "v", (T, H, dv))
-    _need(log_decay, torch.float32, "log_decay", (H,))
+def _qkv(q, k, v, log_decay, io, T, H, G, dk, dv):
+    """Checked; (log_decay, (q, k, v)) as pointers."""
+    return _tensor(log_decay, torch.float32, "log_decay", (H,)), (
+        _tensor(q, io, "q", (T, G, dk)), _tensor(k, io, "k", (T, G, dk)), _tensor(v, io, "v", (T, H, dv)))
+
+
+def _seqlens(cu_seqlens: Optional[torch.Tensor], T: int, device):
+    if cu_seqlens is None:
+        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=device)
+    S = cu_seqlens.numel() - 1
+    _tensor(cu_seqlens, torch.int32, "cu_seqlens", (S + 1,))
+    return cu_seqlens, S
 
 
 def _out(out: Optional[torch.Tensor], v: torch.Tensor) -> torch.Tensor:
     if out is None:
         return torch.empty_like(v)
-    _need(out, v.dtype, "out", v.shape)
+    _tensor(out, v.dtype, "out", v.shape)
     return out
 
 
@@ -234,24 +257,21 @@ def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
     io = _io_from(q)
     T, G, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
-    if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=q.device)
-    S = cu_seqlens.numel() - 1
-    _qkv(q, k, v, log_decay, io, T, H, G, dk, dv)
-    _need(cu_seqlens, torch.int32, "cu_seqlens")
-    if init_state is not None:
-        _need(init_state, torch.float32, "init_state", (S, H, dv, dk))
-    o = _out(None if out is None else out[0], v)
+    dev = q.device
+    cu_seqlens, S = _seqlens(cu_seqlens, T, dev)
+    decay, qkv = _qkv(q, k, v, log_decay, io, T, H, G, dk, dv)
+    state = (S, H, dv, dk)
+    init = None if init_state is None else _tensor(init_state, torch.float32, "init_state", state)
     if out is None:
-        final = torch.empty(S, H, dv, dk, dtype=torch.float32, device=q.device)
+        o, final = torch.empty_like(v), torch.empty(state, dtype=torch.float32, device=dev)
     else:
-        final = out[1]
-        _need(final, torch.float32, "out[1]", (S, H, dv, dk))
-    st = _status(status, check, q.device)
-    code = _abi.lib().ers_linattn_fwd(ctypes.byref(_linattn_dims(H, G, dk, dv, io, scale)), log_decay.data_ptr(), S, T,
-                                      T if max_seqlen is None else int(max_seqlen), cu_seqlens.data_ptr(),
-                                      q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(init_state), o.data_ptr(),
-                                      final.data_ptr(), _stream(stream), _ptr(st.t) if st else None)
+        o, final = out
+        _out(o, v)
+        _tensor(final, torch.float32, "out[1]", state)
+    st = _status(status, check, dev)
+    code = _abi.lib().ers_linattn_fwd(ctypes.byref(_linattn_dims(H, G, dk, dv, io, scale)), decay, S, T,
+                                      T if max_seqlen is None else int(max_seqlen), cu_seqlens.data_ptr(), *qkv,
+                                      init, o.data_ptr(), final.data_ptr(), *_where(dev, st))
     _finish(code, "ers_linattn_fwd", st, check)
     return o, final
 
@@ -261,8 +281,11 @@ def _read_arg(read_page: Optional[torch.Tensor], S: int):
         return None
     if read_page.dim() == 2:   # as pages_own returns it
         read_page = read_page[:, 0]
-    _need(read_page, torch.int32, "read_page", (S,))
-    return read_page.data_ptr()
+    return _tensor(read_page, torch.int32, "read_page", (S,))
+
+
+def _slot(slot: Optional[torch.Tensor], S: int):
+    return None if slot is None else _tensor(slot, torch.int32, "slot", (S,))
 
 
 @_on_stream
@@ -272,19 +295,15 @@ def linattn_prefill(cache: LinAttnCache, q, k, v, log_decay, cu_seqlens: Optiona
                     check: bool = True, stream=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Packed prompts that go on from the slots' cached states (ers_linattn_prefill): each state is read from
     read_page (default: the slot's own page; -1: zeros) and written to the slot's own page.  Returns o [T,H,dv]."""
-    T = q.shape[0]
-    if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=q.device)
-    S = cu_seqlens.numel() - 1
-    _qkv(q, k, v, log_decay, cache.io, T, cache.H, cache.G, cache.dk, cache.dv)
-    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    T, dev = q.shape[0], q.device
+    cu_seqlens, S = _seqlens(cu_seqlens, T, dev)
+    decay, qkv = _qkv(q, k, v, log_decay, cache.io, T, cache.H, cache.G, cache.dk, cache.dv)
     o = _out(out, v)
-    st = _status(status, check, q.device)
+    st = _status(status, check, dev)
     dims = _linattn_dims(cache.H, cache.G, cache.dk, cache.dv, cache.io, scale)
-    code = _abi.lib().ers_linattn_prefill(ctypes.byref(dims), log_decay.data_ptr(), ctypes.byref(cache._c), S, T,
+    code = _abi.lib().ers_linattn_prefill(ctypes.byref(dims), decay, cache._c, S, T,
                                           T if max_seqlen is None else int(max_seqlen), cu_seqlens.data_ptr(),
-                                          _slot_arg(slot, S), _read_arg(read_page, S), q.data_ptr(), k.data_ptr(),
-                                          v.data_ptr(), o.data_ptr(), _stream(stream), _ptr(st.t) if st else None)
+                                          _slot(slot, S), _read_arg(read_page, S), *qkv, o.data_ptr(), *_where(dev, st))
     _finish(code, "ers_linattn_prefill", st, check)
     return o
 
@@ -294,14 +313,13 @@ def linattn_decode(cache: LinAttnCache, q, k, v, log_decay, slot: Optional[torch
                    read_page: Optional[torch.Tensor] = None, scale: float = 1.0, status: Optional[Status] = None,
                    check: bool = True, stream=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One token per sequence (ers_linattn_decode): q, k [S,G,dk], v [S,H,dv]; states as in linattn_prefill."""
-    S = q.shape[0]
-    _qkv(q, k, v, log_decay, cache.io, S, cache.H, cache.G, cache.dk, cache.dv)
+    S, dev = q.shape[0], q.device
+    decay, qkv = _qkv(q, k, v, log_decay, cache.io, S, cache.H, cache.G, cache.dk, cache.dv)
     o = _out(out, v)
-    st = _status(status, check, q.device)
+    st = _status(status, check, dev)
     dims = _linattn_dims(cache.H, cache.G, cache.dk, cache.dv, cache.io, scale)
-    code = _abi.lib().ers_linattn_decode(ctypes.byref(dims), log_decay.data_ptr(), ctypes.byref(cache._c), S,
-                                         _slot_arg(slot, S), _read_arg(read_page, S), q.data_ptr(), k.data_ptr(),
-                                         v.data_ptr(), o.data_ptr(), _stream(stream), _ptr(st.t) if st else None)
+    code = _abi.lib().ers_linattn_decode(ctypes.byref(dims), decay, cache._c, S, _slot(slot, S),
+                                         _read_arg(read_page, S), *qkv, o.data_ptr(), *_where(dev, st))
     _finish(code, "ers_linattn_decode", st, check)
     return o
 
@@ -317,13 +335,13 @@ def token_logprobs(logits: torch.Tensor, target: Optional[torch.Tensor] = None, 
     io = _io_from(logits)
     if logits.dim() != 2:
         raise ValueError(f"logits: shape {tuple(logits.shape)}, expected (rows, vocabulary)")
-    if logits.device.type != "cuda":
+    if not logits.is_cuda:
         raise ValueError("logits: must be a CUDA tensor")
     R, V = logits.shape
     if V > 1 and logits.stride(1) != 1 or R > 1 and logits.stride(0) < V:
         raise ValueError(f"logits: strides {logits.stride()}, expected contiguous rows")
     if target is not None:
-        _need(target, torch.int32, "target", (R,))
+        _tensor(target, torch.int32, "target", (R,))
     dev, k = logits.device, int(top_k)
     if not 0 <= k <= _abi.TOP_MAX:
         raise ValueError(f"top_k: {k}, expected 0 to {_abi.TOP_MAX}")
@@ -335,6 +353,6 @@ def token_logprobs(logits: torch.Tensor, target: Optional[torch.Tensor] = None, 
     code = _abi.lib().ers_token_logprobs(_IO[io], R, V, logits.stride(0) if R > 1 else V, logits.data_ptr(),
                                          _ptr(target), float(scale), k, _ptr(logprob), entropy.data_ptr(),
                                          top_id.data_ptr() if k else None, top_logprob.data_ptr() if k else None,
-                                         _stream(stream), _ptr(st.t) if st else None)
+                                         *_where(dev, st))
     _finish(code, "ers_token_logprobs", st, check)
     return logprob, entropy, top_id, top_logprob
