@@ -1,56 +1,161 @@
 // Linear attention with a decay per head (include/ers.h), a = log_decay[h], lambda = exp(a):
 //   S_t = lambda S_{t-1} + v_t k_t^T  (S [dv x dk], fp32),  o_t = scale S_t q_t
+#include <type_traits>
+
 #include "ers_common.cuh"
 #include "ers_internal.h"
 #include "linattn.cuh"
+#include "tc_common.cuh"
 
 namespace ers {
 namespace {
 
-// ---- the recurrence, token by token -------------------------------------------------------------------
-// A thread owns 16 consecutive k of one state row in registers; dk / 16 neighbouring lanes own a row
-// and add up its product with q by a butterfly.  Tokens pass through shared memory kTok at a time.
-constexpr int kTok = 16;
+// ---- pairs of floats, one instruction for two ------------------------------------------------------------
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float sum_of(uint64_t v) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+  return x + y;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// four consecutive elements as two pairs
+__device__ __forceinline__ void load4(const float* p, uint64_t (&v)[2]) {
+  const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
+  v[0] = u.x;
+  v[1] = u.y;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, uint64_t (&v)[2]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  v[0] = pair(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+  v[1] = pair(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
 
-template <typename T, int DK>
-__global__ void __launch_bounds__(kThreads) k_linattn_steps(LinAttnArgs a) {
-  constexpr int W = DK / 16;              // lanes of a row
-  constexpr int R = kThreads / W;         // rows of a CTA
-  __shared__ float sq[kTok][DK], sk[kTok][DK], sv[kTok][R];
+// Adds up N values (a power of two) across the W neighbouring lanes that each hold a part of all of them, by halving: each
+// step exchanges half of what a lane still holds.  Afterwards v[0 .. max(N / W, 1)) of a lane are the totals of values
+// first, first + 1, ... (where N < W several lanes hold the same one).
+template <int N, int W>
+__device__ __forceinline__ void halve(float (&v)[N], int lane, int* first) {
+  int row = 0, off = W / 2;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2) {
+    if (off < 1) break;
+    const bool upper = (lane & off) != 0;
+#pragma unroll
+    for (int r = 0; r < n; ++r) {
+      const float give = upper ? v[r] : v[r + n], keep = upper ? v[r + n] : v[r];
+      v[r] = keep + __shfl_xor_sync(kFull, give, off);
+    }
+    if (upper) row += n;
+    off /= 2;
+  }
+#pragma unroll
+  for (; off >= 1; off /= 2) v[0] += __shfl_xor_sync(kFull, v[0], off);
+  *first = row;
+}
+
+// ---- the recurrence, token by token -------------------------------------------------------------------
+// fp32 prompts, and bf16 ones too short for chunks.  A warp owns state rows in registers (W = dk / 4 lanes a row, `rows` rows of
+// each lane), so a token costs a row 9 packed instructions and one exchange: no more than the same products in chunks would
+// on these cores, and rounded as the recurrence is.  Its products with q are added up for kBatch tokens at once.  Tokens come
+// through shared memory, kTok at a time, the next ones under way.  Latency: a token takes a warp some 60 cycles, so the
+// rows of a head are spread over as many warps as there are.
+constexpr int kTok = 16, kBatch = 8, kStepThreads = 128;
+
+template <typename T, int DK, int rows>
+__global__ void __launch_bounds__(kStepThreads) k_linattn_steps(LinAttnArgs a) {
+  constexpr int W = DK / 4, side = 32 / W;                  // rows that a warp holds in one register of its lanes
+  constexpr int R = kStepThreads / 32 * rows * side;        // rows of a CTA
+  constexpr int N = kBatch * rows, copies = N < W ? W / N : 1;   // lanes that end up with the same product
+  __shared__ alignas(16) T sq[2][kTok][DK];
+  __shared__ alignas(16) T sk[2][kTok][DK];
+  __shared__ alignas(16) T sv[2][kTok][R];
   const int i = blockIdx.x, h = blockIdx.y, g = h / (a.H / a.G);
   LinAttnSeq s;
   if (!linattn_seq(a, i, h, &s)) return;
-  const int j = threadIdx.x % W, r = threadIdx.x / W, d = blockIdx.z * R + r;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, j = lane % W;
+  const int own = warp * rows * side + lane / W;            // this lane's rows of the CTA: own + r * side
+  const int d0 = blockIdx.z * R;
+  uint64_t st[rows][2];
+#pragma unroll
+  for (int r = 0; r < rows; ++r) {
+    st[r][0] = st[r][1] = 0;
+    if (s.in != nullptr) load4(s.in + (size_t)(d0 + own + r * side) * DK + 4 * j, st[r]);
+  }
+  const auto fetch = [&](int t0, int b) {
+    constexpr int e = 16 / sizeof(T);                       // elements of a copy
+    const int n = min(kTok, s.len - t0);
+    for (int x = threadIdx.x; x < n * (DK / e); x += kStepThreads) {
+      const int t = x / (DK / e), c = x % (DK / e) * e;
+      const size_t at = ((size_t)(s.t0 + t0 + t) * a.G + g) * DK + c;
+      tc::cp_async16(&sq[b][t][c], (const T*)a.q + at);
+      tc::cp_async16(&sk[b][t][c], (const T*)a.k + at);
+    }
+    for (int x = threadIdx.x; x < n * (R / e); x += kStepThreads) {
+      const int t = x / (R / e), c = x % (R / e) * e;
+      tc::cp_async16(&sv[b][t][c], (const T*)a.v + ((size_t)(s.t0 + t0 + t) * a.H + h) * a.dv + d0 + c);
+    }
+    static_assert(R % e == 0, "whole copies");
+  };
+  if (s.len > 0) fetch(0, 0);
   const Decay lambda = decay_of(a.log_decay[h]);
-  float st[16];
+  const uint64_t hi = pair(lambda.hi, lambda.hi), lo = pair(lambda.lo, lambda.lo);
+  for (int t0 = 0, b = 0; t0 < s.len; t0 += kTok, b ^= 1) {
+    tc::cp_async_wait_all();
+    __syncthreads();                                        // this tile is there, the other one no longer read
+    if (t0 + kTok < s.len) fetch(t0 + kTok, b ^ 1);
+    const int n = min(kTok, s.len - t0);
+    const auto batch = [&](int t, auto whole) {             // whole: no token of it is missing, so no branch either
+      float dot[N];
 #pragma unroll
-  for (int c = 0; c < 16; ++c) st[c] = s.in != nullptr ? s.in[(size_t)d * DK + j * 16 + c] : 0.f;
-  for (int t0 = 0; t0 < s.len; t0 += kTok) {
-    const int n = s.len - t0 < kTok ? s.len - t0 : kTok;
-    __syncthreads();
-    for (int e = threadIdx.x; e < n * DK; e += kThreads) {
-      const size_t at = ((size_t)(s.t0 + t0 + e / DK) * a.G + g) * DK + e % DK;
-      sq[e / DK][e % DK] = to_f(((const T*)a.q)[at]);
-      sk[e / DK][e % DK] = to_f(((const T*)a.k)[at]);
-    }
-    for (int e = threadIdx.x; e < n * R; e += kThreads)
-      sv[e / R][e % R] = to_f(((const T*)a.v)[((size_t)(s.t0 + t0 + e / R) * a.H + h) * a.dv + blockIdx.z * R + e % R]);
-    __syncthreads();
-    for (int t = 0; t < n; ++t) {
-      const float vd = sv[t][r];
-      float dot = 0.f;
+      for (int u = 0; u < kBatch; ++u) {
+        if (whole.value || t + u < n) {
+          uint64_t k2[2], q2[2];
+          load4(&sk[b][t + u][4 * j], k2);
+          load4(&sq[b][t + u][4 * j], q2);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        st[c] = lambda.step(st[c], vd * sk[t][j * 16 + c]);
-        dot = fmaf(st[c], sq[t][j * 16 + c], dot);
+          for (int r = 0; r < rows; ++r) {
+            const float x = to_f(sv[b][t + u][own + r * side]);
+            const uint64_t v2 = pair(x, x);
+            st[r][0] = fma2(hi, st[r][0], fma2(lo, st[r][0], mul2(v2, k2[0])));
+            st[r][1] = fma2(hi, st[r][1], fma2(lo, st[r][1], mul2(v2, k2[1])));
+            dot[u * rows + r] = sum_of(fma2(st[r][1], q2[1], mul2(st[r][0], q2[0])));
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < rows; ++r) dot[u * rows + r] = 0.f;
+        }
       }
+      int first;
+      halve<N, W>(dot, lane, &first);
 #pragma unroll
-      for (int off = W / 2; off >= 1; off >>= 1) dot += __shfl_xor_sync(kFull, dot, off);
-      if (j == 0) ((T*)a.o)[((size_t)(s.t0 + t0 + t) * a.H + h) * a.dv + d] = from_f<T>(a.scale * dot);
-    }
+      for (int e = 0; e < (N > W ? N / W : 1); ++e) {
+        const int u = (first + e) / rows, r = (first + e) % rows;
+        if ((whole.value || t + u < n) && j % copies == 0)
+          ((T*)a.o)[((size_t)(s.t0 + t0 + t + u) * a.H + h) * a.dv + d0 + warp * rows * side + lane / W + r * side] =
+              from_f<T>(a.scale * dot[e]);
+      }
+    };
+    int t = 0;
+#pragma unroll 1
+    for (; t + kBatch <= n; t += kBatch) batch(t, std::true_type());
+    if (t < n) batch(t, std::false_type());
   }
 #pragma unroll
-  for (int c = 0; c < 16; ++c) s.out[(size_t)d * DK + j * 16 + c] = st[c];
+  for (int r = 0; r < rows; ++r)
+    *reinterpret_cast<ulonglong2*>(s.out + (size_t)(d0 + own + r * side) * DK + 4 * j) = make_ulonglong2(st[r][0], st[r][1]);
 }
 
 // ---- one token per sequence ---------------------------------------------------------------------------
@@ -98,29 +203,21 @@ __global__ void __launch_bounds__(kThreads) k_linattn_decode(LinAttnArgs a, int 
     const int d1 = d0;
     d0 += kThreads / 32 * rows * side;
     if (d0 < end) load();
-    // halving: after the step over `off` a lane holds the rows whose bit is its own
-    int row = 0;
-    int off = W / 2;
-#pragma unroll
-    for (int n = rows / 2; n >= 1; n /= 2, off /= 2) {
-      const bool upper = (lane & off) != 0;
-#pragma unroll
-      for (int r = 0; r < n; ++r) {
-        const float give = upper ? dot[r] : dot[r + n], keep = upper ? dot[r + n] : dot[r];
-        dot[r] = keep + __shfl_xor_sync(kFull, give, off);
-      }
-      if (upper) row += n;
-    }
-#pragma unroll
-    for (; off >= 1; off /= 2) dot[0] += __shfl_xor_sync(kFull, dot[0], off);
+    int row;
+    halve<rows, W>(dot, lane, &row);
     if (j % (W / rows) == 0) o[d1 + row * side + lane / W] = from_f<T>(a.scale * dot[0]);
   }
 }
 
 template <typename T, int DK>
 cudaError_t steps(const LinAttnArgs& a, cudaStream_t s) {
-  constexpr int R = kThreads / (DK / 16);
-  k_linattn_steps<T, DK><<<dim3(a.nseq, a.H, a.dv / R), kThreads, 0, s>>>(a);
+  constexpr int side = 32 / (DK / 4), one = kStepThreads / 32 * side;   // rows of a CTA per row of a lane
+  // Four rows a lane make most of a token's k and q; two, where that would leave SMs without two CTAs (one row gains nothing:
+  // a token's time is the latency of its chain).
+  if ((long long)a.nseq * a.H * (a.dv / (4 * one)) >= 304)
+    k_linattn_steps<T, DK, 4><<<dim3(a.nseq, a.H, a.dv / (4 * one)), kStepThreads, 0, s>>>(a);
+  else
+    k_linattn_steps<T, DK, 2><<<dim3(a.nseq, a.H, a.dv / (2 * one)), kStepThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -143,7 +240,9 @@ cudaError_t decode(const LinAttnArgs& a, cudaStream_t s) {
 bool linattn_supported(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
 
 cudaError_t linattn_fwd(const LinAttnArgs& a, cudaStream_t s) {
-  if (linattn_tc_supported(a)) return linattn_tc(a, s);
+  // Up to 24 tokens the recurrence is done before a chunk is (one sequence of 32 heads: 8 us against 12 at 24 tokens, 15 against
+  // 12 at 64; of 512 heads 45 against 46 at 24).
+  if (a.max_len > 24 && linattn_tc_supported(a)) return linattn_tc(a, s);
   if (a.io == ERS_DTYPE_BF16)
     return a.dk == 64 ? steps<__nv_bfloat16, 64>(a, s) : steps<__nv_bfloat16, 128>(a, s);
   return a.dk == 64 ? steps<float, 64>(a, s) : steps<float, 128>(a, s);
