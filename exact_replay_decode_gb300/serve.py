@@ -209,7 +209,8 @@ class LinAttnCache:
             table = torch.arange(nslots, dtype=torch.int32, device=state.device).view(nslots, 1)
         else:
             table = torch.full((nslots, 1), -1, dtype=torch.int32, device=state.device)
-        self.pages = PagePool([state], table, None)
+        refs = torch.full((self.npages,), int(npages is None), dtype=torch.int32, device=state.device)
+        self.pages = PagePool([state], table, refs)
         self._c = ctypes.byref(_abi.LinAttnCache(state.data_ptr(), table.data_ptr(), nslots, self.npages))
 
     def nbytes(self) -> int:
