@@ -42,11 +42,12 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 128;                  // tokens of a chunk
-// warps 0-3 make P and own the outputs, 4-7 and 8-11 (two sets) the state; lane quarter: warp % 4.  14 warps: 128 registers
-// each, for with spills every reload would go to L2 (the first-level cache is all shared memory).
+// warps 0-3 make P and own the outputs, 4-7 and 8-11 (two sets) the state, 12 loads and 13 issues, 14 and 15 help with P; lane
+// quarter: warp % 4.  16 warps: 128 registers each, for with spills every reload would go to L2 (the first-level cache is all
+// shared memory).
 constexpr int kStateThread = 128, kStateThreads = 256, kControlThread = 384;
 constexpr int kLoadWarp = 12, kMmaWarp = 13;
-constexpr int kBlock = 448;
+constexpr int kBlock = 512;
 constexpr float kStrong = -1.f;
 constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384, kVStage = 48, kTmemCols = 512;
 constexpr uint32_t kBarState = 1, kBarRows = 2, kBarSet = 3;   // named barriers of the warps of a kind
@@ -80,19 +81,20 @@ struct Shape {
 };
 
 // ---- waits -----------------------------------------------------------------------------------------------
-// Short, and no function call: a call would bind the registers of every caller.
-__device__ __forceinline__ void wait(Hdr& hd, uint64_t* bar, uint32_t parity, int32_t* status) {
+// Short, and no function call: a call would bind the registers of every caller.  False: gave up.
+__device__ __forceinline__ bool wait(Hdr& hd, uint64_t* bar, uint32_t parity, int32_t* status) {
   uint64_t t0 = 0;
 #pragma unroll 1
   while (!mbar_try(bar, parity)) {
     const uint64_t now = globaltimer();
-    if (*(volatile int*)&hd.dead != 0) return;
+    if (*(volatile int*)&hd.dead != 0) return false;
     if (t0 == 0) t0 = now;
     if (now - t0 > kWaitLimitNs) {
       if (status != nullptr) atomicCAS(status, 0, ERS_ETIMEOUT);
       *(volatile int*)&hd.dead = 1;
     }
   }
+  return true;
 }
 __device__ __forceinline__ bool dead(const Hdr& hd) { return *(const volatile int*)&hd.dead != 0; }
 
@@ -142,11 +144,11 @@ __device__ __forceinline__ void arrived(uint32_t (&r)[32]) {
                : "memory");
   asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
-// f(x, values) for the 32-column groups x, x + 32, ... of [0, n)
+// f(x, values) for the 32-column groups x, x + 32, ... of [x0, n)
 template <typename F>
-__device__ __forceinline__ void tmem_each32(uint32_t at, int n, F f) {
+__device__ __forceinline__ void tmem_each32(uint32_t at, int n, F f, int x0 = 0) {
 #pragma unroll 1
-  for (int x = 0; x < n; x += 32) {
+  for (int x = x0; x < n; x += 32) {
     uint32_t r[32];
     tmem_ld32_begin(at + x, r);
     arrived(r);
@@ -271,7 +273,7 @@ struct Cta {
     return Sh::stage > 0 ? tiles + 3 * Sh::ktile + 2 * Sh::vtile : kbuf(m);
   }
   __device__ __forceinline__ int rows(int c) const { return run.len - c * kC < kC ? run.len - c * kC : kC; }
-  __device__ __forceinline__ void wt(uint64_t* bar, uint32_t parity) const { wait(hd, bar, parity & 1u, a.status); }
+  __device__ __forceinline__ bool wt(uint64_t* bar, uint32_t parity) const { return wait(hd, bar, parity & 1u, a.status); }
   // one warp of a kind polls, the others wait for it
   __device__ __forceinline__ void wt_group(int id, uint64_t* bar, uint32_t parity) const {
     if (threadIdx.x % 128 < 32) wt(bar, parity);
@@ -370,9 +372,8 @@ struct Cta {
     uint64_t kd = by_token(kbuf(m));
 #pragma unroll 1
     for (int quarter = 0; quarter < 4; ++quarter, ++quarters, kd += 32 * 128 / 16) {
-      wt(&hd.v_ready[quarters & 1], quarters >> 1);
+      if (!wt(&hd.v_ready[quarters & 1], quarters >> 1)) return false;
       after_sync();
-      if (dead(hd)) return false;
       state_quarter(kd, quarters & 1, accumulate || quarter > 0, leader);
       if (leader) commit(&hd.v_free[quarters & 1]);
     }
@@ -382,7 +383,7 @@ struct Cta {
     const bool leader = elected();
     const int n = run.c1 - run.c0;
     for (int m = 0; m < n; ++m) {
-      wt(&hd.k_full[m & 1], m / 2);
+      if (!wt(&hd.k_full[m & 1], m / 2)) return;
       after_sync();
       if (!state_chunk(m, quarters, m > 0, leader)) return;
       if (leader) {
@@ -401,20 +402,16 @@ struct Cta {
     for (int i = 0; i < run.c1 - run.c0; ++i) {
       const int m = m0 + i;
       const bool with_h = !(fresh && i == 0);
-      wt(&hd.k_full[m & 1], m / 2);
-      wt(&hd.q_full, i);
+      if (!wt(&hd.k_full[m & 1], m / 2) || !wt(&hd.q_full, i)) return;
       after_sync();
-      if (dead(hd)) return;
       chain(tb + kColS, qd, sdesc(smem_u32(kbuf(m)), 16, 1024), kC, kC, DK / 16, id_s, false, leader);
       if (leader) commit(&hd.s_ready);
-      wt(&hd.h_scaled, i);
+      if (!wt(&hd.h_scaled, i)) return;
       after_sync();
       if (!state_chunk(m, quarters, with_h, leader)) return;
       if (leader) commit(&hd.kv_done);
-      if (i > 0) wt(&hd.o_free, i - 1);
-      wt(&hd.h_ready, i);
+      if ((i > 0 && !wt(&hd.o_free, i - 1)) || !wt(&hd.h_ready, i)) return;
       after_sync();
-      if (dead(hd)) return;
       if (with_h) {
 #pragma unroll 1
         for (int term = 0; term < 2; ++term)
@@ -424,10 +421,8 @@ struct Cta {
         commit(&hd.qh_done);
         commit(&hd.q_empty);
       }
-      if (strong) wt(&hd.o_scaled, i);
-      wt(&hd.p_ready, i);
+      if ((strong && !wt(&hd.o_scaled, i)) || !wt(&hd.p_ready, i)) return;
       after_sync();
-      if (dead(hd)) return;
       uint64_t vd = by_token(vbuf(m));
       uint32_t pt = tb + kColS;
 #pragma unroll 1
@@ -452,11 +447,22 @@ struct Cta {
     uint64_t u[16];                                // lambda^-j
 #pragma unroll
     for (int j = 0; j < 16; ++j) u[j] = strong ? 0ull : pair(expf(a_h * (float)(-2 * j)), expf(a_h * (float)(-2 * j - 1)));
+    // The triangle gives quarter q of the rows q + 1 blocks of 32 columns: of the third and the fourth, helpers make what is beyond
+    // two.
+    const int quarter = threadIdx.x / 32 % 4;
+    const bool helper = threadIdx.x >= kControlThread;
+    const int b0 = helper ? 2 : 0, b1 = !helper && quarter > 1 ? 2 : quarter + 1, zeros = !helper && quarter > 1 ? 2 : 4;
     for (int c = run.c0; c < run.c1; ++c) {
       const int i = c - run.c0;
-      wt_group(kBarRows, &hd.s_ready, i);
-      scores(u);
+      if (helper) {
+        wt(&hd.s_ready, i);
+        after_sync();
+      } else {
+        wt_group(kBarRows, &hd.s_ready, i);
+      }
+      scores(u, b0, b1, zeros);
       mbar_arrive(&hd.p_ready);
+      if (helper) continue;
       if (strong) {
         wt_group(kBarRows, &hd.qh_done, i);
         if (!(fresh && i == 0)) scale_rows();
@@ -472,10 +478,11 @@ struct Cta {
   // Columns [16 b, 16 b + 16) of S become the hi terms of P in the first 8 columns of the block and the lo terms in the others.
   // The weights lambda^(63-j) are products of u and one factor per 32 columns: loads from shared memory, which the tensor
   // core's operands keep busy, would cost more than the second multiplication.
-  __device__ __forceinline__ void scores(const uint64_t (&u)[16]) const {
-    const int t = threadIdx.x, quarter = t / 32;
+  // Blocks of 32 columns: [b0, b1) from S, [b1, zeros) above the diagonal.
+  __device__ __forceinline__ void scores(const uint64_t (&u)[16], int b0, int b1, int zeros) const {
+    const int t = threadIdx.x % 128, quarter = t / 32;
     const uint32_t at = tb + ((uint32_t)(32 * quarter) << 16) + kColS;
-    tmem_each32(at, 32 * (quarter + 1), [&](int x, uint32_t (&s)[32]) {
+    tmem_each32(at, 32 * b1, [&](int x, uint32_t (&s)[32]) {
       // whole blocks of code for each kind: branches inside would cost more than all of this
       if (strong) {
 #pragma unroll
@@ -500,9 +507,9 @@ struct Cta {
         }
       }
       tmem_st32(at + x, s);
-    });
+    }, 32 * b0);
 #pragma unroll 1
-    for (int x = 32 * (quarter + 1); x < kC; x += 32) {   // above the diagonal
+    for (int x = 32 * b1; x < 32 * zeros; x += 32) {
       const uint32_t zero[32] = {};
       tmem_st32(at + x, zero);
     }
@@ -562,10 +569,10 @@ struct Cta {
   // ---- warps 4-11: V' and the state ------------------------------------------------------------------------------------------------
   // Quarter `quarter` of a chunk's V', its n-th in all: 32 tokens as three terms into tensor memory, 32 rows d per warp.
   // Even quarters are the first set's and go to stage 0, odd ones the second's and stage 1.  The tile's rows are tokens:
-  // ldmatrix turns 8 x 8 blocks of it as tcgen05.st takes them.  nan collects whether anything was not finite.
-  template <bool scaled>
-  __device__ __forceinline__ void make_quarter(const uint8_t* vt, const float* w, float f, int quarter, int n,
-                                               __nv_bfloat162& nan) const {
+  // ldmatrix turns 8 x 8 blocks of it as tcgen05.st takes them.  settle receives NaN where anything was not finite.
+  template <bool scaled, typename F>
+  __device__ __forceinline__ void make_quarter(const uint8_t* vt, const float* w, float f, int quarter, int n, F settle) const {
+    __nv_bfloat162 nan(0.f, 0.f);
     const int lane = threadIdx.x % 32, row = threadIdx.x % 128 & ~31;
     uint64_t w2[4];                                // the weights of tokens 8 b + 2 (lane % 4) + {0, 1}
 #pragma unroll
@@ -593,6 +600,7 @@ struct Cta {
         }
       }
     }
+    settle(nan);
     if (n >= 2) wt_set(&hd.v_free[n & 1], (n >> 1) - 1);   // only now: the terms were made under the stage's last product
     if (row < DV) {
       const uint32_t at = tb + ((uint32_t)row << 16) + kColV + (n & 1) * kVStage;
@@ -683,14 +691,13 @@ struct Cta {
 
   // first pass: weights up to the run's end
   __device__ __forceinline__ void run_values() const {
-    __nv_bfloat162 nan(0.f, 0.f);
     for (int c = run.c0; c < run.c1; ++c) {
       const int m = c - run.c0;
       wt_set(&hd.v_full[m & 1], m / 2);
       const float f = c + 1 < run.c1 ? expf(a_h * (float)((run.c1 - 1 - c) * kC)) : 1.f;
 #pragma unroll 1
       for (int quarter = set(); quarter < 4; quarter += 2) {
-        make_quarter<true>(vbuf(m), hd.w[0], f, quarter, 4 * m + quarter, nan);
+        make_quarter<true>(vbuf(m), hd.w[0], f, quarter, 4 * m + quarter, [](__nv_bfloat162) {});
         mbar_arrive(&hd.v_ready[set()]);
       }
     }
@@ -722,9 +729,8 @@ struct Cta {
           clear_tail(rows(c), kbuf(m), vbuf(m));
         }
       }
-      __nv_bfloat162 nan(0.f, 0.f);
-      make_quarter<false>(vbuf(m), hd.w[last ? 1 : 0], 1.f, quarter, 4 * m + quarter, nan);
-      settle(vbuf(m), i, quarter, nan, first);
+      make_quarter<false>(vbuf(m), hd.w[last ? 1 : 0], 1.f, quarter, 4 * m + quarter,
+                          [&](__nv_bfloat162 nan) { settle(vbuf(m), i, quarter, nan, first); });
       mbar_arrive(&hd.v_ready[set()]);
     }
     wt_set(&hd.kv_done, kv_phase + run.c1 - run.c0 - 1);
@@ -834,7 +840,8 @@ __global__ void __launch_bounds__(kBlock, 1)
                           &hd.v_empty[0], &hd.v_empty[1], &hd.q_full, &hd.q_empty, &hd.s_ready, &hd.qh_done, &hd.o_ready,
                           &hd.kv_done, &hd.v_free[0], &hd.v_free[1]};
     for (uint64_t* b : by_one) mbar_init(b, 1);
-    uint64_t* by_four[] = {&hd.p_ready, &hd.o_scaled, &hd.o_free, &hd.o_staged, &hd.v_ready[0], &hd.v_ready[1]};
+    mbar_init(&hd.p_ready, 192);
+    uint64_t* by_four[] = {&hd.o_scaled, &hd.o_free, &hd.o_staged, &hd.v_ready[0], &hd.v_ready[1]};
     for (uint64_t* b : by_four) mbar_init(b, 128);
     mbar_init(&hd.h_scaled, 256);
     mbar_init(&hd.h_ready, 256);
@@ -876,7 +883,7 @@ __global__ void __launch_bounds__(kBlock, 1)
       if (lane == 0) cta.load_states();
     } else if (warp == kMmaWarp) {
       cta.issue_states(quarters);
-    } else if (tid >= kStateThread) {
+    } else if (tid >= kStateThread && tid < kControlThread) {
       cta.run_values();
       cta.state_out(nullptr, true);
     }
@@ -896,7 +903,7 @@ __global__ void __launch_bounds__(kBlock, 1)
       if (lane == 0) cta.load_chunks(m0);
     } else if (warp == kMmaWarp) {
       cta.issue_chunks(m0, quarters, !given);
-    } else if (tid >= kStateThread) {
+    } else if (tid >= kStateThread && tid < kControlThread) {
       if (given) cta.state_in(seq.in, run.last_run > 0);
       cta.states(m0, kv_phase, !given);
       if (rank == run.last_run && !dead(hd)) cta.state_out(seq.out, false);
