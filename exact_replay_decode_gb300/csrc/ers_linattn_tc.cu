@@ -177,6 +177,11 @@ __device__ __forceinline__ void tma_store_3d(const void* map, const void* src, i
                "r"(y), "r"(z), "r"(smem_u32(src))
                : "memory");
 }
+__device__ __forceinline__ void st_global_32(void* to, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
@@ -297,24 +302,25 @@ struct Cta {
     if (m >= 2) wt(&hd.v_empty[m & 1], m / 2 - 1);
     load(vbuf(m), &maps.v, DV, h, c, &hd.v_full[m & 1]);
   }
-  __device__ __forceinline__ void load_states() const {
-    for (int c = run.c0; c < run.c1; ++c) {
+  // the first two chunks of a pass, numbers m0 and m0 + 1
+  __device__ __forceinline__ void load_head(int m0, bool with_q) const {
+    for (int j = 0; j < 2 && run.c0 + j < run.c1; ++j) {
+      load_k(m0 + j, run.c0 + j);
+      if (j == 0 && with_q) load(qbuf(), &maps.q, DK, g, run.c0, &hd.q_full);
+      load_v(m0 + j, run.c0 + j);
+    }
+  }
+  __device__ __forceinline__ void load_states() const {   // after their head
+    for (int c = run.c0 + 2; c < run.c1; ++c) {
       load_k(c - run.c0, c);
       load_v(c - run.c0, c);
     }
   }
-  // In the order in which buffers come free: Q after Q H^T, V after P V, and K, long done with then, when the output that
-  // takes its place has been stored: it is the tile that is needed last.  (The rows of a short chunk are stored by their
-  // owners.)
+  // After their head, in the order in which buffers come free: Q after Q H^T, V after P V, and K, long done with then, when the
+  // output that takes its place has been stored: it is the tile that is needed last.  (A short chunk's rows are stored by the
+  // warps that made them.)
   __device__ __forceinline__ void load_chunks(int m0) const {
     const int n = run.c1 - run.c0;
-    load_k(m0, run.c0);
-    load(qbuf(), &maps.q, DK, g, run.c0, &hd.q_full);
-    load_v(m0, run.c0);
-    if (n > 1) {
-      load_k(m0 + 1, run.c0 + 1);
-      load_v(m0 + 1, run.c0 + 1);
-    }
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int c = run.c0 + i;
@@ -471,6 +477,10 @@ struct Cta {
       wt_group(kBarRows, &hd.o_ready, i);
       outputs(c, obuf(m0 + i));
       mbar_arrive(&hd.o_free);
+      if (rows(c) < kC) {
+        named_sync(kBarRows, kStateThread);
+        store_rows(c, obuf(m0 + i));
+      }
       if (i > 0) wt_group(kBarRows, &hd.k_empty[(m0 + i - 1) & 1], (m0 + i - 1) / 2);   // the loader has taken the last one
       mbar_arrive(&hd.o_staged);
     }
@@ -550,20 +560,28 @@ struct Cta {
     const uint32_t at = tb + ((uint32_t)(t & ~31) << 16) + kColO;
     const uint64_t factor = both(strong ? a.scale : a.scale * expf(a_h * (float)(t - 63)));
     const bool bad = *reinterpret_cast<const uint64_t*>(hd.bad[i & 1]) != 0;
-    const int live = rows(c);
-    bf16* out = (bf16*)a.o + ((size_t)(run.t0 + c * kC + t) * a.H + h) * DV;
     tmem_each32(at, DV, [&](int x, uint32_t (&o)[32]) {
       if (bad) spoil(o, hd.first_bad[i & 1][0] + x, hd.first_bad[i & 1][1] + x, t);
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
         const uint4 v = make_uint4(round2(mul2(pair(o[j], o[j + 1]), factor)), round2(mul2(pair(o[j + 2], o[j + 3]), factor)),
                                    round2(mul2(pair(o[j + 4], o[j + 5]), factor)), round2(mul2(pair(o[j + 6], o[j + 7]), factor)));
-        if (live == kC) *reinterpret_cast<uint4*>(stage + sw128(kC, t, x + j)) = v;
-        else if (t < live && !dead(hd)) *reinterpret_cast<uint4*>(out + x + j) = v;
+        *reinterpret_cast<uint4*>(stage + sw128(kC, t, x + j)) = v;
       }
     });
     before_sync();
     fence_async_smem();
+  }
+
+  // a short chunk's rows, whole ones by neighbouring lanes
+  __device__ __forceinline__ void store_rows(int c, const uint8_t* stage) const {
+    bf16* out = (bf16*)a.o + ((size_t)(run.t0 + c * kC) * a.H + h) * DV;
+    if (dead(hd)) return;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < rows(c) * (DV / 8); e += kStateThread) {
+      const int r = e / (DV / 8), x = e % (DV / 8) * 8;
+      *reinterpret_cast<uint4*>(out + (size_t)r * a.H * DV + x) = *reinterpret_cast<const uint4*>(stage + sw128(kC, r, x));
+    }
   }
 
   // ---- warps 4-11: V' and the state ------------------------------------------------------------------------------------------------
@@ -764,7 +782,13 @@ struct Cta {
   __device__ __forceinline__ void state_out(float* dst, bool shared) const {
     const int d = threadIdx.x % 128, x0 = set() * (DK / 2);
     if (d >= DV) return;
+    const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;   // whole sectors
     tmem_each32(tb + ((uint32_t)(d & ~31) << 16) + kColH + x0, DK / 2, [&](int x, uint32_t (&s)[32]) {
+      if (!shared && wide) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) st_global_32(dst + (size_t)d * DK + x0 + x + j, s + j);
+        return;
+      }
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
         const uint4 v = make_uint4(s[j], s[j + 1], s[j + 2], s[j + 3]);
@@ -834,8 +858,10 @@ __global__ void __launch_bounds__(kBlock, 1)
     if (tid == 0) report(a.status, ERS_ECUDA);
     return;
   }
+  // Of a split sequence, all runs but the last first form their own end states (K and V only); the cluster joins them.
+  const bool first = run.last_run > 0 && rank < run.last_run;
   if (warp == kMmaWarp) tmem_alloc(&hd.tmem, kTmemCols);
-  if (tid == 0) {
+  if (tid == 32 * kLoadWarp) {
     uint64_t* by_one[] = {&hd.k_full[0], &hd.k_full[1], &hd.k_empty[0], &hd.k_empty[1], &hd.v_full[0], &hd.v_full[1],
                           &hd.v_empty[0], &hd.v_empty[1], &hd.q_full, &hd.q_empty, &hd.s_ready, &hd.qh_done, &hd.o_ready,
                           &hd.kv_done, &hd.v_free[0], &hd.v_free[1]};
@@ -847,6 +873,8 @@ __global__ void __launch_bounds__(kBlock, 1)
     mbar_init(&hd.h_ready, 256);
     fence_mbar_init();
     hd.dead = 0;
+    // the first tiles come while the others set up
+    Cta<DK, DV>{a, maps, hd, base, hop, 0, h, h / (a.H / a.G), a_h, false, run}.load_head(0, !first);
   }
   const int n_last = seq.len - (chunks - 1) * kC;
   if (tid >= 128 && tid < 128 + kC) {
@@ -860,20 +888,16 @@ __global__ void __launch_bounds__(kBlock, 1)
     }
     hd.w[0][j] = j == kC - 1 ? 1.f : expf(a_h * (float)(kC - 1 - j));
     hd.w[1][j] = j >= n_last ? 0.f : j == n_last - 1 ? 1.f : expf(a_h * (float)(n_last - 1 - j));
-  } else if (tid == 32 * kLoadWarp || tid == 32 * kMmaWarp) {           // multiplied once a chunk over the whole sequence: as two floats
-    const int n = tid == 32 * kLoadWarp ? kC : n_last;
-    const double e = exp((double)a_h * n);
-    const float hi = (float)e, lo = (float)(e - (double)hi);
-    (tid == 32 * kLoadWarp ? hd.step_hi : hd.last_hi) = hi;
-    (tid == 32 * kLoadWarp ? hd.step_lo : hd.last_lo) = lo;
+  } else if (tid < 2) {                            // multiplied once a chunk over the whole sequence: as two floats
+    const Decay e = decay_of(a_h * (float)(tid == 0 ? kC : n_last));
+    (tid == 0 ? hd.step_hi : hd.last_hi) = e.hi;
+    (tid == 0 ? hd.step_lo : hd.last_lo) = e.lo;
   }
   before_sync();
   __syncthreads();
   after_sync();
   Cta<DK, DV> cta{a, maps, hd, base, hop, __shfl_sync(kFull, hd.tmem, 0), h, h / (a.H / a.G), a_h, a_h < kStrong, run};
 
-  // Of a split sequence, all runs but the last first form their own end states (K and V only); the cluster joins them.
-  const bool first = run.last_run > 0 && rank < run.last_run;
   int quarters = 0;
   uint32_t kv_phase = 0;
   const int m0 = first ? run.c1 - run.c0 : 0;
@@ -900,7 +924,10 @@ __global__ void __launch_bounds__(kBlock, 1)
   const bool given = run.last_run > 0 ? (rank > 0 || seq.in != nullptr) : seq.in != nullptr;
   if (run.c0 < run.c1) {
     if (warp == kLoadWarp) {
-      if (lane == 0) cta.load_chunks(m0);
+      if (lane == 0) {
+        if (first) cta.load_head(m0, true);
+        cta.load_chunks(m0);
+      }
     } else if (warp == kMmaWarp) {
       cta.issue_chunks(m0, quarters, !given);
     } else if (tid >= kStateThread && tid < kControlThread) {

@@ -44,22 +44,17 @@ __device__ __forceinline__ bool linattn_seq(const LinAttnArgs& a, int i, int h, 
   return err == ERS_OK;
 }
 
-// exp(a) as the sum of two floats.  A recurrence multiplies by it once a token, so the rounding of a single
-// float would add up over the state's whole memory (256 tokens at a = -1/256: a relative error of 4e-6).
+// exp(x) as the sum of two floats, for factors that a state meets once a token (or once a chunk): the rounding of a single
+// float would add up over the state's whole memory (256 tokens at x = -1/256: a relative error of 4e-6).  Near 1, where
+// the memory is long, 1 + expm1(x) is exact to 2^-24 |x|; further off the memory is short, and one float does.
 struct Decay {
   float hi, lo;
   __device__ __forceinline__ float step(float s, float add) const { return fmaf(hi, s, fmaf(lo, s, add)); }
 };
-// Once per CTA, by one thread (64-bit arithmetic is slow here), through shared memory; ends with a barrier.
-__device__ __forceinline__ Decay decay_of(float a) {
-  __shared__ Decay shared;
-  if (threadIdx.x == 0) {
-    const double e = exp((double)a);
-    const float hi = (float)e;
-    shared = {hi, (float)(e - (double)hi)};
-  }
-  __syncthreads();
-  return shared;
+__device__ __forceinline__ Decay decay_of(float x) {
+  if (fabsf(x) > 0.5f) return {expf(x), 0.f};
+  const float m = expm1f(x), hi = __fadd_rn(1.f, m);
+  return {hi, __fsub_rn(m, __fsub_rn(hi, 1.f))};
 }
 
 }  // namespace ers
