@@ -9,8 +9,8 @@
 //   O = Q H'^T + P V     B = H' as hi + lo in shared memory, A = P as hi + lo in tensor memory, over S
 // The decays of a row are taken out of the products: with P[i,j] = S[i,j] lambda^(63-j) and H' = lambda^64 H the row's output is
 // scale lambda^(i-63) O[i], and both products go into one accumulator.  All factors lie within lambda^(+-64), which fp32
-// and bf16 hold down to a = -1 (6e+-27).  Below that (kStrong) P carries lambda^(i-j), H' = H, and the accumulator
-// is multiplied by lambda^(i+1) between the two products.
+// and bf16 hold down to a = -1 (6e+-27; states above 1e-10 keep all their bits there).  Beyond that (kStrong) P carries
+// lambda^(i-j), H' = H, and the accumulator is multiplied by lambda^(i+1) between the two products.
 // Operands made from fp32 values are split so that outputs keep 16 significant bits before their one rounding (a single
 // bf16 term would cost half as much again as that rounding) and states all 24.  The state stays in tensor memory in
 // fp32 from chunk to chunk.
@@ -48,9 +48,10 @@ constexpr int kC = 128;                  // tokens of a chunk
 constexpr int kStateThread = 128, kStateThreads = 256, kControlThread = 384;
 constexpr int kLoadWarp = 12, kMmaWarp = 13;
 constexpr int kBlock = 512;
-constexpr float kStrong = -1.f;
+constexpr float kStrong = 1.f;
+__device__ __forceinline__ bool is_strong(float a) { return !(fabsf(a) <= kStrong); }
 constexpr uint32_t kColS = 0, kColO = 128, kColH = 256, kColV = 384, kVStage = 48, kTmemCols = 512;
-constexpr uint32_t kBarState = 1, kBarRows = 2, kBarSet = 3;   // named barriers of the warps of a kind
+constexpr uint32_t kBarState = 1, kBarRows = 2, kBarSet = 3 /* and 4, 5 */;   // named barriers of the warps of a kind
 
 struct Hdr {
   alignas(16) float w[2][kC];        // lambda^(n-1-j), 0 from n on: a full chunk, the last chunk (read 16 bytes at a time)
@@ -58,6 +59,7 @@ struct Hdr {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, q_empty;   // tile buffers
   uint64_t s_ready, qh_done, o_ready, kv_done, v_free[2];               // completed by the tensor core
   uint64_t p_ready, o_scaled, o_free, o_staged, h_scaled, h_ready, v_ready[2];    // by the warps
+  uint64_t run_full[3], run_empty[3], run_ready[3], run_free[3];       // the first pass's tiles and V'
   uint32_t tmem;
   int dead;                          // a wait gave up: no further wait waits, no copy or MMA is issued
   float step_hi, step_lo;            // lambda^128 as two floats,
@@ -75,6 +77,7 @@ template <int DK, int DV>
 struct Shape {
   static constexpr uint32_t ktile = kC * DK * 2, vtile = kC * DV * 2;
   static constexpr uint32_t hterm = DV * DK * 2;       // one bf16 term of the state operand
+  static constexpr int run_bufs = 2 * hterm >= ktile + vtile ? 3 : 2;   // first pass: a third K and V where the operand will be
   static constexpr uint32_t stage = vtile > ktile ? vtile : 0;   // outputs on their way out: in a K tile where they fit
   static constexpr uint32_t smem = sizeof(Hdr) + 3 * ktile + 2 * vtile + 2 * hterm + stage;
   static_assert(smem <= 227 * 1024, "one CTA's shared memory");
@@ -270,10 +273,12 @@ struct Cta {
   bool strong;
   Run run;
 
-  // Chunks are numbered m = 0, 1, ... over both passes; number m uses K and V buffer m % 2 for the m / 2th time.
+  // A run's chunk m = 0, 1, ... uses K and V buffer m % 2 for the m / 2th time.
   __device__ __forceinline__ uint8_t* kbuf(int m) const { return tiles + (m & 1) * Sh::ktile; }
   __device__ __forceinline__ uint8_t* vbuf(int m) const { return tiles + 2 * Sh::ktile + (m & 1) * Sh::vtile; }
   __device__ __forceinline__ uint8_t* qbuf() const { return tiles + 2 * Sh::ktile + 2 * Sh::vtile; }
+  __device__ __forceinline__ uint8_t* run_k(int b) const { return b < 2 ? kbuf(b) : hop; }
+  __device__ __forceinline__ uint8_t* run_v(int b) const { return b < 2 ? vbuf(b) : hop + Sh::ktile; }
   __device__ __forceinline__ uint8_t* obuf(int m) const {
     return Sh::stage > 0 ? tiles + 3 * Sh::ktile + 2 * Sh::vtile : kbuf(m);
   }
@@ -302,24 +307,34 @@ struct Cta {
     if (m >= 2) wt(&hd.v_empty[m & 1], m / 2 - 1);
     load(vbuf(m), &maps.v, DV, h, c, &hd.v_full[m & 1]);
   }
-  // the first two chunks of a pass, numbers m0 and m0 + 1
-  __device__ __forceinline__ void load_head(int m0, bool with_q) const {
-    for (int j = 0; j < 2 && run.c0 + j < run.c1; ++j) {
-      load_k(m0 + j, run.c0 + j);
-      if (j == 0 && with_q) load(qbuf(), &maps.q, DK, g, run.c0, &hd.q_full);
-      load_v(m0 + j, run.c0 + j);
-    }
+  // first pass: chunk m's K and V
+  __device__ __forceinline__ void load_run(int m) const {
+    const int b = m % Sh::run_bufs, use = m / Sh::run_bufs, z = run.t0 + (run.c0 + m) * kC;
+    if (use > 0) wt(&hd.run_empty[b], use - 1);
+    if (dead(hd)) return;
+    uint64_t* bar = &hd.run_full[b];
+    mbar_arrive_expect_tx(bar, Sh::ktile + Sh::vtile);
+    for (int x = 0; x < DK; x += 64) tma_load_3d(run_k(b) + x / 64 * (kC * 128), &maps.k, x, g, z, bar);
+    for (int x = 0; x < DV; x += 64) tma_load_3d(run_v(b) + x / 64 * (kC * 128), &maps.v, x, h, z, bar);
   }
-  __device__ __forceinline__ void load_states() const {   // after their head
-    for (int c = run.c0 + 2; c < run.c1; ++c) {
-      load_k(c - run.c0, c);
-      load_v(c - run.c0, c);
+  // the first chunks, which need not wait for anything
+  __device__ __forceinline__ void load_run_head() const {
+    for (int m = 0; m < Sh::run_bufs && run.c0 + m < run.c1; ++m) load_run(m);
+  }
+  __device__ __forceinline__ void load_run_rest() const {
+    for (int m = Sh::run_bufs; run.c0 + m < run.c1; ++m) load_run(m);
+  }
+  __device__ __forceinline__ void load_head() const {
+    for (int m = 0; m < 2 && run.c0 + m < run.c1; ++m) {
+      load_k(m, run.c0 + m);
+      if (m == 0) load(qbuf(), &maps.q, DK, g, run.c0, &hd.q_full);
+      load_v(m, run.c0 + m);
     }
   }
   // After their head, in the order in which buffers come free: Q after Q H^T, V after P V, and K, long done with then, when the
   // output that takes its place has been stored: it is the tile that is needed last.  (A short chunk's rows are stored by the
   // warps that made them.)
-  __device__ __forceinline__ void load_chunks(int m0) const {
+  __device__ __forceinline__ void load_chunks() const {
     const int n = run.c1 - run.c0;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
@@ -328,16 +343,16 @@ struct Cta {
         wt(&hd.q_empty, i);
         load(qbuf(), &maps.q, DK, g, c + 1, &hd.q_full);
       }
-      if (i + 2 < n) load_v(m0 + i + 2, c + 2);
+      if (i + 2 < n) load_v(i + 2, c + 2);
       wt(&hd.o_staged, i);
       if (!dead(hd) && rows(c) == kC) {
         for (int x = 0; x < DV; x += 64)
-          tma_store_3d(&maps.o, obuf(m0 + i) + x / 64 * (kC * 128), x, h, run.t0 + c * kC);
+          tma_store_3d(&maps.o, obuf(i) + x / 64 * (kC * 128), x, h, run.t0 + c * kC);
         bulk_commit();
         bulk_wait_read();
       }
-      mbar_arrive(&hd.k_empty[(m0 + i) & 1]);
-      if (i + 2 < n) load_k(m0 + i + 2, c + 2);
+      mbar_arrive(&hd.k_empty[i & 1]);
+      if (i + 2 < n) load_k(i + 2, c + 2);
     }
   }
   // After a wait gave up: no copy or MMA may be left in flight when the CTA ends.
@@ -360,10 +375,9 @@ struct Cta {
       bd += (uint64_t)brows * 8;
     }
   }
-  // one quarter (32 tokens) of H += V'^T K
-  __device__ __forceinline__ void state_quarter(uint64_t kd, uint32_t stage, bool accumulate, bool leader) const {
+  // one quarter (32 tokens) of H += V'^T K, V' from columns `at` on
+  __device__ __forceinline__ void state_quarter(uint64_t kd, uint32_t at, bool accumulate, bool leader) const {
     constexpr uint32_t id = idesc_bf16(128, DK, false, true);
-    uint32_t at = tb + kColV + stage * kVStage;
 #pragma unroll 1
     for (int term = 0; term < 3; ++term, at += 16) {
       if (leader) {
@@ -373,40 +387,36 @@ struct Cta {
     }
   }
   __device__ __forceinline__ uint64_t by_token(const uint8_t* tile) const { return sdesc(smem_u32(tile), kC * 128, 1024); }
-  // the quarters of chunk number m; false: a wait gave up
-  __device__ __forceinline__ bool state_chunk(int m, int& quarters, bool accumulate, bool leader) const {
-    uint64_t kd = by_token(kbuf(m));
-#pragma unroll 1
-    for (int quarter = 0; quarter < 4; ++quarter, ++quarters, kd += 32 * 128 / 16) {
-      if (!wt(&hd.v_ready[quarters & 1], quarters >> 1)) return false;
-      after_sync();
-      state_quarter(kd, quarters & 1, accumulate || quarter > 0, leader);
-      if (leader) commit(&hd.v_free[quarters & 1]);
-    }
-    return true;
-  }
-  __device__ __forceinline__ void issue_states(int& quarters) const {
+  // First pass: the quarters one after the other, by three sets of warps in turn; the outputs' columns hold the third stage.
+  static __device__ __forceinline__ uint32_t run_stage(int s) { return s == 2 ? kColO : kColV + s * kVStage; }
+  __device__ __forceinline__ void issue_states() const {
     const bool leader = elected();
-    const int n = run.c1 - run.c0;
-    for (int m = 0; m < n; ++m) {
-      if (!wt(&hd.k_full[m & 1], m / 2)) return;
-      after_sync();
-      if (!state_chunk(m, quarters, m > 0, leader)) return;
-      if (leader) {
-        commit(&hd.k_empty[m & 1]);
-        commit(&hd.v_empty[m & 1]);
+    int s = 0, use = 0;                            // quarter number = 3 use + s
+#pragma unroll 1
+    for (int m = 0; m < run.c1 - run.c0; ++m) {
+      const int b = m % Sh::run_bufs;
+      if (!wt(&hd.run_full[b], m / Sh::run_bufs)) return;
+      uint64_t kd = by_token(run_k(b));
+#pragma unroll 1
+      for (int quarter = 0; quarter < 4; ++quarter, kd += 32 * 128 / 16) {
+        if (!wt(&hd.run_ready[s], use)) return;
+        after_sync();
+        state_quarter(kd, tb + run_stage(s), m > 0 || quarter > 0, leader);
+        if (leader) commit(&hd.run_free[s]);
+        if (++s == 3) s = 0, ++use;
       }
+      if (leader) commit(&hd.run_empty[b]);
     }
     if (leader) commit(&hd.kv_done);
   }
-  __device__ __forceinline__ void issue_chunks(int m0, int quarters, bool fresh) const {
+  __device__ __forceinline__ void issue_chunks(bool fresh) const {
     constexpr uint32_t id_s = idesc_bf16(128, kC, false, false), id_h = idesc_bf16(128, DV, false, false),
                        id_v = idesc_bf16(128, DV, false, true);
     const uint64_t qd = sdesc(smem_u32(qbuf()), 16, 1024), h_hi = sdesc(smem_u32(hop), 16, 1024);
     const bool leader = elected();
 #pragma unroll 1
     for (int i = 0; i < run.c1 - run.c0; ++i) {
-      const int m = m0 + i;
+      const int m = i;
       const bool with_h = !(fresh && i == 0);
       if (!wt(&hd.k_full[m & 1], m / 2) || !wt(&hd.q_full, i)) return;
       after_sync();
@@ -414,7 +424,14 @@ struct Cta {
       if (leader) commit(&hd.s_ready);
       if (!wt(&hd.h_scaled, i)) return;
       after_sync();
-      if (!state_chunk(m, quarters, with_h, leader)) return;
+      uint64_t ks = by_token(kbuf(m));
+#pragma unroll 1
+      for (int quarter = 0; quarter < 4; ++quarter, ks += 32 * 128 / 16) {   // two in each of the stages
+        if (!wt(&hd.v_ready[quarter & 1], quarter >> 1)) return;
+        after_sync();
+        state_quarter(ks, tb + kColV + (quarter & 1) * kVStage, with_h || quarter > 0, leader);
+        if (leader) commit(&hd.v_free[quarter & 1]);
+      }
       if (leader) commit(&hd.kv_done);
       if ((i > 0 && !wt(&hd.o_free, i - 1)) || !wt(&hd.h_ready, i)) return;
       after_sync();
@@ -449,7 +466,7 @@ struct Cta {
   }
 
   // ---- warps 0-3: P over S, and the outputs, a thread per row ------------------------------------------------------------------
-  __device__ __forceinline__ void rows_of_chunks(int m0, bool fresh) const {
+  __device__ __forceinline__ void rows_of_chunks(bool fresh) const {
     uint64_t u[16];                                // lambda^-j
 #pragma unroll
     for (int j = 0; j < 16; ++j) u[j] = strong ? 0ull : pair(expf(a_h * (float)(-2 * j)), expf(a_h * (float)(-2 * j - 1)));
@@ -475,13 +492,13 @@ struct Cta {
         mbar_arrive(&hd.o_scaled);
       }
       wt_group(kBarRows, &hd.o_ready, i);
-      outputs(c, obuf(m0 + i));
+      outputs(c, obuf(i));
       mbar_arrive(&hd.o_free);
       if (rows(c) < kC) {
         named_sync(kBarRows, kStateThread);
-        store_rows(c, obuf(m0 + i));
+        store_rows(c, obuf(i));
       }
-      if (i > 0) wt_group(kBarRows, &hd.k_empty[(m0 + i - 1) & 1], (m0 + i - 1) / 2);   // the loader has taken the last one
+      if (i > 0) wt_group(kBarRows, &hd.k_empty[(i - 1) & 1], (i - 1) / 2);   // the loader has taken the last one
       mbar_arrive(&hd.o_staged);
     }
   }
@@ -585,11 +602,11 @@ struct Cta {
   }
 
   // ---- warps 4-11: V' and the state ------------------------------------------------------------------------------------------------
-  // Quarter `quarter` of a chunk's V', its n-th in all: 32 tokens as three terms into tensor memory, 32 rows d per warp.
-  // Even quarters are the first set's and go to stage 0, odd ones the second's and stage 1.  The tile's rows are tokens:
-  // ldmatrix turns 8 x 8 blocks of it as tcgen05.st takes them.  settle receives NaN where anything was not finite.
+  // Quarter `quarter` of a chunk's V': 32 tokens as three terms into tensor memory, columns `to` on, 32 rows d per warp.
+  // The tile's rows are tokens: ldmatrix turns 8 x 8 blocks of it as tcgen05.st takes them.  between receives NaN where
+  // anything was not finite, and waits for the columns to be free: only then, for the terms are made under their last product.
   template <bool scaled, typename F>
-  __device__ __forceinline__ void make_quarter(const uint8_t* vt, const float* w, float f, int quarter, int n, F settle) const {
+  __device__ __forceinline__ void make_quarter(const uint8_t* vt, const float* w, float f, int quarter, uint32_t to, F between) const {
     __nv_bfloat162 nan(0.f, 0.f);
     const int lane = threadIdx.x % 32, row = threadIdx.x % 128 & ~31;
     uint64_t w2[4];                                // the weights of tokens 8 b + 2 (lane % 4) + {0, 1}
@@ -618,10 +635,9 @@ struct Cta {
         }
       }
     }
-    settle(nan);
-    if (n >= 2) wt_set(&hd.v_free[n & 1], (n >> 1) - 1);   // only now: the terms were made under the stage's last product
+    between(nan);
     if (row < DV) {
-      const uint32_t at = tb + ((uint32_t)row << 16) + kColV + (n & 1) * kVStage;
+      const uint32_t at = tb + ((uint32_t)row << 16) + to;
 #pragma unroll
       for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -707,21 +723,23 @@ struct Cta {
     mbar_arrive(&hd.h_ready);
   }
 
-  // first pass: weights up to the run's end
-  __device__ __forceinline__ void run_values() const {
+  // First pass, set s of three (warps 4-7, 8-11, 0-3): every third quarter, with weights up to the run's end.
+  __device__ __forceinline__ void run_values(int s) const {
+    int n = s;                                     // quarter number, of which there are 4 a chunk
     for (int c = run.c0; c < run.c1; ++c) {
-      const int m = c - run.c0;
-      wt_set(&hd.v_full[m & 1], m / 2);
+      const int m = c - run.c0, b = m % Sh::run_bufs;
+      wt_group(kBarSet + s, &hd.run_full[b], m / Sh::run_bufs);
       const float f = c + 1 < run.c1 ? expf(a_h * (float)((run.c1 - 1 - c) * kC)) : 1.f;
 #pragma unroll 1
-      for (int quarter = set(); quarter < 4; quarter += 2) {
-        make_quarter<true>(vbuf(m), hd.w[0], f, quarter, 4 * m + quarter, [](__nv_bfloat162) {});
-        mbar_arrive(&hd.v_ready[set()]);
+      for (; n < 4 * (m + 1); n += 3) {
+        make_quarter<true>(run_v(b), hd.w[0], f, n & 3, run_stage(s), [&](__nv_bfloat162) {
+          if (n >= 3) wt_group(kBarSet + s, &hd.run_free[s], n / 3 - 1);
+        });
+        mbar_arrive(&hd.run_ready[s]);
       }
     }
-    wt_set(&hd.kv_done, 0);
   }
-  __device__ __forceinline__ void states(int m0, uint32_t kv_phase, bool fresh) const {
+  __device__ __forceinline__ void states(uint32_t kv_phase, bool fresh) const {
     const int c_end = (run.len + kC - 1) / kC;     // of the sequence
     const int all = 2 * (run.c1 - run.c0);
     int first = kC;
@@ -729,7 +747,7 @@ struct Cta {
     // as much of V' as there is room for is made before the state is there.
 #pragma unroll 1
     for (int n = 0; n < all; ++n) {
-      const int i = n >> 1, quarter = 2 * (n & 1) + set(), c = run.c0 + i, m = m0 + i;
+      const int i = n >> 1, quarter = 2 * (n & 1) + set(), c = run.c0 + i, m = i;
       const bool last = c + 1 == c_end;
       if (n == 0 || (i > 0 && quarter >= 2)) {
         if (i > 0) wt_set(&hd.kv_done, kv_phase + i - 1);
@@ -747,8 +765,10 @@ struct Cta {
           clear_tail(rows(c), kbuf(m), vbuf(m));
         }
       }
-      make_quarter<false>(vbuf(m), hd.w[last ? 1 : 0], 1.f, quarter, 4 * m + quarter,
-                          [&](__nv_bfloat162 nan) { settle(vbuf(m), i, quarter, nan, first); });
+      make_quarter<false>(vbuf(m), hd.w[last ? 1 : 0], 1.f, quarter, kColV + set() * kVStage, [&](__nv_bfloat162 nan) {
+        settle(vbuf(m), i, quarter, nan, first);
+        if (n > 0) wt_set(&hd.v_free[set()], n - 1);
+      });
       mbar_arrive(&hd.v_ready[set()]);
     }
     wt_set(&hd.kv_done, kv_phase + run.c1 - run.c0 - 1);
@@ -802,6 +822,7 @@ struct Cta {
   __device__ __forceinline__ void join(const float* init, int rank, int split) const {
     const int rows_each = DV / split;
     const float f = expf(a_h * (float)(run.per * kC));
+#pragma unroll 2
     for (int e = threadIdx.x; e < rows_each * (DK / 4); e += kBlock) {
       const int d = rank * rows_each + e / (DK / 4), x = e % (DK / 4) * 4;
       const uint32_t at = smem_u32(hop) + cell(d, x);
@@ -833,6 +854,7 @@ __global__ void __launch_bounds__(kBlock, 1)
   using Sh = Shape<DK, DV>;
   const int rank = blockIdx.x % split, unit = blockIdx.x / split;
   const int i = unit / a.H, h = unit % a.H;
+  const float a_h = a.log_decay[h];
   LinAttnSeq seq;
   if (!linattn_seq(a, i, h, &seq)) return;   // the same for every CTA of the cluster
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0), lane = tid % 32;
@@ -841,7 +863,6 @@ __global__ void __launch_bounds__(kBlock, 1)
       for (int e = tid; e < DV * DK; e += kBlock) seq.out[e] = seq.in != nullptr ? seq.in[e] : 0.f;
     return;
   }
-  const float a_h = a.log_decay[h];
   const int chunks = (seq.len + kC - 1) / kC;
   Run run;
   run.t0 = seq.t0;
@@ -864,23 +885,28 @@ __global__ void __launch_bounds__(kBlock, 1)
   if (tid == 32 * kLoadWarp) {
     uint64_t* by_one[] = {&hd.k_full[0], &hd.k_full[1], &hd.k_empty[0], &hd.k_empty[1], &hd.v_full[0], &hd.v_full[1],
                           &hd.v_empty[0], &hd.v_empty[1], &hd.q_full, &hd.q_empty, &hd.s_ready, &hd.qh_done, &hd.o_ready,
-                          &hd.kv_done, &hd.v_free[0], &hd.v_free[1]};
+                          &hd.kv_done, &hd.v_free[0], &hd.v_free[1], &hd.run_free[0], &hd.run_free[1], &hd.run_free[2],
+                          &hd.run_full[0], &hd.run_full[1], &hd.run_full[2], &hd.run_empty[0], &hd.run_empty[1],
+                          &hd.run_empty[2]};
     for (uint64_t* b : by_one) mbar_init(b, 1);
     mbar_init(&hd.p_ready, 192);
-    uint64_t* by_four[] = {&hd.o_scaled, &hd.o_free, &hd.o_staged, &hd.v_ready[0], &hd.v_ready[1]};
+    uint64_t* by_four[] = {&hd.o_scaled, &hd.o_free, &hd.o_staged, &hd.v_ready[0], &hd.v_ready[1],
+                           &hd.run_ready[0], &hd.run_ready[1], &hd.run_ready[2]};
     for (uint64_t* b : by_four) mbar_init(b, 128);
     mbar_init(&hd.h_scaled, 256);
     mbar_init(&hd.h_ready, 256);
     fence_mbar_init();
     hd.dead = 0;
     // the first tiles come while the others set up
-    Cta<DK, DV>{a, maps, hd, base, hop, 0, h, h / (a.H / a.G), a_h, false, run}.load_head(0, !first);
+    const Cta<DK, DV> loader{a, maps, hd, base, hop, 0, h, h / (a.H / a.G), a_h, false, run};
+    if (first) loader.load_run_head();
+    else loader.load_head();
   }
   const int n_last = seq.len - (chunks - 1) * kC;
   if (tid >= 128 && tid < 128 + kC) {
     const int j = tid - 128;
     // lambda^0 = 1 whatever lambda
-    const bool strong = a_h < kStrong;
+    const bool strong = is_strong(a_h);
     hd.power[j] = strong ? (j == 0 ? 1.f : expf(a_h * (float)j)) : expf(a_h * (float)(63 - j));
     if (j == 0) {
       hd.power[kC] = expf(a_h * (float)kC);   // of the strong ones
@@ -896,22 +922,22 @@ __global__ void __launch_bounds__(kBlock, 1)
   before_sync();
   __syncthreads();
   after_sync();
-  Cta<DK, DV> cta{a, maps, hd, base, hop, __shfl_sync(kFull, hd.tmem, 0), h, h / (a.H / a.G), a_h, a_h < kStrong, run};
+  Cta<DK, DV> cta{a, maps, hd, base, hop, __shfl_sync(kFull, hd.tmem, 0), h, h / (a.H / a.G), a_h, is_strong(a_h), run};
 
-  int quarters = 0;
   uint32_t kv_phase = 0;
-  const int m0 = first ? run.c1 - run.c0 : 0;
   if (first) {
     kv_phase = 1;
     if (warp == kLoadWarp) {
-      if (lane == 0) cta.load_states();
+      if (lane == 0) cta.load_run_rest();
     } else if (warp == kMmaWarp) {
-      cta.issue_states(quarters);
-    } else if (tid >= kStateThread && tid < kControlThread) {
-      cta.run_values();
-      cta.state_out(nullptr, true);
+      cta.issue_states();
+    } else if (tid < kControlThread) {
+      cta.run_values(tid < kStateThread ? 2 : cta.set());
+      if (tid >= kStateThread) {
+        cta.wt_set(&hd.kv_done, 0);
+        cta.state_out(nullptr, true);
+      }
     }
-    quarters = 4 * (run.c1 - run.c0);
     __syncwarp();
   }
   if (split > 1) {
@@ -925,17 +951,17 @@ __global__ void __launch_bounds__(kBlock, 1)
   if (run.c0 < run.c1) {
     if (warp == kLoadWarp) {
       if (lane == 0) {
-        if (first) cta.load_head(m0, true);
-        cta.load_chunks(m0);
+        if (first) cta.load_head();
+        cta.load_chunks();
       }
     } else if (warp == kMmaWarp) {
-      cta.issue_chunks(m0, quarters, !given);
+      cta.issue_chunks(!given);
     } else if (tid >= kStateThread && tid < kControlThread) {
       if (given) cta.state_in(seq.in, run.last_run > 0);
-      cta.states(m0, kv_phase, !given);
+      cta.states(kv_phase, !given);
       if (rank == run.last_run && !dead(hd)) cta.state_out(seq.out, false);
     } else {
-      cta.rows_of_chunks(m0, !given);
+      cta.rows_of_chunks(!given);
     }
   }
   __syncwarp();

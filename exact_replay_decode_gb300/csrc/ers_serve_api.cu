@@ -243,7 +243,7 @@ ers_status ers_token_logprobs(int32_t io_dtype, int32_t nrows, int32_t vocab, in
                               const int32_t* target, float scale, int32_t top_k, float* logprob, float* entropy,
                               int32_t* top_id, float* top_logprob, ers_stream_t stream, int32_t* dev_status) {
   if (io_dtype != ERS_DTYPE_F32 && io_dtype != ERS_DTYPE_BF16) return ERS_EDTYPE;
-  if (nrows < 0 || vocab < 1 || row_stride < vocab) return ERS_EINVAL;
+  if (nrows < 0 || vocab < 1 || vocab > 0x7fff0000 || row_stride < vocab) return ERS_EINVAL;
   if (top_k < 0 || top_k > ERS_TOP_MAX || !(scale > 0.f) || !isfinite(scale)) return ERS_EINVAL;
   if (nrows == 0) return ERS_OK;
   const uintptr_t element = io_dtype == ERS_DTYPE_BF16 ? 2 : 4;

@@ -474,7 +474,7 @@ ERS_API ers_status ers_conv1d_update(const ers_conv_dims* dims, int32_t nseq, co
  *
  *   dims: dk and dv in {64, 128}, nheads % ngroups == 0, io_dtype for q, k, v and o; scale multiplies
  *     the fp32 output before its one rounding.
- *   log_decay [H] fp32, <= 0 (-inf: nothing is remembered; a positive value grows without bound).
+ *   log_decay [H] fp32, <= 0 (-inf: nothing is remembered; a positive one lets states grow without bound).
  *   q, k [T, G, dk], v, o [T, H, dv] in the io dtype, T = ntokens (packed by cu_seqlens [nseq+1]) or nseq (decode).
  *   max_seqlen is the length of the longest sequence as the caller knows it (>= 0): it chooses how
  *     the work is split, never what is computed.  A split changes the order of the state's fp32 sums, so the
@@ -488,7 +488,7 @@ ERS_API ers_status ers_conv1d_update(const ers_conv_dims* dims, int32_t nseq, co
  *   a call no slot's own page may be another sequence's own page or read page.  Decode takes one token per sequence.
  * A NaN or infinity in a token reaches that token and later ones of its sequence and no others.
  * Device errors: ERS_ESLOT (slot, or a page outside [0, npages)), ERS_EINVAL (cu_seqlens not ascending within
- *   [0, ntokens]), ERS_ETIMEOUT; the sequence's outputs are then left unwritten. */
+ *   [0, ntokens]): the sequence's outputs are then left unwritten; ERS_ETIMEOUT: they are undefined. */
 typedef struct ers_linattn_dims {
   int32_t nheads;
   int32_t ngroups;
