@@ -12,7 +12,9 @@
 // Logits below kFloor count as kFloor in that pass (-inf times a weight of nothing would be NaN): a row whose maximum is
 // not far above it, or so large that x c would overflow, is read once more and summed with x - m in place of x c - r.
 //
-// What bounds it: 2 (4) bytes a logit from memory; 152 SMs at 6.8 TB/s leave 10.9 issue slots a bf16 logit, of which it takes 6.
+// What bounds it: 2 (4) bytes a logit from memory; 152 SMs at 6.8 TB/s leave 10.9 issue slots a bf16 logit, of
+// which it takes 6.  2048 x 131072: 92 us (86 % of the measured bandwidth) without alternatives, 127 us with 20, of
+// which half goes into noting maxima and half into choosing.
 #include <limits.h>
 #include <math.h>
 #include <string.h>
@@ -25,7 +27,7 @@ namespace ers {
 namespace {
 
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;           // segments a warp has under way
+constexpr int kUnroll = 3;           // segments a warp has under way while it works on as many
 constexpr int kSegs = 2048;          // segment maxima of a CTA
 constexpr int kCandidates = 256;
 constexpr int kMaxSplit = 8;         // CTAs of a row
@@ -254,12 +256,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   float r = r0;
   uint64_t z2 = 0, zu2 = 0;                 // two zeros each
   const uint64_t c2 = pair(c, c);
+  uint4 next[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u)
+    if (s0 + warp + u * kWarps < s1) next[u] = x.get((s0 + warp + u * kWarps) * 32 + lane);
+#pragma unroll 1
   for (int g = s0 + warp; g < s1; g += kWarps * kUnroll) {
     uint4 raw[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int seg = g + u * kWarps;
-      if (seg < s1) raw[u] = x.get(seg * 32 + lane);
+      raw[u] = next[u];
+      const int seg = g + (u + kUnroll) * kWarps;
+      if (seg < s1) next[u] = x.get(seg * 32 + lane);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -385,10 +393,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
       uint4 raw[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) raw[u] = x.get(v + u * kThreads);
-#pragma unroll 1
-      for (int u = 0; u < kUnroll && v + u * kThreads < s1 * 32; ++u) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (v + u * kThreads >= s1 * 32) break;
         float y[n];
-        Vec<T>::unpack(u == 0 ? raw[0] : u == 1 ? raw[1] : u == 2 ? raw[2] : raw[3], y);
+        Vec<T>::unpack(raw[u], y);
 #pragma unroll
         for (int e = 0; e < n; ++e) {
           const float w = (y[e] - top) * c, p = exp2_fast(w);
