@@ -345,7 +345,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
       const int from = max(key_order(bound), nothing + 1);
       for (int i0 = warp; i0 < noted; i0 += kThreads) {   // a lane per noted maximum, warps taking turns
         const int i = i0 + lane * kWarps;
-        unsigned hits = __ballot_sync(kFull, i < noted && sh.seg_max[i] >= from);
+        // (among equals of the bound, only what comes before it)
+        unsigned hits = __ballot_sync(kFull, i < noted && sh.seg_max[i] >= from &&
+                                                 (sh.seg_max[i] > key_order(bound) ||
+                                                  (unsigned)max((s0 + i * group) * 32 * n - x.shift, 0) <= (unsigned)key_index(bound)));
         while (hits != 0) {
           const int first = s0 + (i0 + (__ffs(hits) - 1) * kWarps) * group;
           hits &= hits - 1;
