@@ -1,5 +1,6 @@
 // Linear attention with a decay per head (include/ers.h), a = log_decay[h], lambda = exp(a):
 //   S_t = lambda S_{t-1} + v_t k_t^T  (S [dv x dk], fp32),  o_t = scale S_t q_t
+#include <mutex>
 #include <type_traits>
 
 #include "ers_common.cuh"
@@ -70,18 +71,32 @@ __device__ __forceinline__ void halve(float (&v)[N], int lane, int* first) {
 // fp32 prompts, and bf16 ones too short for chunks.  A warp owns state rows in registers (W = dk / 4 lanes a row, `rows` rows of
 // each lane), so a token costs a row 9 packed instructions and one exchange: no more than the same products in chunks would
 // on these cores, and rounded as the recurrence is.  Its products with q are added up for kBatch tokens at once.  Tokens come
-// through shared memory, kTok at a time, the next ones under way.  Latency: a token takes a warp some 60 cycles, so the
-// rows of a head are spread over as many warps as there are.
-constexpr int kTok = 16, kBatch = 8, kStepThreads = 128;
+// through shared memory, kTok at a time, the next ones under way.  Latency: the rows of a head are spread over as many warps
+// as there are, and a token still takes 43 ns with two rows of 64 a lane, 70 with two of 128 (4096 tokens x 16 heads of
+// 128 x 128, fp32: 285 us, against 365 by tiles of 16 and batches of 8, which wait for an exchange four times as
+// often).  A bf16 prompt that comes here is one tile; 16 x 24 tokens x 32 heads: 42 us.
+constexpr int kStepThreads = 128;
+
+template <typename T, int DK, int rows>
+struct StepTiles {
+  static constexpr int kTok = sizeof(T) == 4 ? (rows == 2 ? 32 : 16) : 24, kBatch = sizeof(T) == 4 ? (rows == 2 ? 32 : 16) : 8;
+  static constexpr int R = kStepThreads / 32 * rows * (32 / (DK / 4));   // rows of a CTA
+  T q[2][kTok][DK];
+  T k[2][kTok][DK];
+  T v[2][kTok][R];
+};
 
 template <typename T, int DK, int rows>
 __global__ void __launch_bounds__(kStepThreads) k_linattn_steps(LinAttnArgs a) {
   constexpr int W = DK / 4, side = 32 / W;                  // rows that a warp holds in one register of its lanes
-  constexpr int R = kStepThreads / 32 * rows * side;        // rows of a CTA
+  using Tiles = StepTiles<T, DK, rows>;
+  constexpr int R = Tiles::R, kTok = Tiles::kTok, kBatch = Tiles::kBatch;
   constexpr int N = kBatch * rows, copies = N < W ? W / N : 1;   // lanes that end up with the same product
-  __shared__ alignas(16) T sq[2][kTok][DK];
-  __shared__ alignas(16) T sk[2][kTok][DK];
-  __shared__ alignas(16) T sv[2][kTok][R];
+  extern __shared__ __align__(16) unsigned char smem[];
+  Tiles& tiles = *reinterpret_cast<Tiles*>(smem);
+  auto& sq = tiles.q;
+  auto& sk = tiles.k;
+  auto& sv = tiles.v;
   const int i = blockIdx.x, h = blockIdx.y, g = h / (a.H / a.G);
   LinAttnSeq s;
   if (!linattn_seq(a, i, h, &s)) return;
@@ -209,16 +224,34 @@ __global__ void __launch_bounds__(kThreads) k_linattn_decode(LinAttnArgs a, int 
   }
 }
 
+template <typename T, int DK, int rows>
+cudaError_t launch_steps(const LinAttnArgs& a, cudaStream_t s) {
+  using Tiles = StepTiles<T, DK, rows>;
+  const auto kernel = k_linattn_steps<T, DK, rows>;
+  if (sizeof(Tiles) > 48 * 1024) {                          // more than a kernel may have without asking: once per device
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Tiles));
+      if (e != cudaSuccess) return e;
+      done[dev] = true;
+    }
+  }
+  kernel<<<dim3(a.nseq, a.H, a.dv / Tiles::R), kStepThreads, sizeof(Tiles), s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, int DK>
 cudaError_t steps(const LinAttnArgs& a, cudaStream_t s) {
-  constexpr int side = 32 / (DK / 4), one = kStepThreads / 32 * side;   // rows of a CTA per row of a lane
   // Four rows a lane make most of a token's k and q; two, where that would leave SMs without two CTAs (one row gains nothing:
   // a token's time is the latency of its chain).
-  if ((long long)a.nseq * a.H * (a.dv / (4 * one)) >= 304)
-    k_linattn_steps<T, DK, 4><<<dim3(a.nseq, a.H, a.dv / (4 * one)), kStepThreads, 0, s>>>(a);
-  else
-    k_linattn_steps<T, DK, 2><<<dim3(a.nseq, a.H, a.dv / (2 * one)), kStepThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  if ((long long)a.nseq * a.H * (a.dv / StepTiles<T, DK, 4>::R) >= 304) return launch_steps<T, DK, 4>(a, s);
+  return launch_steps<T, DK, 2>(a, s);
 }
 
 template <typename T, int DK>
