@@ -4,18 +4,19 @@
 //
 // One pass over the logits.  A thread keeps a running maximum m and, relative to r = m c (c = scale log2 e), the sums of
 // 2^(x c - r) and of that times its exponent, two logits an instruction; threads, and the CTAs of a row's cluster where
-// rows are few, are joined at the end.  For the alternatives the pass notes the maximum of each segment (a warp's 512
-// bytes): the k-th largest of the maxima of 64 disjoint parts is a lower bound of the k-th best logit, so the segments that
-// reach it, about 1.2 k of them, are read again (from L2) and what reaches it is ranked.  Should the candidates overflow, the
-// k-th best of those found is a better bound, and the segments are read once more.
+// rows are few, are joined at the end.  For the alternatives a thread notes the maximum of every turn (kUnroll vectors) in
+// shared memory: the k-th largest of the maxima of 64 disjoint parts is a lower bound of the k-th best logit, so the turns
+// that reach it, about 1.2 k of them, are read again by the threads that noted them and what reaches it is ranked.
+// Should the candidates overflow, the k-th best of those found is a better bound, and the turns are read once more.  (A
+// maximum per warp and segment, the segments then read again by whole warps, cost 130 us where this costs 117.)
 //
 // Logits below kFloor count as kFloor in that pass (-inf times a weight of nothing would be NaN): a row whose maximum is
 // not far above it, or so large that x c would overflow, is read once more and summed with x - m in place of x c - r.
 //
 // What bounds it: 2 (4) bytes a logit from memory; 152 SMs at 6.8 TB/s leave 10.9 issue slots a bf16 logit, of
-// which it takes 6.  2048 x 131072: 92 us (86 % of the measured bandwidth) without alternatives, 127 us with 20, of
-// which half goes into noting maxima and half into choosing.
-#include <limits.h>
+// which it takes 6.  2048 x 131072 bf16: 92 us (86 % of the measured bandwidth) without alternatives, 111 with 5 and 117 with
+// 20 (68 %): the notes, and that a CTA that chooses (reads, counts and ranks in turn) streams nothing meanwhile.  Rows of
+// equals, which overflow the candidates, cost twice a plain row's time (515 x 32000 bf16: 26 us against 15).
 #include <math.h>
 #include <string.h>
 
@@ -27,9 +28,9 @@ namespace ers {
 namespace {
 
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 3;           // segments a warp has under way while it works on as many
-constexpr int kSegs = 2048;          // segment maxima of a CTA
-constexpr int kCandidates = 256;
+constexpr int kUnroll = 3;           // vectors that a thread has under way while it works on as many (2: 102 us, 4: 88 but 124 with 20)
+constexpr int kNotes = 32;           // maxima that a thread notes
+constexpr int kCandidates = 128;     // (256: the same but for rows of equals, 33 us)
 constexpr int kMaxSplit = 8;         // CTAs of a row
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
@@ -86,14 +87,20 @@ template <> struct Vec<float> {
     x[2] = __uint_as_float(r.z);
     x[3] = __uint_as_float(r.w);
   }
-  static __device__ __forceinline__ float top(const uint4& r) {
-    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  template <int N>
+  static __device__ __forceinline__ float top(const uint4 (&r)[N]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[i].x), __uint_as_float(r[i].y)), fmaxf(__uint_as_float(r[i].z), __uint_as_float(r[i].w))));
+    return m;
   }
   // at least kFloor, in pairs
   static __device__ __forceinline__ void raised(const uint4& r, uint64_t (&x)[2]) {
     x[0] = pair(max_nan(__uint_as_float(r.x), kFloor), max_nan(__uint_as_float(r.y), kFloor));
     x[1] = pair(max_nan(__uint_as_float(r.z), kFloor), max_nan(__uint_as_float(r.w), kFloor));
   }
+  static __device__ __forceinline__ float at(const uint4& r, int e) { return __uint_as_float(e < 2 ? e < 1 ? r.x : r.y : e < 3 ? r.z : r.w); }
   static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
@@ -109,8 +116,12 @@ template <> struct Vec<__nv_bfloat16> {
     }
   }
   static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
-  static __device__ __forceinline__ float top(const uint4& r) {
-    const __nv_bfloat162 m = __hmax2(__hmax2(two(r.x), two(r.y)), __hmax2(two(r.z), two(r.w)));
+  template <int N>
+  static __device__ __forceinline__ float top(const uint4 (&r)[N]) {
+    __nv_bfloat162 m = __hmax2(__hmax2(two(r[0].x), two(r[0].y)), __hmax2(two(r[0].z), two(r[0].w)));
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+      m = __hmax2(m, __hmax2(__hmax2(two(r[i].x), two(r[i].y)), __hmax2(two(r[i].z), two(r[i].w))));
     return fmaxf(__low2float(m), __high2float(m));
   }
   static __device__ __forceinline__ void raised(const uint4& r, uint64_t (&x)[4]) {
@@ -122,6 +133,10 @@ template <> struct Vec<__nv_bfloat16> {
       const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
       x[i] = pair(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     }
+  }
+  static __device__ __forceinline__ float at(const uint4& r, int e) {
+    const uint32_t w = e < 4 ? e < 2 ? r.x : r.y : e < 6 ? r.z : r.w;
+    return __uint_as_float(e % 2 == 0 ? w << 16 : w & 0xffff0000u);
   }
   static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {   // of values that are bf16 already
     uint32_t w[4];
@@ -198,7 +213,7 @@ struct Shared {
   Sums all_sums[kMaxSplit], again[kMaxSplit];
   float all_top[kMaxSplit];   // of every CTA
   unsigned long long all_best[kMaxSplit * ERS_TOP_MAX];
-  int seg_max[kSegs];
+  float notes[kNotes][kThreads];   // of each thread
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -242,13 +257,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   const int segs = (x.vectors() + 31) / 32;
   const int per = (segs + split - 1) / split;
   const int s0 = min(rank * per, segs), s1 = min(s0 + per, segs);
-  const int group = (per + kSegs - 1) / kSegs;   // segments behind one noted maximum
-  const int noted = (s1 - s0 + group - 1) / group;
+  // A thread notes the maximum of each of its turns, or of each `group` turns of a long row.
+  constexpr int kTurn = kWarps * kUnroll;        // segments of a turn
+  const int group = (s1 - s0 + kTurn * kNotes - 1) / (kTurn * kNotes);
   const float c = a.scale * kLog2e;
-  if (tops && group > 1) {
-    for (int i = threadIdx.x; i < noted; i += kThreads) sh.seg_max[i] = INT_MIN;
-    __syncthreads();
-  }
 
   // ---- one pass ------------------------------------------------------------------------------------------------------
   const float r0 = kFloor * c;
@@ -257,11 +269,17 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   uint64_t z2 = 0, zu2 = 0;                 // two zeros each
   const uint64_t c2 = pair(c, c);
   uint4 next[kUnroll];
+  int noted = 0, since = 0;                 // the thread's notes, turns in the last one
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u)
-    if (s0 + warp + u * kWarps < s1) next[u] = x.get((s0 + warp + u * kWarps) * 32 + lane);
+  for (int u = 0; u < kUnroll; ++u) {
+    const int seg = s0 + warp + u * kWarps;
+    next[u] = next[0];
+    if (seg < s1) next[u] = x.get(seg * 32 + lane);
+  }
 #pragma unroll 1
-  for (int g = s0 + warp; g < s1; g += kWarps * kUnroll) {
+  for (int g = s0 + warp; g < s1; g += kTurn) {
+    // The vectors of this turn.  Those that the row ends before are the thread's own of an earlier one or of this one, so
+    // they change no maximum but at most a note's, which then sends one reader in vain.
     uint4 raw[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -269,26 +287,30 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
       const int seg = g + (u + kUnroll) * kWarps;
       if (seg < s1) next[u] = x.get(seg * 32 + lane);
     }
+    const float t = Vec<T>::top(raw);
+    if (tops) {
+      if (since == 0) sh.notes[noted++][threadIdx.x] = t;
+      else sh.notes[noted - 1][threadIdx.x] = fmaxf(sh.notes[noted - 1][threadIdx.x], t);
+      if (++since == group) since = 0;
+    }
+    if (t > top) {
+      top = t;
+      const float to = fmaxf(t, kFloor) * c;
+      float za, zb, ua, ub;
+      unpair(z2, za, zb);
+      unpair(zu2, ua, ub);
+      Sums s = {r, za + zb, ua + ub};
+      s.raise(to);
+      r = to;
+      z2 = pair(s.z, 0.f);
+      zu2 = pair(s.zu, 0.f);
+    }
+    const uint64_t r2 = pair(-r, -r);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int seg = g + u * kWarps;
-      if (seg >= s1) break;
-      const float t = Vec<T>::top(raw[u]);
-      if (t > top) {
-        top = t;
-        const float to = fmaxf(t, kFloor) * c;
-        float za, zb, ua, ub;
-        unpair(z2, za, zb);
-        unpair(zu2, ua, ub);
-        Sums s = {r, za + zb, ua + ub};
-        s.raise(to);
-        r = to;
-        z2 = pair(s.z, 0.f);
-        zu2 = pair(s.zu, 0.f);
-      }
+      if (g + u * kWarps >= s1) break;
       uint64_t y[n / 2];
       Vec<T>::raised(raw[u], y);
-      const uint64_t r2 = pair(-r, -r);
 #pragma unroll
       for (int e = 0; e < n / 2; ++e) {
         const uint64_t w = fma2(y[e], c2, r2);
@@ -297,13 +319,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
         const uint64_t p = pair(exp2_fast(wa), exp2_fast(wb));
         z2 = add2(z2, p);
         zu2 = fma2(p, w, zu2);
-      }
-      if (tops) {
-        const int o = __reduce_max_sync(kFull, order_of(t));
-        if (lane == 0) {
-          if (group == 1) sh.seg_max[seg - s0] = o;
-          else atomicMax(&sh.seg_max[(seg - s0) / group], o);
-        }
       }
     }
   }
@@ -343,28 +358,49 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
     unsigned long long bound = (unsigned long long)least << 48;
     for (;;) {
       const int from = max(key_order(bound), nothing + 1);
-      for (int i0 = warp; i0 < noted; i0 += kThreads) {   // a lane per noted maximum, warps taking turns
-        const int i = i0 + lane * kWarps;
+      const float least_of = value_of(from);                  // (a NaN reaches nothing)
+      unsigned hits = 0;                                      // the thread's notes that reach the bound
+#pragma unroll 4
+      for (int i = 0; i < noted; ++i) {
+        const int o = order_of(sh.notes[i][threadIdx.x]);
         // (among equals of the bound, only what comes before it)
-        unsigned hits = __ballot_sync(kFull, i < noted && sh.seg_max[i] >= from &&
-                                                 (sh.seg_max[i] > key_order(bound) ||
-                                                  (unsigned)max((s0 + i * group) * 32 * n - x.shift, 0) <= (unsigned)key_index(bound)));
-        while (hits != 0) {
-          const int first = s0 + (i0 + (__ffs(hits) - 1) * kWarps) * group;
-          hits &= hits - 1;
-          for (int seg = first; seg < min(first + group, s1); ++seg) {
-            if (*(volatile int*)&sh.count > kCandidates) break;   // there will be another time
-            float y[n];
-            Vec<T>::unpack(x.get(seg * 32 + lane), y);
+        const int first = ((s0 + i * group * kTurn + warp) * 32 + lane) * n - x.shift;
+        if (o >= from && (o > key_order(bound) || (unsigned)max(first, 0) <= (unsigned)key_index(bound))) hits |= 1u << i;
+      }
+#pragma unroll 1
+      while (hits != 0) {
+        const int begin = s0 + (__ffs(hits) - 1) * group * kTurn + warp;
+        hits &= hits - 1;
+#pragma unroll 1
+        for (int g = begin; g < min(begin + group * kTurn, s1); g += kTurn) {
+          if (*(volatile int*)&sh.count > kCandidates) break;   // there will be another time
+          uint4 raw[kUnroll];
 #pragma unroll
-            for (int e = 0; e < n; ++e) {
-              const int o = order_of(y[e]);
-              if (o < from || !(y[e] > -INFINITY)) continue;
-              const unsigned long long key = key_of(o, (seg * 32 + lane) * n + e - x.shift);
-              if (key >= bound) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kCandidates) sh.candidates[at] = key;
-              }
+          for (int u = 0; u < kUnroll; ++u)
+            if (g + u * kWarps < s1) raw[u] = x.get((g + u * kWarps) * 32 + lane);
+          unsigned which = 0;                                 // of their logits, those that do
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) {
+            if (g + u * kWarps >= s1) break;
+            float y[n];
+            Vec<T>::unpack(raw[u], y);
+#pragma unroll
+            for (int e = 0; e < n; ++e)
+              if (y[e] >= least_of) which |= 1u << (u * n + e);
+          }
+#pragma unroll 1
+          while (which != 0 && *(volatile int*)&sh.count <= kCandidates) {
+            const int w = __ffs(which) - 1, e = w % n;
+            which &= which - 1;
+            uint4 v = raw[0];
+#pragma unroll
+            for (int u = 1; u < kUnroll; ++u)
+              if (w / n == u) v = raw[u];
+            const unsigned long long key =
+                key_of(order_of(Vec<T>::at(v, e)), ((g + w / n * kWarps) * 32 + lane) * n + e - x.shift);
+            if (key >= bound) {
+              const int at = atomicAdd(&sh.count, 1);
+              if (at < kCandidates) sh.candidates[at] = key;
             }
           }
         }
