@@ -14,7 +14,7 @@
 // not far above it, or so large that x c would overflow, is read once more and summed with x - m in place of x c - r.
 //
 // What bounds it: 2 (4) bytes a logit from memory; 152 SMs at 6.8 TB/s leave 10.9 issue slots a bf16 logit, of
-// which it takes 6.  2048 x 131072 bf16: 92 us (86 % of the measured bandwidth) without alternatives, 111 with 5 and 117 with
+// which it takes 6.  2048 x 131072 bf16: 88 us (90 % of the measured bandwidth) without alternatives, 111 with 5 and 117 with
 // 20 (68 %): the notes, and that a CTA that chooses (reads, counts and ranks in turn) streams nothing meanwhile.  Rows of
 // equals, which overflow the candidates, cost twice a plain row's time (515 x 32000 bf16: 26 us against 15).
 #include <math.h>
@@ -28,7 +28,6 @@ namespace ers {
 namespace {
 
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 3;           // vectors that a thread has under way while it works on as many (2: 102 us, 4: 88 but 124 with 20)
 constexpr int kNotes = 32;           // maxima that a thread notes
 constexpr int kCandidates = 128;     // (256: the same but for rows of equals, 33 us)
 constexpr int kMaxSplit = 8;         // CTAs of a row
@@ -249,6 +248,9 @@ __device__ __forceinline__ Sums join_warps(const Sums* sums) {
 template <typename T, bool tops>
 __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, int split) {
   constexpr int n = Vec<T>::n;
+  // Vectors that a thread has under way while it works on as many (2048 x 131072: 2 take 102 us, 3 92, 4 88; with 20
+  // alternatives 3 take 117 and 4 124).
+  constexpr int kUnroll = tops ? 3 : 4;
   __shared__ Shared sh;
   const int row = blockIdx.x / split, rank = blockIdx.x % split;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
