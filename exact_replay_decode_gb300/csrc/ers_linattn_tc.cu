@@ -15,13 +15,18 @@
 // bf16 term would cost half as much again as that rounding) and states all 24.  The state stays in tensor memory in
 // fp32 from chunk to chunk.
 //
+// Measured (128 x 128, kernel alone): 97 tokens x 32 heads 10.5 us, 2048 x 32 33, 32768 x 32 299 (40 % of the measured
+// bandwidth), 4096 x 128 119 (46 %; tensor pipe 49 % busy).
+//
 // What bounds it: at one CTA per SM a chunk moves 128 KB (2.9 us of an SM's share of the memory), 64 MMAs of 64 cycles
 // and some 2500 issue slots of operand making per scheduler, in one dependent loop through the state.  So the warps are
 // specialised and run side by side, and the MMAs are ordered S, H, O so that each group's work on one product lies under the
 // others: while H accumulates the scores become P and the last chunk's outputs are stored; while O accumulates the state is
 // handed on.  Four warps make P and own the outputs (on warps of their own the outputs made every product slower: more
 // tensor-memory traffic at once), eight make V' and hand the state on, one loads the tiles (TMA; two
-// buffers for K and V, one for Q) and one issues every MMA.
+// buffers for K and V, one for Q), one issues every MMA and two help with P.  A chunk takes some 6500 cycles where the
+// SM's 64 MMAs of 64 cycles would take 4100: under way with the other traffic of shared memory an MMA takes 75 to 115,
+// and 900 cycles pass at hand-overs.
 //
 // A long sequence of few heads is split over the CTAs of a cluster, each a run of chunks: every CTA but the
 // last first forms its run's own end state (K and V only), the cluster turns those into start states through
@@ -984,37 +989,85 @@ bool encode(CUtensorMap* m, const void* base, long long T, int heads, int d) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kSplits = 4;               // 1, 2, 4 and 8 CTAs of a sequence and head
+
 template <int DK, int DV>
-cudaError_t raise_smem() {
+cudaLaunchConfig_t config(cudaLaunchAttribute* attr, long long units, int split, cudaStream_t s) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)(units * split));
+  cfg.blockDim = dim3(kBlock);
+  cfg.dynamicSmemBytes = Shape<DK, DV>::smem;
+  cfg.stream = s;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)split;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// How many clusters of 1, 2, 4 and 8 CTAs the current device runs at once; the first call on it also lets the kernel have its
+// shared memory.
+template <int DK, int DV>
+cudaError_t clusters_at_once(int (&fit)[kSplits]) {
   static std::mutex mu;
   static bool done[64];
+  static int known[64][kSplits];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
-  if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(k_linattn_chunks<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DK, DV>::smem);
-  done[dev] = e == cudaSuccess;
-  return e;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(k_linattn_chunks<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DK, DV>::smem);
+    for (int i = 0; i < kSplits && e == cudaSuccess; ++i) {
+      cudaLaunchAttribute attr;
+      const cudaLaunchConfig_t cfg = config<DK, DV>(&attr, 1, 1 << i, nullptr);
+      e = cudaOccupancyMaxActiveClusters(&known[dev][i], k_linattn_chunks<DK, DV>, &cfg);
+    }
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  memcpy(fit, known[dev], sizeof(fit));
+  return cudaSuccess;
+}
+
+// Over how many CTAs a sequence goes: what takes the least time by a model in quarters of a chunk's time (0.8 us).  A split
+// sequence's chunks cost half as much again (the first pass) and a join 6; clusters that do not fit at once wait for
+// others, and not all that the SMs would hold fit (of 8 CTAs the GPU's clusters of SMs hold few); a short sequence costs 10.
+// Of the lengths only the longest and the sum are known: as many sequences as the sum has longest ones count, the
+// others as short (one of 4096 tokens and 30 of 40 x 32 heads: 113 us by 1 CTA, 162 by 2).  128 x 128, by 1, 2, 4 and 8 CTAs, us:
+//   512 tokens x 32 heads   19.9  21.2   19.8     -     |   2048 x 64   57.1   51.3   64.8  110.8
+//   1024 x 32               32.2  30.2   24.4   51.9    |   2048 x 128  62.1  102.7  126.5  199.4
+//   2048 x 16               55.8  45.7   31.0   43.7    |   8192 x 8   200.2  142.5   79.4   47.8
+//   2048 x 32               56.7  47.0   33.5   64.6    |   8192 x 64  204.7  159.4  169.4  238.6
+int split_of(const LinAttnArgs& a, const int (&fit)[kSplits]) {
+  const long long chunks = (a.max_len + kC - 1) / kC;
+  const long long full = a.max_len > 0 ? (a.ntokens + a.max_len - 1) / a.max_len : 0;
+  int best = 0;
+  long long least = 0;
+  for (int i = 0; i < kSplits && (chunks >> i) >= 1; ++i) {
+    if (fit[i] <= 0) break;
+    const long long run = (chunks + (1 << i) - 1) >> i, waves = (full * a.H + fit[i] - 1) / fit[i];
+    const long long others = (a.nseq > full ? a.nseq - full : 0) * a.H * 10 / fit[i];
+    const long long cost = waves * (i == 0 ? 4 * run : 6 * run + 6) + others;
+    if (i == 0 || cost < least) {
+      least = cost;
+      best = i;
+    }
+  }
+  return 1 << best;
 }
 
 template <int DK, int DV>
-cudaError_t launch(const LinAttnArgs& a, const Maps& maps, int split, cudaStream_t s) {
-  cudaError_t e = raise_smem<DK, DV>();
+cudaError_t launch(const LinAttnArgs& a, const Maps& maps, cudaStream_t s) {
+  int fit[kSplits];
+  const cudaError_t e = clusters_at_once<DK, DV>(fit);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)((long long)a.nseq * a.H * split));
-  cfg.blockDim = dim3(kBlock);
-  cfg.dynamicSmemBytes = Shape<DK, DV>::smem;
-  cfg.stream = s;
+  const int split = split_of(a, fit);
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg = config<DK, DV>(&attr, (long long)a.nseq * a.H, split, s);
   return cudaLaunchKernelEx(&cfg, k_linattn_chunks<DK, DV>, a, maps, split);
 }
 
@@ -1030,12 +1083,8 @@ cudaError_t linattn_tc(const LinAttnArgs& a, cudaStream_t s) {
   if (!encode(&maps.q, a.q, a.ntokens, a.G, a.dk) || !encode(&maps.k, a.k, a.ntokens, a.G, a.dk) ||
       !encode(&maps.v, a.v, a.ntokens, a.H, a.dv) || !encode(&maps.o, a.o, a.ntokens, a.H, a.dv))
     return cudaErrorInvalidValue;
-  // Runs of a sequence: as many as fill the SMs, of two chunks at least.
-  const int chunks = (int)((a.max_len + kC - 1) / kC);
-  int split = 1;
-  while (split < 8 && (long long)a.nseq * a.H * split * 2 <= 152 && chunks >= 4 * split) split *= 2;
-  if (a.dk == 64) return a.dv == 64 ? launch<64, 64>(a, maps, split, s) : launch<64, 128>(a, maps, split, s);
-  return a.dv == 64 ? launch<128, 64>(a, maps, split, s) : launch<128, 128>(a, maps, split, s);
+  if (a.dk == 64) return a.dv == 64 ? launch<64, 64>(a, maps, s) : launch<64, 128>(a, maps, s);
+  return a.dv == 64 ? launch<128, 64>(a, maps, s) : launch<128, 128>(a, maps, s);
 }
 
 }  // namespace ers

@@ -126,6 +126,18 @@ def test_long_prompts_whatever_the_split(lens, H):
     _check(o, fin, q, k, v, decay, lens, init)
 
 
+@pytest.mark.parametrize("lens,H", [([129, 1, 0], 2), ([256], 3), ([385, 640], 20), ([512], 8), ([1025, 3, 0, 128], 16),
+                                    ([1100] + [1] * 12, 8), ([897], 36)], ids=str)
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_runs_of_few_chunks(lens, H, dk, dv):
+    """Sequences cut into runs of one chunk or two, some CTAs of a sequence without any."""
+    q, k, v, decay = _inputs(H, sum(lens), H, 1, dk, dv, BF16)
+    init = torch.randn(len(lens), H, dv, dk, device="cuda", generator=_gen(2)) * 0.3
+    for most in (max(lens), max(lens) + 700):
+        o, fin = _ers().linattn_fwd(q, k, v, decay, _cu(lens), init_state=init, max_seqlen=most)
+        _check(o, fin, q, k, v, decay, lens, init)
+
+
 @pytest.mark.parametrize("io", [BF16, F32], ids=["bf16", "f32"])
 def test_neighbours_do_not_leak(io):
     """A sequence of NaN and infinities between two others touches neither, nor their final states."""
