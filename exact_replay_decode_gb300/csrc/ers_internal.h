@@ -183,6 +183,7 @@ struct LinAttnArgs {
   float scale;
   const float* log_decay;   // [H]
   int nseq, max_len;
+  int len0, len1;           // sequences of len0 to len1 tokens only
   long long ntokens;
   const int32_t* cu;        // prompts: [nseq + 1]
   const void* q;            // [T, G, dk]

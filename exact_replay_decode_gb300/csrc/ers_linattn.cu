@@ -251,7 +251,7 @@ cudaError_t steps(const LinAttnArgs& a, cudaStream_t s) {
   // Four rows a lane make most of a token's k and q (4 x 1024 tokens x 64 heads, fp32: 768 us against 904); two, where
   // that would leave SMs without a CTA (1024 x 16: 73.6 against 77.6; 1024 x 32: 144 against 128).  Of the lengths
   // only the longest and the sum are known: as many sequences as the sum has longest ones count.
-  const long long full = a.max_len > 0 ? (a.ntokens + a.max_len - 1) / a.max_len : 0;
+  const long long full = a.max_len > 0 ? min((a.ntokens + a.max_len - 1) / a.max_len, (long long)a.nseq) : 0;
   if (full * a.H * (a.dv / StepTiles<T, DK, 4>::R) >= 152) return launch_steps<T, DK, 4>(a, s);
   return launch_steps<T, DK, 2>(a, s);
 }
@@ -276,9 +276,22 @@ cudaError_t decode(const LinAttnArgs& a, cudaStream_t s) {
 bool linattn_supported(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
 
 cudaError_t linattn_fwd(const LinAttnArgs& a, cudaStream_t s) {
+  constexpr int kFewTokens = 24, kStepLen = 8;
   // Up to 24 tokens the recurrence is done before a chunk is (one sequence of 32 heads: 8 us against 12 at 24 tokens, 15 against
   // 12 at 64; of 512 heads 45 against 46 at 24).
-  if (a.max_len > 24 && linattn_tc_supported(a)) return linattn_tc(a, s);
+  if (a.max_len > kFewTokens && linattn_tc_supported(a)) {
+    // A prompt or two among many single tokens: the recurrence takes the short sequences, in a launch of its own (32 heads,
+    // 97 tokens and 15 single ones: 21.7 us against 37.9 together, 2048 and 63: 98 against 135, but 97 and three: 13.9 against
+    // 10.9; 2048 and 63 of 20 tokens: 193 against 134).
+    if ((long long)a.nseq * a.H > 304 && a.ntokens - a.max_len <= (long long)kStepLen * (a.nseq - 1)) {
+      LinAttnArgs few = a, many = a;
+      few.len1 = few.max_len = kStepLen;
+      many.len0 = kStepLen + 1;
+      const cudaError_t e = a.dk == 64 ? steps<__nv_bfloat16, 64>(few, s) : steps<__nv_bfloat16, 128>(few, s);
+      return e != cudaSuccess ? e : linattn_tc(many, s);
+    }
+    return linattn_tc(a, s);
+  }
   if (a.io == ERS_DTYPE_BF16)
     return a.dk == 64 ? steps<__nv_bfloat16, 64>(a, s) : steps<__nv_bfloat16, 128>(a, s);
   return a.dk == 64 ? steps<float, 64>(a, s) : steps<float, 128>(a, s);

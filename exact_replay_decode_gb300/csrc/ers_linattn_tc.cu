@@ -1035,23 +1035,25 @@ cudaError_t clusters_at_once(int (&fit)[kSplits]) {
 
 // Over how many CTAs a sequence goes: what takes the least time by a model in quarters of a chunk's time (0.8 us).  A split
 // sequence's chunks cost half as much again (the first pass) and a join 6; clusters that do not fit at once wait for
-// others, and not all that the SMs would hold fit (of 8 CTAs the GPU's clusters of SMs hold few); a short sequence costs 10.
-// Of the lengths only the longest and the sum are known: as many sequences as the sum has longest ones count, the
-// others as short (one of 4096 tokens and 30 of 40 x 32 heads: 113 us by 1 CTA, 162 by 2).  128 x 128, by 1, 2, 4 and 8 CTAs, us:
+// others, and not all that the SMs would hold fit (of 8 CTAs the GPU's clusters of SMs hold few).  Of the lengths only
+// the longest and the sum are known: as many sequences as the sum has longest ones count, the others as short ones, 10
+// each, beside them or after them (2 where this launch leaves short ones out).  128 x 128, by 1, 2, 4 and 8 CTAs, us:
 //   512 tokens x 32 heads   19.9  21.2   19.8     -     |   2048 x 64   57.1   51.3   64.8  110.8
 //   1024 x 32               32.2  30.2   24.4   51.9    |   2048 x 128  62.1  102.7  126.5  199.4
 //   2048 x 16               55.8  45.7   31.0   43.7    |   8192 x 8   200.2  142.5   79.4   47.8
 //   2048 x 32               56.7  47.0   33.5   64.6    |   8192 x 64  204.7  159.4  169.4  238.6
+// 4096 and 30 of 40 tokens x 32 heads: 113, 162; 2048 and three of 1: by 2 47.4, by 4 52.7.
 int split_of(const LinAttnArgs& a, const int (&fit)[kSplits]) {
   const long long chunks = (a.max_len + kC - 1) / kC;
-  const long long full = a.max_len > 0 ? (a.ntokens + a.max_len - 1) / a.max_len : 0;
+  const long long full = min(max((a.ntokens + a.max_len / 2) / max(a.max_len, 1), 1LL), (long long)a.nseq);
+  const long long others = (a.nseq - full) * a.H * (a.len0 > 1 ? 2 : 10);
   int best = 0;
   long long least = 0;
   for (int i = 0; i < kSplits && (chunks >> i) >= 1; ++i) {
     if (fit[i] <= 0) break;
-    const long long run = (chunks + (1 << i) - 1) >> i, waves = (full * a.H + fit[i] - 1) / fit[i];
-    const long long others = (a.nseq > full ? a.nseq - full : 0) * a.H * 10 / fit[i];
-    const long long cost = waves * (i == 0 ? 4 * run : 6 * run + 6) + others;
+    const long long run = (chunks + (1 << i) - 1) >> i, one = i == 0 ? 4 * run : 6 * run + 6;
+    const long long waves = (full * a.H + fit[i] - 1) / fit[i];
+    const long long cost = max(waves * one, (full * a.H * one + others) / fit[i]);
     if (i == 0 || cost < least) {
       least = cost;
       best = i;

@@ -53,6 +53,7 @@ ers::LinAttnArgs linattn_args(const ers_linattn_dims* d, const float* log_decay,
   a.scale = d->scale;
   a.log_decay = log_decay;
   a.nseq = nseq;
+  a.len1 = INT32_MAX;
   a.q = q;
   a.k = k;
   a.v = v;

@@ -13,7 +13,7 @@ struct LinAttnSeq {
 };
 
 // Sequence i, head h.  False (reported by one thread) where an index leads outside the caller's memory:
-// nothing of that sequence may then be touched.
+// nothing of that sequence may then be touched.  False as well where another launch takes the sequence.
 __device__ __forceinline__ bool linattn_seq(const LinAttnArgs& a, int i, int h, LinAttnSeq* s) {
   int32_t err = ERS_OK;
   s->t0 = i;
@@ -41,7 +41,7 @@ __device__ __forceinline__ bool linattn_seq(const LinAttnArgs& a, int i, int h, 
     }
   }
   if (err != ERS_OK && threadIdx.x == 0) report(a.status, err);
-  return err == ERS_OK;
+  return err == ERS_OK && s->len >= a.len0 && s->len <= a.len1;
 }
 
 // exp(x) as the sum of two floats, for factors that a state meets once a token (or once a chunk): the rounding of a single

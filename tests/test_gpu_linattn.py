@@ -138,6 +138,17 @@ def test_runs_of_few_chunks(lens, H, dk, dv):
         _check(o, fin, q, k, v, decay, lens, init)
 
 
+@pytest.mark.parametrize("lens,H", [([1] * 20 + [200] + [0, 3, 8, 9, 1], 16), ([300] + [1] * 70, 5), ([0] * 40 + [25], 8)],
+                         ids=["among", "first", "last"])
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 128)])
+def test_a_prompt_among_single_tokens(lens, H, dk, dv):
+    q, k, v, decay = _inputs(H, sum(lens), H, 1, dk, dv, BF16)
+    init = torch.randn(len(lens), H, dv, dk, device="cuda", generator=_gen(3)) * 0.3
+    for most in (max(lens), max(lens) + 700):
+        o, fin = _ers().linattn_fwd(q, k, v, decay, _cu(lens), init_state=init, max_seqlen=most)
+        _check(o, fin, q, k, v, decay, lens, init)
+
+
 @pytest.mark.parametrize("io", [BF16, F32], ids=["bf16", "f32"])
 def test_neighbours_do_not_leak(io):
     """A sequence of NaN and infinities between two others touches neither, nor their final states."""
