@@ -69,21 +69,30 @@ __device__ __forceinline__ void halve(float (&v)[N], int lane, int* first) {
 
 // ---- the recurrence, token by token -------------------------------------------------------------------
 // fp32 prompts, and bf16 ones too short for chunks.  A warp owns state rows in registers (W = dk / 4 lanes a row, `rows` rows of
-// each lane), so a token costs a row 9 packed instructions and one exchange: no more than the same products in chunks would
-// on these cores, and rounded as the recurrence is.  Its products with q are added up for kBatch tokens at once.  Tokens come
-// through shared memory, kTok at a time, the next ones under way.  Latency: the rows of a head are spread over as many warps
-// as there are, and a token still takes 43 ns with two rows of 64 a lane, 70 with two of 128 (4096 tokens x 16 heads of
-// 128 x 128, fp32: 285 us, against 365 by tiles of 16 and batches of 8, which wait for an exchange four times as
-// often).  A bf16 prompt that comes here is one tile; 16 x 24 tokens x 32 heads: 42 us.
+// each lane).  Its products with q are added up for kBatch tokens at once.  Tokens come through shared memory, kTok at a
+// time, the next ones under way.
+//
+// While |a| <= kLevel the state is not decayed token by token but held at the level of the middle of the tile: with
+// c = kTok / 2, U_j = lambda^(c-1-j) S_j is U_(j-1) + lambda^(c-1-j) v_j k_j^T, an output lambda^(j+1-c) scale U_j q_j, and the
+// next tile starts from lambda^n U.  That is 5 packed instructions a row of a token in place of 9; the factors lie within
+// e^(+-c), and U is rounded as S would be.  (Chunks of products would need no fewer on these cores.)
+//
+// What bounds it: a long prompt of few heads is a chain, 44 ns a token (packed FMAs at half rate, shared-memory reads of k and q
+// by every warp); many heads are packed FMAs.  fp32, 128 x 128: 4096 tokens x 16 heads 233 us, 4 x 1024 x 64 605 us (with
+// the state decayed each token 733).  bf16, 16 x 24 tokens x 32 heads: 37 us.
 constexpr int kStepThreads = 128;
+constexpr float kLevel = 1.f;            // (c of 16 at most: factors within 1.2e-7 .. 8.9e6)
 
 template <typename T, int DK, int rows>
 struct StepTiles {
-  static constexpr int kTok = sizeof(T) == 4 ? (rows == 2 ? 32 : 16) : 24, kBatch = sizeof(T) == 4 ? (rows == 2 ? 32 : 16) : 8;
+  // bf16: all that come here in one tile.  fp32: larger tiles and batches wait less often (4096 tokens x 16 heads by 16 and 16
+  // 317 us, by 32 and 32 277, both of two rows); 32 tokens of four rows at once would not fit the registers.
+  static constexpr int kTok = sizeof(T) == 2 ? 24 : 32, kBatch = sizeof(T) == 2 ? 8 : rows == 2 ? 32 : 16;
   static constexpr int R = kStepThreads / 32 * rows * (32 / (DK / 4));   // rows of a CTA
   T q[2][kTok][DK];
   T k[2][kTok][DK];
   T v[2][kTok][R];
+  float in[kTok], out[kTok];        // factors of the tile's values and of its outputs
 };
 
 template <typename T, int DK, int rows>
@@ -97,12 +106,13 @@ __global__ void __launch_bounds__(kStepThreads) k_linattn_steps(LinAttnArgs a) {
   auto& sq = tiles.q;
   auto& sk = tiles.k;
   auto& sv = tiles.v;
-  const int i = blockIdx.x, h = blockIdx.y, g = h / (a.H / a.G);
+  const int parts = a.dv / R, part = blockIdx.x % parts, unit = blockIdx.x / parts;   // a sequence's CTAs side by side
+  const int i = unit / a.H, h = unit % a.H, g = h / (a.H / a.G);
   LinAttnSeq s;
   if (!linattn_seq(a, i, h, &s)) return;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, j = lane % W;
   const int own = warp * rows * side + lane / W;            // this lane's rows of the CTA: own + r * side
-  const int d0 = blockIdx.z * R;
+  const int d0 = part * R;
   uint64_t st[rows][2];
 #pragma unroll
   for (int r = 0; r < rows; ++r) {
@@ -125,48 +135,76 @@ __global__ void __launch_bounds__(kStepThreads) k_linattn_steps(LinAttnArgs a) {
     static_assert(R % e == 0, "whole copies");
   };
   if (s.len > 0) fetch(0, 0);
-  const Decay lambda = decay_of(a.log_decay[h]);
-  const uint64_t hi = pair(lambda.hi, lambda.hi), lo = pair(lambda.lo, lambda.lo);
-  for (int t0 = 0, b = 0; t0 < s.len; t0 += kTok, b ^= 1) {
-    tc::cp_async_wait_all();
-    __syncthreads();                                        // this tile is there, the other one no longer read
-    if (t0 + kTok < s.len) fetch(t0 + kTok, b ^ 1);
-    const int n = min(kTok, s.len - t0);
-    const auto batch = [&](int t, auto whole) {             // whole: no token of it is missing, so no branch either
-      float dot[N];
+  const float a_h = a.log_decay[h];
+  const bool level = fabsf(a_h) <= kLevel;
+  const Decay lambda = decay_of(a_h), tile_step = decay_of_tokens(a_h, kTok);
+  if (level && threadIdx.x < kTok) {
+    tiles.in[threadIdx.x] = power_of(a_h, kTok / 2 - 1 - (int)threadIdx.x);
+    tiles.out[threadIdx.x] = a.scale * power_of(a_h, (int)threadIdx.x + 1 - kTok / 2);
+  }
+  const auto times = [&](Decay d) {
+    const uint64_t hi = pair(d.hi, d.hi), lo = pair(d.lo, d.lo);
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (whole.value || t + u < n) {
-          uint64_t k2[2], q2[2];
-          load4(&sk[b][t + u][4 * j], k2);
-          load4(&sq[b][t + u][4 * j], q2);
+    for (int r = 0; r < rows; ++r) {
+      st[r][0] = fma2(hi, st[r][0], mul2(lo, st[r][0]));
+      st[r][1] = fma2(hi, st[r][1], mul2(lo, st[r][1]));
+    }
+  };
+  const auto walk = [&](auto is_level) {
+    const uint64_t hi = pair(lambda.hi, lambda.hi), lo = pair(lambda.lo, lambda.lo);
+    for (int t0 = 0, b = 0; t0 < s.len; t0 += kTok, b ^= 1) {
+      tc::cp_async_wait_all();
+      __syncthreads();                                      // this tile is there, the other one no longer read
+      if (t0 + kTok < s.len) fetch(t0 + kTok, b ^ 1);
+      const int n = min(kTok, s.len - t0);
+      const auto batch = [&](int t, auto whole) {           // whole: no token of it is missing, so no branch either
+        float dot[N];
 #pragma unroll
-          for (int r = 0; r < rows; ++r) {
-            const float x = to_f(sv[b][t + u][own + r * side]);
-            const uint64_t v2 = pair(x, x);
-            st[r][0] = fma2(hi, st[r][0], fma2(lo, st[r][0], mul2(v2, k2[0])));
-            st[r][1] = fma2(hi, st[r][1], fma2(lo, st[r][1], mul2(v2, k2[1])));
-            dot[u * rows + r] = sum_of(fma2(st[r][1], q2[1], mul2(st[r][0], q2[0])));
+        for (int u = 0; u < kBatch; ++u) {
+          if (whole.value || t + u < n) {
+            uint64_t k2[2], q2[2];
+            load4(&sk[b][t + u][4 * j], k2);
+            load4(&sq[b][t + u][4 * j], q2);
+#pragma unroll
+            for (int r = 0; r < rows; ++r) {
+              const float x = to_f(sv[b][t + u][own + r * side]) * (is_level.value ? tiles.in[t + u] : 1.f);
+              const uint64_t v2 = pair(x, x);
+              if (is_level.value) {
+                st[r][0] = fma2(v2, k2[0], st[r][0]);
+                st[r][1] = fma2(v2, k2[1], st[r][1]);
+              } else {
+                st[r][0] = fma2(hi, st[r][0], fma2(lo, st[r][0], mul2(v2, k2[0])));
+                st[r][1] = fma2(hi, st[r][1], fma2(lo, st[r][1], mul2(v2, k2[1])));
+              }
+              dot[u * rows + r] = sum_of(fma2(st[r][1], q2[1], mul2(st[r][0], q2[0])));
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < rows; ++r) dot[u * rows + r] = 0.f;
           }
-        } else {
-#pragma unroll
-          for (int r = 0; r < rows; ++r) dot[u * rows + r] = 0.f;
         }
-      }
-      int first;
-      halve<N, W>(dot, lane, &first);
+        int first;
+        halve<N, W>(dot, lane, &first);
 #pragma unroll
-      for (int e = 0; e < (N > W ? N / W : 1); ++e) {
-        const int u = (first + e) / rows, r = (first + e) % rows;
-        if ((whole.value || t + u < n) && j % copies == 0)
-          ((T*)a.o)[((size_t)(s.t0 + t0 + t + u) * a.H + h) * a.dv + d0 + warp * rows * side + lane / W + r * side] =
-              from_f<T>(a.scale * dot[e]);
-      }
-    };
-    int t = 0;
+        for (int e = 0; e < (N > W ? N / W : 1); ++e) {
+          const int u = (first + e) / rows, r = (first + e) % rows;
+          if ((whole.value || t + u < n) && j % copies == 0)
+            ((T*)a.o)[((size_t)(s.t0 + t0 + t + u) * a.H + h) * a.dv + d0 + warp * rows * side + lane / W + r * side] =
+                from_f<T>((is_level.value ? tiles.out[t + u] : a.scale) * dot[e]);
+        }
+      };
+      int t = 0;
 #pragma unroll 1
-    for (; t + kBatch <= n; t += kBatch) batch(t, std::true_type());
-    if (t < n) batch(t, std::false_type());
+      for (; t + kBatch <= n; t += kBatch) batch(t, std::true_type());
+      if (t < n) batch(t, std::false_type());
+      if (is_level.value) times(n == kTok && t0 + n < s.len ? tile_step : decay_of_tokens(a_h, n - kTok / 2));
+    }
+  };
+  if (level) {
+    if (s.len > 0) times(decay_of_tokens(a_h, kTok / 2));
+    walk(std::true_type());
+  } else {
+    walk(std::false_type());
   }
 #pragma unroll
   for (int r = 0; r < rows; ++r)
@@ -224,11 +262,15 @@ __global__ void __launch_bounds__(kThreads) k_linattn_decode(LinAttnArgs a, int 
   }
 }
 
+constexpr int kAlone = 116 * 1024;       // bytes of shared memory with which a CTA is the only one of its SM
+
 template <typename T, int DK, int rows>
-cudaError_t launch_steps(const LinAttnArgs& a, cudaStream_t s) {
+cudaError_t launch_steps(const LinAttnArgs& a, bool alone, cudaStream_t s) {
   using Tiles = StepTiles<T, DK, rows>;
+  static_assert(sizeof(Tiles) <= kAlone, "one size does");
   const auto kernel = k_linattn_steps<T, DK, rows>;
-  if (sizeof(Tiles) > 48 * 1024) {                          // more than a kernel may have without asking: once per device
+  const int smem = alone ? kAlone : (int)sizeof(Tiles);
+  if (smem > 48 * 1024) {                                   // more than a kernel may have without asking: once per device
     static std::mutex mu;
     static bool done[64] = {};
     int dev = 0;
@@ -237,23 +279,31 @@ cudaError_t launch_steps(const LinAttnArgs& a, cudaStream_t s) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Tiles));
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlone);
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
   }
-  kernel<<<dim3(a.nseq, a.H, a.dv / Tiles::R), kStepThreads, sizeof(Tiles), s>>>(a);
+  kernel<<<dim3((unsigned)((long long)a.nseq * a.H * (a.dv / Tiles::R))), kStepThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int DK>
+template <int DK>
 cudaError_t steps(const LinAttnArgs& a, cudaStream_t s) {
-  // Four rows a lane make most of a token's k and q (4 x 1024 tokens x 64 heads, fp32: 768 us against 904); two, where
-  // that would leave SMs without a CTA (1024 x 16: 73.6 against 77.6; 1024 x 32: 144 against 128).  Of the lengths
-  // only the longest and the sum are known: as many sequences as the sum has longest ones count.
-  const long long full = a.max_len > 0 ? min((a.ntokens + a.max_len - 1) / a.max_len, (long long)a.nseq) : 0;
-  if (full * a.H * (a.dv / StepTiles<T, DK, 4>::R) >= 152) return launch_steps<T, DK, 4>(a, s);
-  return launch_steps<T, DK, 2>(a, s);
+  // bf16 prompts are short here: four rows a lane, CTAs side by side (8 tokens x 32 heads, 1, 2 and 4 sequences: 4.6, 5.6, 7.6 us;
+  // two rows 4.8, 6.0, 9.3, and a CTA per SM 6.3, 10.5, 17.0).
+  if (a.io == ERS_DTYPE_BF16) return launch_steps<__nv_bfloat16, DK, 4>(a, false, s);
+  // fp32 ones: a token takes a CTA of two rows a lane 44 ns and one of four 60, alone on their SM; two CTAs beside each
+  // other take 70 and 95, and four of four rows 150.  CTAs may be placed beside others while SMs are idle, so where there
+  // is work for one per SM it is held to that.  Of the lengths only the longest and the sum are known: as many
+  // sequences as the sum has longest ones count.  1024 tokens, 128 x 128, two rows alone / two / four, us:
+  //   x 8 heads   45 /  45 /  61        1024, 300 and 20 x 8      59 / 75 /  62
+  //   x 16        88 /  75 /  61        1025 and 300 x 16 (dk 64) 60 / 80 / 103 (four alone: 71)
+  //   x 24       138 / 104 /  96
+  const long long full = min(max((a.ntokens + a.max_len / 2) / max(a.max_len, 1), 1LL), (long long)a.nseq);
+  const long long ctas2 = (long long)a.H * (a.dv / StepTiles<float, DK, 2>::R), ctas4 = ctas2 / 2;
+  if (full * ctas2 <= 152 && a.ntokens * ctas2 / 152 <= a.max_len + a.max_len / 4) return launch_steps<float, DK, 2>(a, true, s);
+  return launch_steps<float, DK, 4>(a, a.ntokens * ctas4 / 152 <= a.max_len, s);
 }
 
 template <typename T, int DK>
@@ -287,14 +337,12 @@ cudaError_t linattn_fwd(const LinAttnArgs& a, cudaStream_t s) {
       LinAttnArgs few = a, many = a;
       few.len1 = few.max_len = kStepLen;
       many.len0 = kStepLen + 1;
-      const cudaError_t e = a.dk == 64 ? steps<__nv_bfloat16, 64>(few, s) : steps<__nv_bfloat16, 128>(few, s);
+      const cudaError_t e = a.dk == 64 ? steps<64>(few, s) : steps<128>(few, s);
       return e != cudaSuccess ? e : linattn_tc(many, s);
     }
     return linattn_tc(a, s);
   }
-  if (a.io == ERS_DTYPE_BF16)
-    return a.dk == 64 ? steps<__nv_bfloat16, 64>(a, s) : steps<__nv_bfloat16, 128>(a, s);
-  return a.dk == 64 ? steps<float, 64>(a, s) : steps<float, 128>(a, s);
+  return a.dk == 64 ? steps<64>(a, s) : steps<128>(a, s);
 }
 
 cudaError_t linattn_decode(const LinAttnArgs& a, cudaStream_t s) {

@@ -57,4 +57,16 @@ __device__ __forceinline__ Decay decay_of(float x) {
   return {hi, __fsub_rn(m, __fsub_rn(hi, 1.f))};
 }
 
+// exp(a n): of whole n, the product's rounding made good
+__device__ __forceinline__ Decay decay_of_tokens(float a, int n) {
+  const float x = a * (float)n, rest = fmaf(a, (float)n, -x);
+  Decay d = decay_of(x);
+  d.lo = fmaf(d.hi, rest, d.lo);
+  return d;
+}
+__device__ __forceinline__ float power_of(float a, int n) {
+  const Decay d = decay_of_tokens(a, n);
+  return d.hi + d.lo;
+}
+
 }  // namespace ers
