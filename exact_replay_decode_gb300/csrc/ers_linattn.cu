@@ -85,7 +85,7 @@ constexpr float kLevel = 1.f;            // (c of 16 at most: factors within 1.2
 
 template <typename T, int DK, int rows>
 struct StepTiles {
-  // bf16: all that come here in one tile.  fp32: larger tiles and batches wait less often (4096 tokens x 16 heads by 16 and 16
+  // bf16: most that come here in one tile.  fp32: larger tiles and batches wait less often (4096 tokens x 16 heads by 16 and 16
   // 317 us, by 32 and 32 277, both of two rows); 32 tokens of four rows at once would not fit the registers.
   static constexpr int kTok = sizeof(T) == 2 ? 24 : 32, kBatch = sizeof(T) == 2 ? 8 : rows == 2 ? 32 : 16;
   static constexpr int R = kStepThreads / 32 * rows * (32 / (DK / 4));   // rows of a CTA
@@ -95,8 +95,9 @@ struct StepTiles {
   float in[kTok], out[kTok];        // factors of the tile's values and of its outputs
 };
 
-template <typename T, int DK, int rows>
-__global__ void __launch_bounds__(kStepThreads) k_linattn_steps(LinAttnArgs a) {
+template <typename T, int DK, int rows, bool leveled>
+__global__ void __launch_bounds__(kStepThreads, sizeof(T) == 2 ? 8 : 1)   // (bf16: 64 x 32 single tokens 42 us, by six a SM 47)
+    k_linattn_steps(LinAttnArgs a) {
   constexpr int W = DK / 4, side = 32 / W;                  // rows that a warp holds in one register of its lanes
   using Tiles = StepTiles<T, DK, rows>;
   constexpr int R = Tiles::R, kTok = Tiles::kTok, kBatch = Tiles::kBatch;
@@ -136,8 +137,10 @@ __global__ void __launch_bounds__(kStepThreads) k_linattn_steps(LinAttnArgs a) {
   };
   if (s.len > 0) fetch(0, 0);
   const float a_h = a.log_decay[h];
-  const bool level = fabsf(a_h) <= kLevel;
-  const Decay lambda = decay_of(a_h), tile_step = decay_of_tokens(a_h, kTok);
+  const bool level = leveled && fabsf(a_h) <= kLevel;
+  Decay lambda = {}, tile_step = {};
+  if (level) tile_step = decay_of_tokens(a_h, kTok);
+  else lambda = decay_of(a_h);
   if (level && threadIdx.x < kTok) {
     tiles.in[threadIdx.x] = power_of(a_h, kTok / 2 - 1 - (int)threadIdx.x);
     tiles.out[threadIdx.x] = a.scale * power_of(a_h, (int)threadIdx.x + 1 - kTok / 2);
@@ -200,9 +203,9 @@ __global__ void __launch_bounds__(kStepThreads) k_linattn_steps(LinAttnArgs a) {
       if (is_level.value) times(n == kTok && t0 + n < s.len ? tile_step : decay_of_tokens(a_h, n - kTok / 2));
     }
   };
-  if (level) {
+  if (leveled && level) {
     if (s.len > 0) times(decay_of_tokens(a_h, kTok / 2));
-    walk(std::true_type());
+    walk(std::bool_constant<leveled>());
   } else {
     walk(std::false_type());
   }
@@ -264,11 +267,11 @@ __global__ void __launch_bounds__(kThreads) k_linattn_decode(LinAttnArgs a, int 
 
 constexpr int kAlone = 116 * 1024;       // bytes of shared memory with which a CTA is the only one of its SM
 
-template <typename T, int DK, int rows>
+template <typename T, int DK, int rows, bool leveled>
 cudaError_t launch_steps(const LinAttnArgs& a, bool alone, cudaStream_t s) {
   using Tiles = StepTiles<T, DK, rows>;
   static_assert(sizeof(Tiles) <= kAlone, "one size does");
-  const auto kernel = k_linattn_steps<T, DK, rows>;
+  const auto kernel = k_linattn_steps<T, DK, rows, leveled>;
   const int smem = alone ? kAlone : (int)sizeof(Tiles);
   if (smem > 48 * 1024) {                                   // more than a kernel may have without asking: once per device
     static std::mutex mu;
@@ -292,7 +295,10 @@ template <int DK>
 cudaError_t steps(const LinAttnArgs& a, cudaStream_t s) {
   // bf16 prompts are short here: four rows a lane, CTAs side by side (8 tokens x 32 heads, 1, 2 and 4 sequences: 4.6, 5.6, 7.6 us;
   // two rows 4.8, 6.0, 9.3, and a CTA per SM 6.3, 10.5, 17.0).
-  if (a.io == ERS_DTYPE_BF16) return launch_steps<__nv_bfloat16, DK, 4>(a, false, s);
+  // Of the shortest the state is decayed each token (64 sequences x 32 heads: 8 tokens 66 us against 71, 12 tokens
+  // 94 against 95, 24 154 against 139).
+  if (a.io == ERS_DTYPE_BF16)
+    return a.max_len > 12 ? launch_steps<__nv_bfloat16, DK, 4, true>(a, false, s) : launch_steps<__nv_bfloat16, DK, 4, false>(a, false, s);
   // fp32 ones: a token takes a CTA of two rows a lane 44 ns and one of four 60, alone on their SM; two CTAs beside each
   // other take 70 and 95, and four of four rows 150.  CTAs may be placed beside others while SMs are idle, so where there
   // is work for one per SM it is held to that.  Of the lengths only the longest and the sum are known: as many
@@ -302,8 +308,8 @@ cudaError_t steps(const LinAttnArgs& a, cudaStream_t s) {
   //   x 24       138 / 104 /  96
   const long long full = min(max((a.ntokens + a.max_len / 2) / max(a.max_len, 1), 1LL), (long long)a.nseq);
   const long long ctas2 = (long long)a.H * (a.dv / StepTiles<float, DK, 2>::R), ctas4 = ctas2 / 2;
-  if (full * ctas2 <= 152 && a.ntokens * ctas2 / 152 <= a.max_len + a.max_len / 4) return launch_steps<float, DK, 2>(a, true, s);
-  return launch_steps<float, DK, 4>(a, a.ntokens * ctas4 / 152 <= a.max_len, s);
+  if (full * ctas2 <= 152 && a.ntokens * ctas2 / 152 <= a.max_len + a.max_len / 4) return launch_steps<float, DK, 2, true>(a, true, s);
+  return launch_steps<float, DK, 4, true>(a, a.ntokens * ctas4 / 152 <= a.max_len, s);
 }
 
 template <typename T, int DK>
@@ -326,14 +332,16 @@ cudaError_t decode(const LinAttnArgs& a, cudaStream_t s) {
 bool linattn_supported(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
 
 cudaError_t linattn_fwd(const LinAttnArgs& a, cudaStream_t s) {
-  constexpr int kFewTokens = 24, kStepLen = 8;
-  // Up to 24 tokens the recurrence is done before a chunk is (one sequence of 32 heads: 8 us against 12 at 24 tokens, 15 against
-  // 12 at 64; of 512 heads 45 against 46 at 24).
-  if (a.max_len > kFewTokens && linattn_tc_supported(a)) {
+  constexpr int kStepLen = 8;
+  // Of few tokens the recurrence is done before a chunk is, which takes 10.4 us whatever it holds (32 heads: 7.6 us for 40
+  // tokens, 10.0 for 64; 64 heads: 9.6 for 32, 11.2 for 40; 512 heads: 36.8 against 38.0 for 24, 45 against 38 for 32).
+  const long long heads = (long long)a.nseq * a.H;
+  const int few_tokens = heads <= 32 ? 56 : heads <= 64 ? 32 : 24;
+  if (a.max_len > few_tokens && linattn_tc_supported(a)) {
     // A prompt or two among many single tokens: the recurrence takes the short sequences, in a launch of its own (32 heads,
     // 97 tokens and 15 single ones: 21.7 us against 37.9 together, 2048 and 63: 98 against 135, but 97 and three: 13.9 against
     // 10.9; 2048 and 63 of 20 tokens: 193 against 134).
-    if ((long long)a.nseq * a.H > 304 && a.ntokens - a.max_len <= (long long)kStepLen * (a.nseq - 1)) {
+    if (heads > 304 && a.ntokens - a.max_len <= (long long)kStepLen * (a.nseq - 1)) {
       LinAttnArgs few = a, many = a;
       few.len1 = few.max_len = kStepLen;
       many.len0 = kStepLen + 1;

@@ -138,6 +138,26 @@ def test_runs_of_few_chunks(lens, H, dk, dv):
         _check(o, fin, q, k, v, decay, lens, init)
 
 
+@pytest.mark.parametrize("lens,H", [([56], 8), ([31, 57], 4), ([57], 8), ([32, 0, 25], 20), ([33, 1], 20)], ids=str)
+@pytest.mark.parametrize("decays", ["graded", "strong"])
+def test_few_tokens_by_either_form(lens, H, decays):
+    q, k, v, decay = _inputs(H, sum(lens), H, 2, 128, 128, BF16)
+    if decays == "strong":   # either side of -1, where the state is no longer held at a common level
+        decay = torch.linspace(-0.9, -3.0, H, device="cuda")
+    init = torch.randn(len(lens), H, 128, 128, device="cuda", generator=_gen(4)) * 0.3
+    o, fin = _ers().linattn_fwd(q, k, v, decay, _cu(lens), init_state=init, max_seqlen=max(lens))
+    _check(o, fin, q, k, v, decay, lens, init)
+
+
+@pytest.mark.parametrize("lens,H", [([95], 3), ([64, 1, 33], 16), ([200], 40)], ids=str)
+def test_fp32_tiles_at_every_decay(lens, H):
+    q, k, v, decay = _inputs(H, sum(lens), H, 1, 64, 128, F32)
+    decay = -torch.logspace(-4, 0.5, H, device="cuda")
+    init = torch.randn(len(lens), H, 128, 64, device="cuda", generator=_gen(5)) * 0.3
+    o, fin = _ers().linattn_fwd(q, k, v, decay, _cu(lens), init_state=init, max_seqlen=max(lens))
+    _check(o, fin, q, k, v, decay, lens, init)
+
+
 @pytest.mark.parametrize("lens,H", [([1] * 20 + [200] + [0, 3, 8, 9, 1], 16), ([300] + [1] * 70, 5), ([0] * 40 + [25], 8)],
                          ids=["among", "first", "last"])
 @pytest.mark.parametrize("dk,dv", [(64, 128), (128, 128)])
