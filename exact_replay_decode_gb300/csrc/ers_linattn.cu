@@ -77,17 +77,17 @@ __device__ __forceinline__ void halve(float (&v)[N], int lane, int* first) {
 // next tile starts from lambda^n U.  That is 5 packed instructions a row of a token in place of 9; the factors lie within
 // e^(+-c), and U is rounded as S would be.  (Chunks of products would need no fewer on these cores.)
 //
-// What bounds it: a long prompt of few heads is a chain, 44 ns a token (packed FMAs at half rate, shared-memory reads of k and q
-// by every warp); many heads are packed FMAs.  fp32, 128 x 128: 4096 tokens x 16 heads 233 us, 4 x 1024 x 64 605 us (with
-// the state decayed each token 733).  bf16, 16 x 24 tokens x 32 heads: 37 us.
+// What bounds it: a long prompt of few heads is a chain, 44 ns a token; many heads are reads of k and q from shared memory by every
+// warp, and packed FMAs at half rate.  fp32, 128 x 128: 4096 tokens x 16 heads 233 us, 4 x 1024 x 64 547 us.
+// bf16, 16 x 24 tokens x 32 heads: 37 us.
 constexpr int kStepThreads = 128;
 constexpr float kLevel = 1.f;            // (c of 16 at most: factors within 1.2e-7 .. 8.9e6)
 
 template <typename T, int DK, int rows>
 struct StepTiles {
   // bf16: most that come here in one tile.  fp32: larger tiles and batches wait less often (4096 tokens x 16 heads by 16 and 16
-  // 317 us, by 32 and 32 277, both of two rows); 32 tokens of four rows at once would not fit the registers.
-  static constexpr int kTok = sizeof(T) == 2 ? 24 : 32, kBatch = sizeof(T) == 2 ? 8 : rows == 2 ? 32 : 16;
+  // 317 us, by 32 and 32 277, both of two rows); 32 tokens of four rows or 16 of eight at once would not fit the registers.
+  static constexpr int kTok = sizeof(T) == 2 ? 24 : 32, kBatch = sizeof(T) == 2 ? 8 : rows == 2 ? 32 : rows == 4 ? 16 : 8;
   static constexpr int R = kStepThreads / 32 * rows * (32 / (DK / 4));   // rows of a CTA
   T q[2][kTok][DK];
   T k[2][kTok][DK];
@@ -309,6 +309,10 @@ cudaError_t steps(const LinAttnArgs& a, cudaStream_t s) {
   const long long full = min(max((a.ntokens + a.max_len / 2) / max(a.max_len, 1), 1LL), (long long)a.nseq);
   const long long ctas2 = (long long)a.H * (a.dv / StepTiles<float, DK, 2>::R), ctas4 = ctas2 / 2;
   if (full * ctas2 <= 152 && a.ntokens * ctas2 / 152 <= a.max_len + a.max_len / 4) return launch_steps<float, DK, 2, true>(a, true, s);
+  // Many heads are bound by the reads of k and q from shared memory, 79 % of its cycles with four rows, which eight halve (4 x
+  // 1024 x 64 heads: 547 us against 595, 40 x 100 x 16 of 64 values: 75 against 82; 2 x 1024 x 64, whose CTAs are not quite a
+  // wave and a half: 321 against 305).
+  if (a.ntokens * (ctas4 / 2) / 152 >= 5LL * a.max_len) return launch_steps<float, DK, 8, true>(a, false, s);
   return launch_steps<float, DK, 4, true>(a, a.ntokens * ctas4 / 152 <= a.max_len, s);
 }
 

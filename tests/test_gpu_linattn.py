@@ -149,7 +149,7 @@ def test_few_tokens_by_either_form(lens, H, decays):
     _check(o, fin, q, k, v, decay, lens, init)
 
 
-@pytest.mark.parametrize("lens,H", [([95], 3), ([64, 1, 33], 16), ([200], 40)], ids=str)
+@pytest.mark.parametrize("lens,H", [([95], 3), ([64, 1, 33], 16), ([200], 40), ([45, 0] + [40] * 40, 16)], ids=["few", "odd", "heads", "many"])
 def test_fp32_tiles_at_every_decay(lens, H):
     q, k, v, decay = _inputs(H, sum(lens), H, 1, 64, 128, F32)
     decay = -torch.logspace(-4, 0.5, H, device="cuda")
