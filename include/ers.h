@@ -478,7 +478,7 @@ ERS_API ers_status ers_conv1d_update(const ers_conv_dims* dims, int32_t nseq, co
  *   q, k [T, G, dk], v, o [T, H, dv] in the io dtype, T = ntokens (packed by cu_seqlens [nseq+1]) or nseq (decode).
  *   max_seqlen is the length of the longest sequence as the caller knows it (>= 0): it chooses how
  *     the work is split, never what is computed.  A split changes the order of the state's fp32 sums, so the
- *     bits of two calls agree when nseq, max_seqlen and dims agree.
+ *     bits of two calls agree when nseq, ntokens, max_seqlen and dims agree.
  * ers_linattn_fwd: prompts from init_state [nseq, H, dv, dk] (NULL: zeros); final_state [nseq, H, dv, dk] (may be
  *   init_state itself).  An empty sequence's final state is its initial one.
  * ers_linattn_prefill / ers_linattn_decode: the states live in the pages of a pool, cache->state [npages, H,
@@ -487,6 +487,8 @@ ERS_API ers_status ers_conv1d_update(const ers_conv_dims* dims, int32_t nseq, co
  *   page, so a sequence that was forked goes on from its parent's page into its own with no copy in between.  Within
  *   a call no slot's own page may be another sequence's own page or read page.  Decode takes one token per sequence.
  * A NaN or infinity in a token reaches that token and later ones of its sequence and no others.
+ * Range: a prompt's sums are held at levels that differ from the results' by up to exp(64 |a|), |a| <= 1 (bf16), or
+ *   exp(16 |a|) (fp32): products (q.k) v above 1e10 (fp32: 1e31) may overflow to infinity where a is near -1.
  * Device errors: ERS_ESLOT (slot, or a page outside [0, npages)), ERS_EINVAL (cu_seqlens not ascending within
  *   [0, ntokens]): the sequence's outputs are then left unwritten; ERS_ETIMEOUT: they are undefined. */
 typedef struct ers_linattn_dims {
