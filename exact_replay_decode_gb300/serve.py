@@ -217,10 +217,11 @@ class LinAttnCache:
         return sum(t.numel() * t.element_size() for t in (self.state, self.pages.table, self.pages.refs))
 
 
-def _linattn_dims(H: int, G: int, dk: int, dv: int, io: torch.dtype, scale: float) -> _abi.LinAttnDims:
+@functools.lru_cache(maxsize=64)
+def _linattn_dims(H: int, G: int, dk: int, dv: int, io: torch.dtype, scale: float):
     if io not in _IO:
         raise TypeError(f"io dtype {io} not supported (bf16 or fp32)")
-    return _abi.LinAttnDims(H, G, dk, dv, _IO[io], float(scale))
+    return ctypes.byref(_abi.LinAttnDims(H, G, dk, dv, _IO[io], scale))
 
 
 def _qkv(q, k, v, log_decay, io, T, H, G, dk, dv):
@@ -270,7 +271,7 @@ def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
         _out(o, v)
         _tensor(final, torch.float32, "out[1]", state)
     st = _status(status, check, dev)
-    code = _abi.lib().ers_linattn_fwd(ctypes.byref(_linattn_dims(H, G, dk, dv, io, scale)), decay, S, T,
+    code = _abi.lib().ers_linattn_fwd(_linattn_dims(H, G, dk, dv, io, float(scale)), decay, S, T,
                                       T if max_seqlen is None else int(max_seqlen), cu_seqlens.data_ptr(), *qkv,
                                       init, o.data_ptr(), final.data_ptr(), *_where(dev, st))
     _finish(code, "ers_linattn_fwd", st, check)
@@ -301,8 +302,8 @@ def linattn_prefill(cache: LinAttnCache, q, k, v, log_decay, cu_seqlens: Optiona
     decay, qkv = _qkv(q, k, v, log_decay, cache.io, T, cache.H, cache.G, cache.dk, cache.dv)
     o = _out(out, v)
     st = _status(status, check, dev)
-    dims = _linattn_dims(cache.H, cache.G, cache.dk, cache.dv, cache.io, scale)
-    code = _abi.lib().ers_linattn_prefill(ctypes.byref(dims), decay, cache._c, S, T,
+    dims = _linattn_dims(cache.H, cache.G, cache.dk, cache.dv, cache.io, float(scale))
+    code = _abi.lib().ers_linattn_prefill(dims, decay, cache._c, S, T,
                                           T if max_seqlen is None else int(max_seqlen), cu_seqlens.data_ptr(),
                                           _slot(slot, S), _read_arg(read_page, S), *qkv, o.data_ptr(), *_where(dev, st))
     _finish(code, "ers_linattn_prefill", st, check)
@@ -318,8 +319,8 @@ def linattn_decode(cache: LinAttnCache, q, k, v, log_decay, slot: Optional[torch
     decay, qkv = _qkv(q, k, v, log_decay, cache.io, S, cache.H, cache.G, cache.dk, cache.dv)
     o = _out(out, v)
     st = _status(status, check, dev)
-    dims = _linattn_dims(cache.H, cache.G, cache.dk, cache.dv, cache.io, scale)
-    code = _abi.lib().ers_linattn_decode(ctypes.byref(dims), decay, cache._c, S, _slot(slot, S),
+    dims = _linattn_dims(cache.H, cache.G, cache.dk, cache.dv, cache.io, float(scale))
+    code = _abi.lib().ers_linattn_decode(dims, decay, cache._c, S, _slot(slot, S),
                                          _read_arg(read_page, S), *qkv, o.data_ptr(), *_where(dev, st))
     _finish(code, "ers_linattn_decode", st, check)
     return o
