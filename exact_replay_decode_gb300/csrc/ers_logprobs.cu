@@ -215,11 +215,14 @@ struct Shared {
   float notes[kNotes][kThreads];   // of each thread
 };
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 template <typename V>
-__device__ __forceinline__ V* at_cta(V* p, int rank) {   // the same object of the cluster's rank-th CTA
+__device__ __forceinline__ V* at_cta(V* p, int rank) {   // the same object of the cluster's rank-th CTA, which has to be running
   uint64_t r;
   asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
   return reinterpret_cast<V*>(r);
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   __shared__ Shared sh;
   const int row = blockIdx.x / split, rank = blockIdx.x % split;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (split > 1) cluster_arrive();   // this CTA runs: waited for before anything is written to another's shared memory
   const T* x0 = (const T*)a.logits + (long long)row * a.stride;
   const Row<T> x(x0, a.vocab);
   const int segs = (x.vectors() + 31) / 32;
@@ -421,9 +425,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
 
   // ---- the row ---------------------------------------------------------------------------------------------------------
   if (split > 1) {
+    __syncwarp();
+    cluster_wait();
     if (threadIdx.x < split) at_cta(sh.all_top, threadIdx.x)[rank] = top;
     if (threadIdx.x == 0) at_first(sh.all_sums)[rank] = s;
     if (tops && threadIdx.x < a.top_k) at_first(sh.all_best)[rank * a.top_k + threadIdx.x] = sh.best[threadIdx.x];
+    __syncwarp();
     cluster_sync();
     for (int q = 0; q < split; ++q) top = fmaxf(top, sh.all_top[q]);
   }
@@ -455,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
     if (warp == 0) s = join_warps(sh.sums);
     if (split > 1) {
       if (threadIdx.x == 0) at_first(sh.again)[rank] = s;
+      __syncwarp();
       cluster_sync();
     }
   }

@@ -169,6 +169,26 @@ def test_repeats_and_other_streams_give_the_same_bits():
     assert all(torch.equal(a, b) for a, b in zip(one, two))
 
 
+@pytest.mark.parametrize("io", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R", [1, 2, 17, 30])
+def test_rows_split_over_a_cluster(R, io):
+    """Slices of 8 KB, so short that a CTA may be done with its own before another of its row has started: what it hands over
+    waits for that.  Beside a kernel that holds part of the SMs, and over and over, the bits stay."""
+    V = 8 * 8192 // io.itemsize
+    x = (torch.randn(R, V, device="cuda", generator=_gen(R)) * 3).to(io)
+    t = _target(R, V)
+    _check(x, t, 20)
+    one = _ers().token_logprobs(x, t, top_k=20)
+    load = torch.randn(2048, 2048, device="cuda", generator=_gen(1)).to(BF16)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            load @ load
+        again = _ers().token_logprobs(x, t, top_k=20, check=False)
+        assert all(torch.equal(a, b) for a, b in zip(one, again))
+
+
 def test_refusals_and_errors():
     ers = _ers()
     x = torch.zeros(4, 64, dtype=BF16, device="cuda")
