@@ -497,13 +497,19 @@ struct Cta {
         mbar_arrive(&hd.o_scaled);
       }
       wt_group(kBarRows, &hd.o_ready, i);
+      // The last chunk's store has read its staged rows: before they are overwritten where one buffer stages every chunk's, else
+      // before the loader is told of these (its k_empty arrivals stay one a chunk).
+      const auto last_stored = [&] {
+        if (i > 0) wt_group(kBarRows, &hd.k_empty[(i - 1) & 1], (i - 1) / 2);
+      };
+      if (Sh::stage > 0) last_stored();
       outputs(c, obuf(i));
       mbar_arrive(&hd.o_free);
       if (rows(c) < kC) {
         named_sync(kBarRows, kStateThread);
         store_rows(c, obuf(i));
       }
-      if (i > 0) wt_group(kBarRows, &hd.k_empty[(i - 1) & 1], (i - 1) / 2);   // the loader has taken the last one
+      if (Sh::stage == 0) last_stored();
       mbar_arrive(&hd.o_staged);
     }
   }

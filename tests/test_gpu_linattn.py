@@ -138,6 +138,24 @@ def test_runs_of_few_chunks(lens, H, dk, dv):
         _check(o, fin, q, k, v, decay, lens, init)
 
 
+@pytest.mark.parametrize("lens,H,most", [([2048], 160, 2048), ([1000, 2200], 24, 3200), ([1500] * 12, 16, 1500)], ids=str)
+def test_many_chunks_through_one_staging_buffer(lens, H, most):
+    """dk 64, dv 128: outputs do not fit a K tile, so every chunk of a CTA is staged in the same buffer and must wait for the
+    last one's store.  Whole sequences and runs of many chunks, next to traffic that holds stores up; bits stay over repeats."""
+    q, k, v, decay = _inputs(H, sum(lens), H, 1, 64, 128, BF16)
+    init = torch.randn(len(lens), H, 128, 64, device="cuda", generator=_gen(6)) * 0.3
+    cu = _cu(lens)
+    o, fin = _ers().linattn_fwd(q, k, v, decay, cu, init_state=init, max_seqlen=most)
+    _check(o, fin, q, k, v, decay, lens, init)
+    busy, side = torch.empty(1 << 29, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            busy.add_(1)
+        again, fin2 = _ers().linattn_fwd(q, k, v, decay, cu, init_state=init, max_seqlen=most, check=False)
+        assert torch.equal(o, again) and torch.equal(fin, fin2)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("lens,H", [([56], 8), ([31, 57], 4), ([57], 8), ([32, 0, 25], 20), ([33, 1], 20)], ids=str)
 @pytest.mark.parametrize("decays", ["graded", "strong"])
 def test_few_tokens_by_either_form(lens, H, decays):
