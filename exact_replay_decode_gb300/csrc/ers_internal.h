@@ -235,6 +235,7 @@ struct LogprobArgs {
   int io, nrows, vocab, top_k;
   long long stride;
   float scale;
+  float c, floor;           // the launch's own: scale log2 e, and the value that lower logits count as
   const void* logits;
   const int32_t* target;
   float* logprob;

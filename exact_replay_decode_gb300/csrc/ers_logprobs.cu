@@ -10,8 +10,10 @@
 // Should the candidates overflow, the k-th best of those found is a better bound, and the turns are read once more.  (A
 // maximum per warp and segment, the segments then read again by whole warps, cost 130 us where this costs 117.)
 //
-// Logits below kFloor count as kFloor in that pass (-inf times a weight of nothing would be NaN): a row whose maximum is
-// not far above it, or so large that x c would overflow, is read once more and summed with x - m in place of x c - r.
+// x c - r is exact to one rounding while the rounding of r itself, half a unit of |m c|, is a small exponent.  So logits
+// below a floor of -kFar / c count as the floor in that pass (-inf times a weight of nothing would be NaN as well), whatever a
+// thread's own maximum, and a row whose maximum is not far above the floor, or is above kFar / c, is read once more and
+// summed with (x - m) scale in place of x c - r.
 //
 // What bounds it: 2 (4) bytes a logit from memory; 152 SMs at 6.8 TB/s leave 10.9 issue slots a bf16 logit, of
 // which it takes 6.  2048 x 131072 bf16: 88 us (90 % of the measured bandwidth) without alternatives, 111 with 5 and 117 with
@@ -75,7 +77,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // a NaN stays on
   return r;
 }
 
-constexpr float kFloor = -1.2676506e30f;   // -2^100: a bf16 number
+// The largest |x c| of the one pass, and how far a row's maximum has to be above the floor (in exponents: nothing is left of
+// the floor then).
+constexpr float kFar = 1048576.f, kAbove = 256.f;
+constexpr float kMost = 3.4028235e38f, kLowest = -3.3895314e38f;   // the largest float, the lowest bf16 number
 
 template <typename T> struct Vec;   // 16 bytes of logits
 template <> struct Vec<float> {
@@ -94,10 +99,10 @@ template <> struct Vec<float> {
       m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[i].x), __uint_as_float(r[i].y)), fmaxf(__uint_as_float(r[i].z), __uint_as_float(r[i].w))));
     return m;
   }
-  // at least kFloor, in pairs
-  static __device__ __forceinline__ void raised(const uint4& r, uint64_t (&x)[2]) {
-    x[0] = pair(max_nan(__uint_as_float(r.x), kFloor), max_nan(__uint_as_float(r.y), kFloor));
-    x[1] = pair(max_nan(__uint_as_float(r.z), kFloor), max_nan(__uint_as_float(r.w), kFloor));
+  // at least the floor, in pairs
+  static __device__ __forceinline__ void raised(const uint4& r, float floor, uint64_t (&x)[2]) {
+    x[0] = pair(max_nan(__uint_as_float(r.x), floor), max_nan(__uint_as_float(r.y), floor));
+    x[1] = pair(max_nan(__uint_as_float(r.z), floor), max_nan(__uint_as_float(r.w), floor));
   }
   static __device__ __forceinline__ float at(const uint4& r, int e) { return __uint_as_float(e < 2 ? e < 1 ? r.x : r.y : e < 3 ? r.z : r.w); }
   static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
@@ -123,9 +128,9 @@ template <> struct Vec<__nv_bfloat16> {
       m = __hmax2(m, __hmax2(__hmax2(two(r[i].x), two(r[i].y)), __hmax2(two(r[i].z), two(r[i].w))));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ void raised(const uint4& r, uint64_t (&x)[4]) {
+  static __device__ __forceinline__ void raised(const uint4& r, float floor, uint64_t (&x)[4]) {   // (floor: a bf16 number)
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    const __nv_bfloat162 least = __floats2bfloat162_rn(kFloor, kFloor);
+    const __nv_bfloat162 least = __float2bfloat162_rn(floor);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 v = __hmax2_nan(two(w[i]), least);
@@ -180,7 +185,7 @@ struct Row {
   __device__ __forceinline__ uint4 get(int v) const { return whole(v) ? load(v) : edge(v); }
 };
 
-// z = sum 2^(u) and zu = sum 2^(u) u, u = x c - r (or, of the rows that are read again, (x - m) c with r = 0)
+// z = sum 2^(u) and zu = sum 2^(u) u, u = x c - r (or, of the rows that are read again, (x - m) scale log2 e with r = 0)
 struct Sums {
   float r, z, zu;
   __device__ __forceinline__ void raise(float to) {
@@ -266,10 +271,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   // A thread notes the maximum of each of its turns, or of each `group` turns of a long row.
   constexpr int kTurn = kWarps * kUnroll;        // segments of a turn
   const int group = (s1 - s0 + kTurn * kNotes - 1) / (kTurn * kNotes);
-  const float c = a.scale * kLog2e;
+  const float c = a.c, floor = a.floor;
 
   // ---- one pass ------------------------------------------------------------------------------------------------------
-  const float r0 = kFloor * c;
+  const float r0 = floor * c;
   float top = -INFINITY;                    // the thread's maximum
   float r = r0;
   uint64_t z2 = 0, zu2 = 0;                 // two zeros each
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
     }
     if (t > top) {
       top = t;
-      const float to = fmaxf(t, kFloor) * c;
+      const float to = fmaxf(t, floor) * c;
       float za, zb, ua, ub;
       unpair(z2, za, zb);
       unpair(zu2, ua, ub);
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
     for (int u = 0; u < kUnroll; ++u) {
       if (g + u * kWarps >= s1) break;
       uint64_t y[n / 2];
-      Vec<T>::raised(raw[u], y);
+      Vec<T>::raised(raw[u], floor, y);
 #pragma unroll
       for (int e = 0; e < n / 2; ++e) {
         const uint64_t w = fma2(y[e], c2, r2);
@@ -434,7 +439,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
     cluster_sync();
     for (int q = 0; q < split; ++q) top = fmaxf(top, sh.all_top[q]);
   }
-  const bool again = fabsf(top) >= 1e29f && fabsf(top) < INFINITY;
+  const float most_c = top * c;
+  const bool again = fabsf(top) < INFINITY && !(fabsf(most_c) < kFar && most_c - r0 >= kAbove && a.scale * kLog2e <= kMost);
+  // (x - m) scale, the difference halved where scale < 1 would bring one that overflows back
+  const float half = a.scale < 1.f ? 0.5f : 1.f, by = a.scale / half, half_top = half * top;
   if (again) {
     s = {0.f, 0.f, 0.f};
     for (int v = s0 * 32 + threadIdx.x; v < s1 * 32; v += kThreads * kUnroll) {
@@ -448,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
         Vec<T>::unpack(raw[u], y);
 #pragma unroll
         for (int e = 0; e < n; ++e) {
-          const float w = (y[e] - top) * c, p = exp2_fast(w);
+          const float w = fmaf(y[e], half, -half_top) * by * kLog2e, p = exp2_fast(w);
           s.z += p;
           if (!(p == 0.f)) s.zu = fmaf(p, w, s.zu);
         }
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   const bool none = !(s.z < INFINITY) || top == INFINITY, empty = top == -INFINITY && !none;
   // r is the maximum's x c but for its rounding
   const float log_z = logf(s.z), most = (again ? 0.f : fmaf(top, c, -s.r) * kLn2) - log_z;
-  const auto logprob = [&](float v) { return fmaf(v - top, a.scale, most); };
+  const auto logprob = [&](float v) { return fmaf(fmaf(v, half, -half_top), by, most); };
   if (threadIdx.x == 0) {
     if (a.logprob != nullptr) {
       const int t = a.target[row];
@@ -524,7 +532,10 @@ cudaError_t launch(const LogprobArgs& a, int split, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t token_logprobs(const LogprobArgs& a, cudaStream_t s) {
+cudaError_t token_logprobs(const LogprobArgs& args, cudaStream_t s) {
+  LogprobArgs a = args;
+  a.c = fminf(a.scale * kLog2e, kMost);
+  a.floor = __bfloat162float(__float2bfloat16_rn(fmaxf(-kFar / a.c, kLowest)));
   // A row is split while that leaves SMs without two CTAs, down to 8 KB a CTA.  131072 bf16 logits, 8 alternatives: 1 row 16.2 us
   // whole, 10.1 split; 100 rows by up to 152, 304 and 608 CTAs 15.5, 15.1, 20.3; 200 rows 21.2, 18.7, 23.3; 300 rows
   // 22.4, 23.3, 31.0.  8192 logits: 6.5 by one CTA or two.

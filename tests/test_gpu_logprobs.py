@@ -129,6 +129,60 @@ def test_masks_and_rows_that_are_left_nothing(io, V):
         _check(x, t, 32, scale)
 
 
+@pytest.mark.parametrize("io", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [100, 5003, 131072])
+def test_finite_values_of_any_size(io, V):
+    """Rows under an additive mask of any usual size, at the front (whole turns of threads see nothing else), at the end and
+    scattered; even rows, and rows around a large value, of either sign and any size."""
+    g = _gen(V)
+    noise = (torch.randn(V, device="cuda", generator=g) * 3).to(io)
+    scattered = torch.rand(V, device="cuda", generator=g) < 0.99
+    scattered[V // 2] = False
+    rows = []
+    for size in (1e5, 1e6, 1e9, 2.1e9, 1e10, 1e12, 1e15, 1e20, 1e25, 1e29, 1e30, 1e35):
+        for mask in (slice(None, V - 3), slice(3, None), scattered):
+            rows.append(noise.clone())
+            rows[-1][mask] = -size
+            rows.append(noise.clone())
+            rows[-1][mask] -= size
+        for value in (-size, size):
+            rows.append(torch.full_like(noise, value))
+            rows.append(torch.full_like(noise, value))
+            rows[-1][V // 2] *= 1 + 2.0 ** -7            # one step of a bf16 away
+            rows.append((torch.full_like(noise, value).float() * (1 + noise.float() * 1e-7)).to(io))
+            rows[-1][1] = -math.inf
+    x = torch.stack(rows)
+    for R in (len(rows), 5, 1):                          # whole rows, and rows split over a cluster
+        for r in range(0, len(rows), R):
+            _check(x[r:r + R].contiguous(), _target(len(rows), V)[r:r + R].clone(), 20)
+
+
+@pytest.mark.parametrize("io", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [7, 5003, 131072])
+@pytest.mark.parametrize("power", [-149, -130, -120, -96, -40, -10, 10, 21, 27, 28, 60, 100, 127])
+def test_any_scale(io, V, power):
+    """Inverse temperatures (powers of two, exact in fp32) from the least float to the largest."""
+    low, high = torch.finfo(io).min, torch.finfo(io).max
+    x = (torch.randn(12, V, device="cuda", generator=_gen(power + 200)) * 3).to(io)
+    x[1, : V // 2] = -math.inf
+    x[2, 1:] = -math.inf
+    x[3] = -math.inf
+    x[4, ::2] = low
+    x[5, ::3] = high
+    x[5, 1] = low
+    x[6] = 0.0
+    x[7] *= 2.0 ** 100
+    x[8] *= 2.0 ** -100
+    x[8, 0] = -math.inf
+    x[9, V // 2] = math.nan
+    x[10] = x[10] * 2.0 ** -120
+    x[10, 3:] = low
+    x[11, ::2] = -1e9
+    t = _target(12, V)
+    _check(x, t, 7, 2.0 ** power)
+    _check(x[:4].contiguous(), t[:4].clone(), 7, 2.0 ** power)
+
+
 @pytest.mark.parametrize("V", [5000, 131072])
 def test_ties_and_orders(V):
     """Few distinct values, ascending and descending rows, and the best alternatives side by side."""
