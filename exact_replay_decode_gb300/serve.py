@@ -66,7 +66,8 @@ class PagePool:
         if refs is None:
             held = table.flatten()
             refs = torch.zeros(npages + 1, dtype=torch.int32, device=table.device)
-            refs.index_add_(0, torch.where(held < 0, npages, held).long(), torch.ones_like(held))
+            named = (held >= 0) & (held < npages)   # others name no page (the calls report what is out of range)
+            refs.index_add_(0, torch.where(named, held, npages).long(), torch.ones_like(held))
             refs = refs[:-1].contiguous()
         _need(refs, torch.int32, "refs", (npages,))
         for k, x in enumerate(self.arrays):

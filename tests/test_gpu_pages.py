@@ -201,6 +201,19 @@ def test_refusals():
         ers.ReplayCache(1, 4, 1, 64, 128, 16).page_pool()
 
 
+def test_counting_a_table_that_names_pages_out_of_range():
+    """The pool counts what is in range; the calls report the rest."""
+    ers = _ers()
+    x, st = torch.zeros(4, 8, device="cuda"), ers.Status("cuda")
+    pool = ers.PagePool([x], _ints([[2, 4], [-5, 2], [1, 2**31 - 1], [-1, -(2**31)]]))
+    assert pool.refs.tolist() == [0, 1, 2, 0]
+    for slot in range(4):
+        st.reset()
+        ers.pages_free(pool, _ints([slot]), status=st, check=False)
+        assert st.read() == 8
+    assert pool.refs.tolist() == [0, 1, 2, 0]
+
+
 def test_many_slots():
     """A table larger than the default shared memory's bitmap."""
     n = 600_000
