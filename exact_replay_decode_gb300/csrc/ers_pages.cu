@@ -14,6 +14,7 @@ namespace ers {
 namespace {
 
 constexpr int kPlan = 1024;   // threads of a deciding CTA
+static_assert(ERS_PAGES_MAX <= 0x7fffffff - kPlan + 1, "its loops go one step past the last entry or page");
 // CTAs that move bytes: two full waves of eight per SM.  By 1216, 2432, 4864 and 9728: 128 pages of 2 MB 80.9, 80.4, 78.8, 78.5
 // us; a compaction with nothing to move 4.8, 6.0, 8.4, 13.3.
 constexpr int kMovers = 2432;

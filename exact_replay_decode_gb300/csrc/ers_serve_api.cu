@@ -80,7 +80,8 @@ ers_status check_pool(const ers_page_pool* p, int32_t n, bool counted) {
   }
   if (!counted) return ERS_OK;
   if (p->nslots < 0 || p->nslots > ERS_PAGE_SLOTS_MAX || p->slot_pages < 1) return ERS_ESHAPE;
-  if ((int64_t)p->nslots * p->slot_pages > 0x7fffffff || n > p->nslots) return ERS_EINVAL;
+  // the deciding CTA counts in steps of 1024 in 32 bits
+  if ((int64_t)p->nslots * p->slot_pages > ERS_PAGES_MAX || p->npages > ERS_PAGES_MAX || n > p->nslots) return ERS_EINVAL;
   ERS_TRY(check_ptr(p->table, p->nslots > 0));
   return check_ptr(p->refs, p->npages > 0);
 }

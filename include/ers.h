@@ -528,7 +528,8 @@ ERS_API ers_status ers_linattn_decode(const ers_linattn_dims* dims, const float*
  *
  *   table [nslots, slot_pages] int32: the pages of a slot, -1 where it has none; refs [npages] int32: how many
  *   table entries name a page (0: free); array[k]: npages pages of page_bytes[k] bytes each (a multiple of 2), for
- *   k < narrays.  One page index addresses all arrays.  nslots <= ERS_PAGE_SLOTS_MAX.
+ *   k < narrays.  One page index addresses all arrays.  nslots <= ERS_PAGE_SLOTS_MAX; npages and nslots * slot_pages
+ *   <= ERS_PAGES_MAX (ers_pages_copy: any npages).
  * Every call but ers_pages_copy is decided on the device in list order, whole or not at all: a call that finds an
  *   error changes nothing and reports it.  Slots within one list are distinct (ERS_EINVAL).
  * ers_pages_fork: row dst[i] of the table (all -1 before) takes the pages of row src[i]; src may repeat, a slot is
@@ -548,6 +549,7 @@ ERS_API ers_status ers_linattn_decode(const ers_linattn_dims* dims, const float*
  * Device errors: ERS_ESLOT (slot, or a page outside [0, npages)), ERS_EINVAL, ERS_EOVERFLOW. */
 #define ERS_PAGE_ARRAYS_MAX 12
 #define ERS_PAGE_SLOTS_MAX (1 << 20)
+#define ERS_PAGES_MAX 0x7ffffc00
 #define ERS_FLAG_COPY 8u
 
 typedef struct ers_page_pool {

@@ -94,6 +94,14 @@ def test_pages_refusals(lib):
 
 
 @needs_no_gpu
+def test_pages_past_32_bits_are_refused(lib):
+    # counts that the deciding CTA's steps of 1024 would carry past 32 bits (699734 * 3069 = 2^31 - 2)
+    for kw in (dict(npages=2**31 - 1), dict(npages=0x7ffffc01), dict(nslots=699734, slot_pages=3069)):
+        assert lib.ers_pages_free(ctypes.byref(_pool(**kw)), 0, None, None, None) == 1, kw
+    assert lib.ers_pages_free(ctypes.byref(_pool(npages=0x7ffffc00)), 0, None, None, None) == 0
+
+
+@needs_no_gpu
 def test_logprobs_refusals(lib):
     from exact_replay_decode_gb300 import _abi
 
