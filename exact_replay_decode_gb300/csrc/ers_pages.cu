@@ -75,7 +75,15 @@ __device__ __forceinline__ int32_t check_slots(const PageArgs& a, const int32_t*
   return err;
 }
 
-__device__ __forceinline__ bool page_ok(const PageArgs& a, int p) { return p >= -1 && p < a.npages; }
+// Entry e of the listed slots' table rows, one row after the other.
+__device__ __forceinline__ int32_t* entry(const PageArgs& a, int e) {
+  return &a.table[(size_t)a.dst[e / a.slot_pages] * a.slot_pages + e % a.slot_pages];
+}
+// An entry: -1, or a page of the pool that has a reference (one without counts as free: it would be handed out again).
+__device__ __forceinline__ int32_t check_entry(const PageArgs& a, int p) {
+  if (p < -1 || p >= a.npages) return ERS_ESLOT;
+  return p >= 0 && a.refs[p] < 1 ? ERS_EINVAL : ERS_OK;
+}
 
 __global__ void __launch_bounds__(kPlan) k_pages_fork(PageArgs a) {
   extern __shared__ uint32_t seen[];
@@ -91,7 +99,8 @@ __global__ void __launch_bounds__(kPlan) k_pages_fork(PageArgs a) {
   for (int e = threadIdx.x; e < m; e += kPlan) {
     const int i = e / a.slot_pages, c = e % a.slot_pages;
     if (a.table[(size_t)a.dst[i] * a.slot_pages + c] != -1) err = ERS_EINVAL;   // it would be lost
-    if (!page_ok(a, a.table[(size_t)a.src[i] * a.slot_pages + c])) err = ERS_ESLOT;
+    const int32_t bad = check_entry(a, a.table[(size_t)a.src[i] * a.slot_pages + c]);
+    if (bad != ERS_OK) err = bad;
   }
   if (failed(err, a.status)) return;
   for (int e = threadIdx.x; e < m; e += kPlan) {
@@ -108,14 +117,16 @@ __global__ void __launch_bounds__(kPlan) k_pages_free(PageArgs a) {
   const int m = a.n * a.slot_pages;
   if (failed(check_slots(a, a.dst, seen), a.status)) return;
   int32_t err = ERS_OK;
-  for (int e = threadIdx.x; e < m; e += kPlan)
-    if (!page_ok(a, a.table[(size_t)a.dst[e / a.slot_pages] * a.slot_pages + e % a.slot_pages])) err = ERS_ESLOT;
-  if (failed(err, a.status)) return;
   for (int e = threadIdx.x; e < m; e += kPlan) {
-    int32_t* at = &a.table[(size_t)a.dst[e / a.slot_pages] * a.slot_pages + e % a.slot_pages];
-    const int p = *at;
-    if (p >= 0) atomicSub(&a.refs[p], 1);
-    *at = -1;
+    const int p = *entry(a, e);
+    if (p < -1 || p >= a.npages) err = ERS_ESLOT;
+    else if (p >= 0 && atomicSub(&a.refs[p], 1) < 1) err = ERS_EINVAL;   // named more often than counted
+  }
+  const bool bad = failed(err, a.status);   // then all references are given back
+  for (int e = threadIdx.x; e < m; e += kPlan) {
+    const int p = *entry(a, e);
+    if (!bad) *entry(a, e) = -1;
+    else if (p >= 0 && p < a.npages) atomicAdd(&a.refs[p], 1);
   }
 }
 
@@ -135,8 +146,9 @@ __global__ void __launch_bounds__(kPlan) k_pages_own(PageArgs a) {
       const int e = e0 + threadIdx.x;
       int need = 0, p = -1;
       if (e < m) {
-        p = a.table[(size_t)a.dst[e / a.slot_pages] * a.slot_pages + e % a.slot_pages];
-        if (!page_ok(a, p)) err = ERS_ESLOT;
+        p = *entry(a, e);
+        const int32_t wrong = check_entry(a, p);
+        if (wrong != ERS_OK) err = wrong;
         else need = p < 0 || a.refs[p] > 1;
       }
       int total;
@@ -158,39 +170,50 @@ __global__ void __launch_bounds__(kPlan) k_pages_own(PageArgs a) {
     if (found < needed) err = ERS_EOVERFLOW;
     bad = failed(err, a.status);
   }
+  if (!bad) {
+    for (int e = threadIdx.x; e < m; e += kPlan) {
+      const int r = rank[e], old = a.read_page[e];
+      if (r < 0) continue;
+      const int p = free_page[r];
+      a.refs[p] = 1;
+      *entry(a, e) = p;
+      if (old >= 0 && atomicSub(&a.refs[old], 1) < 1) err = ERS_EINVAL;   // named more often than counted
+    }
+    bad = failed(err, a.status);            // then all of it is taken back
+    for (int e = threadIdx.x; bad && e < m; e += kPlan) {
+      const int r = rank[e], old = a.read_page[e];
+      if (r < 0) continue;
+      a.refs[free_page[r]] = 0;
+      *entry(a, e) = old;
+      if (old >= 0) atomicAdd(&a.refs[old], 1);
+    }
+  }
   if (bad) {
     for (int e = threadIdx.x; e < m; e += kPlan) {
       rank[e] = -1;
       a.read_page[e] = -2;
     }
-    return;
-  }
-  for (int e = threadIdx.x; e < m; e += kPlan) {
-    const int r = rank[e], old = a.read_page[e];
-    if (r < 0) continue;
-    const int p = free_page[r];
-    if (old >= 0) atomicSub(&a.refs[old], 1);
-    a.refs[p] = 1;
-    a.table[(size_t)a.dst[e / a.slot_pages] * a.slot_pages + e % a.slot_pages] = p;
   }
 }
 
-// ws: [0] pages that move, [1, 1 + npages) where from, then [npages] where to
+// ws: [0] pages that move (-1: an error was found), [1, 1 + npages) where from, then [npages] where to
 __global__ void __launch_bounds__(kPlan) k_pages_compact(PageArgs a) {
   __shared__ int scratch[kPlan / 32];
   follow();
   int32_t* from = a.ws + 1;
   int32_t* to = from + a.npages;
   int32_t err = ERS_OK;
-  for (long long e = threadIdx.x; e < (long long)a.nslots * a.slot_pages; e += kPlan)
-    if (!page_ok(a, a.table[e])) err = ERS_ESLOT;
-  const bool bad = failed(err, a.status);
+  for (long long e = threadIdx.x; e < (long long)a.nslots * a.slot_pages; e += kPlan) {
+    const int32_t wrong = check_entry(a, a.table[e]);
+    if (wrong != ERS_OK) err = wrong;
+  }
   int live = 0;
   for (int p0 = 0; p0 < a.npages; p0 += kPlan) {
     int total;
     block_scan(p0 + threadIdx.x < a.npages && a.refs[p0 + threadIdx.x] > 0, scratch, &total);
     live += total;
   }
+  const bool bad = failed(err, a.status);
   int holes = 0, movers = 0;
   for (int p0 = 0; p0 < a.npages; p0 += kPlan) {
     const int p = p0 + threadIdx.x;
@@ -213,7 +236,7 @@ __global__ void __launch_bounds__(kPlan) k_pages_compact(PageArgs a) {
     a.refs[from[r]] = 0;
   }
   if (threadIdx.x == 0) {
-    a.ws[0] = movers;
+    a.ws[0] = bad ? -1 : movers;
     *a.live = live;
   }
 }
@@ -260,10 +283,11 @@ template <int kind>
 __global__ void __launch_bounds__(kThreads) k_pages_move(PageArgs a, long long pieces) {
   follow();
   if (kind == kMoveCompact) {   // the tables follow
+    const bool good = a.ws[0] >= 0;
     const long long entries = (long long)a.nslots * a.slot_pages;
     for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < entries; e += (long long)gridDim.x * kThreads) {
       const int p = a.table[e];
-      if (p >= 0 && p < a.npages) a.table[e] = a.remap[p];   // out of range: found by the plan, nothing moves
+      if (good && p >= 0) a.table[e] = a.remap[p];
     }
   }
   const long long count = kind == kMoveCompact ? a.ws[0] : kind == kMoveOwn ? a.n * a.slot_pages : a.n;

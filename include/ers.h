@@ -546,7 +546,8 @@ ERS_API ers_status ers_linattn_decode(const ers_linattn_dims* dims, const float*
  * ers_pages_copy: page dst[i] receives page src[i] in every array (table and refs unused, may be NULL); src may repeat; no
  *   page is both, and dst are distinct.
  * Workspaces are 16-byte aligned buffers of the size that the query returns.
- * Device errors: ERS_ESLOT (slot, or a page outside [0, npages)), ERS_EINVAL, ERS_EOVERFLOW. */
+ * Device errors: ERS_ESLOT (slot, or a page outside [0, npages)), ERS_EINVAL (also an entry whose page has no reference, or
+ *   pages given up more often than they have references), ERS_EOVERFLOW. */
 #define ERS_PAGE_ARRAYS_MAX 12
 #define ERS_PAGE_SLOTS_MAX (1 << 20)
 #define ERS_PAGES_MAX 0x7ffffc00

@@ -201,6 +201,43 @@ def test_refusals():
         ers.ReplayCache(1, 4, 1, 64, 128, 16).page_pool()
 
 
+def test_entries_without_a_reference_change_nothing():
+    """A table that names a page more often than refs counts it: reported by every call that meets it, nothing changes."""
+    ers = _ers()
+    pool, model, _ = _pool(11, 6, 2, 12, [(32,)])
+    ers.pages_own(pool, _ints([0, 1, 2]))
+    model.own([0, 1, 2], True)
+    ers.pages_free(pool, _ints([0]))                                  # pages 0 and 1: holes below the others
+    model.free([0])
+    st = ers.Status("cuda")
+
+    def fails(f, *args, **kw):
+        st.reset()
+        out = f(*args, status=st, check=False, **kw)
+        assert st.read() == 1
+        _same(pool, model)
+        return out
+
+    pool.refs[4] = model.refs[4] = 0                                  # slot 2's first
+    fails(ers.pages_free, pool, _ints([1, 2]))
+    fails(ers.pages_fork, pool, _ints([1, 2]), _ints([3, 4]))
+    for copy in (True, False):
+        assert (fails(ers.pages_own, pool, _ints([3, 2]), copy=copy) == -2).all()
+    remap, live = fails(ers.pages_compact, pool)
+    assert int(live) == 3 and remap.tolist() == [-1, -1, 2, 3, -1, 5] + [-1] * 6
+    pool.refs[4] = model.refs[4] = 1
+    ers.pages_fork(pool, _ints([2, 2]), _ints([3, 4]))
+    model.fork([2, 2], [3, 4])
+    pool.refs[5] = model.refs[5] = 2                                  # named by three slots
+    fails(ers.pages_free, pool, _ints([3, 2, 4]))
+    for copy in (True, False):
+        assert (fails(ers.pages_own, pool, _ints([0, 4, 2, 3]), copy=copy) == -2).all()
+    pool.refs[5] = model.refs[5] = 3
+    read = ers.pages_own(pool, _ints([4, 2]))
+    assert np.array_equal(read.cpu().numpy(), model.own([4, 2], True))
+    _same(pool, model)
+
+
 def test_counting_a_table_that_names_pages_out_of_range():
     """The pool counts what is in range; the calls report the rest."""
     ers = _ers()
