@@ -44,7 +44,7 @@ EXPORTS = (
     "ers_conv1d_update", "ers_gdn_verify", "ers_gdn_commit", "ers_gdn_refresh", "ers_selftest_bounded_wait",
     "ers_spec_verify_exact_workspace_size", "ers_spec_verify_exact", "ers_commit_exact",
     "ers_linattn_fwd", "ers_linattn_prefill", "ers_linattn_decode", "ers_pages_fork", "ers_pages_own_workspace_size",
-    "ers_pages_own", "ers_pages_free", "ers_pages_compact_workspace_size", "ers_pages_compact", "ers_pages_copy",
+    "ers_pages_own", "ers_pages_clone", "ers_pages_free", "ers_pages_compact_workspace_size", "ers_pages_compact", "ers_pages_copy",
     "ers_token_logprobs",
 )
 
@@ -153,6 +153,7 @@ _SIGS = {
     "ers_pages_fork": ([_POOL, _I32, _P, _P, _P, _P], _I32),
     "ers_pages_own_workspace_size": ([_POOL, _I32], _SZ),
     "ers_pages_own": ([_POOL, _I32, _P, _U32, _P, _P, _SZ, _P, _P], _I32),
+    "ers_pages_clone": ([_POOL, _I32, _P, _P, _P, _P, _SZ, _P, _P], _I32),
     "ers_pages_free": ([_POOL, _I32, _P, _P, _P], _I32),
     "ers_pages_compact_workspace_size": ([_POOL], _SZ),
     "ers_pages_compact": ([_POOL, _P, _P, _P, _SZ, _P, _P], _I32),

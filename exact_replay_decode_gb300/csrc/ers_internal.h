@@ -226,6 +226,7 @@ struct PageArgs {
 };
 cudaError_t pages_fork(const PageArgs& a, cudaStream_t s);
 cudaError_t pages_own(const PageArgs& a, bool copy, cudaStream_t s);   // ws: 2 n slot_pages
+cudaError_t pages_clone(const PageArgs& a, cudaStream_t s);            // ws: 2 n slot_pages
 cudaError_t pages_free(const PageArgs& a, cudaStream_t s);
 cudaError_t pages_compact(const PageArgs& a, cudaStream_t s);          // ws: 1 + 2 npages
 cudaError_t pages_copy(const PageArgs& a, cudaStream_t s);

@@ -196,6 +196,63 @@ __global__ void __launch_bounds__(kPlan) k_pages_own(PageArgs a) {
   }
 }
 
+// As free of dst, fork and own of the same lists, in one decision: every entry of dst's rows gets a page of its own, to be filled
+// from src's.  ws as k_pages_own.
+__global__ void __launch_bounds__(kPlan) k_pages_clone(PageArgs a) {
+  extern __shared__ uint32_t seen[];
+  __shared__ int scratch[kPlan / 32];
+  follow();
+  const int m = a.n * a.slot_pages;
+  int32_t* rank = a.ws;
+  int32_t* free_page = a.ws + m;
+  int32_t err = check_slots(a, a.dst, seen);
+  for (int i = threadIdx.x; i < a.n; i += kPlan) {
+    const int s = a.src[i];
+    if (s < 0 || s >= a.nslots) err = ERS_ESLOT;
+    else if ((seen[s >> 5] >> (s & 31)) & 1u) err = ERS_EINVAL;
+  }
+  bool bad = failed(err, a.status);
+  const bool given_up = !bad;
+  if (!bad) {
+    for (int e = threadIdx.x; e < m; e += kPlan) {
+      const int p = a.table[(size_t)a.src[e / a.slot_pages] * a.slot_pages + e % a.slot_pages], old = *entry(a, e);
+      a.read_page[e] = p;
+      if (p < -1 || p >= a.npages || old < -1 || old >= a.npages) err = ERS_ESLOT;
+      if (old >= 0 && old < a.npages && atomicSub(&a.refs[old], 1) < 1) err = ERS_EINVAL;   // named more often than counted
+    }
+    bad = failed(err, a.status);
+  }
+  if (!bad) {
+    int found = 0;
+    for (int e = threadIdx.x; e < m; e += kPlan) {
+      const int32_t wrong = check_entry(a, a.read_page[e]);   // (what dst gave up is no longer counted)
+      if (wrong != ERS_OK) err = wrong;
+    }
+    for (int p0 = 0; p0 < a.npages && found < m; p0 += kPlan) {
+      const int p = p0 + threadIdx.x;
+      const int is_free = p < a.npages && a.refs[p] <= 0;
+      int total;
+      const int r = found + block_scan(is_free, scratch, &total) - 1;
+      if (is_free && r < m) free_page[r] = p;
+      found += total;
+    }
+    if (found < m) err = ERS_EOVERFLOW;
+    bad = failed(err, a.status);
+  }
+  for (int e = threadIdx.x; e < m; e += kPlan) {
+    if (bad) {
+      const int old = given_up ? *entry(a, e) : -1;
+      if (old >= 0 && old < a.npages) atomicAdd(&a.refs[old], 1);
+      rank[e] = -1;
+      a.read_page[e] = -2;
+    } else {
+      rank[e] = e;
+      a.refs[free_page[e]] = 1;
+      *entry(a, e) = free_page[e];
+    }
+  }
+}
+
 // ws: [0] pages that move (-1: an error was found), [1, 1 + npages) where from, then [npages] where to
 __global__ void __launch_bounds__(kPlan) k_pages_compact(PageArgs a) {
   __shared__ int scratch[kPlan / 32];
@@ -360,6 +417,11 @@ cudaError_t pages_free(const PageArgs& a, cudaStream_t s) { return plan(k_pages_
 cudaError_t pages_own(const PageArgs& a, bool copy, cudaStream_t s) {
   const cudaError_t e = plan(k_pages_own, a, s);
   return e != cudaSuccess || !copy ? e : move(a, kMoveOwn, (long long)a.n * a.slot_pages, s);
+}
+
+cudaError_t pages_clone(const PageArgs& a, cudaStream_t s) {
+  const cudaError_t e = plan(k_pages_clone, a, s);
+  return e != cudaSuccess ? e : move(a, kMoveOwn, (long long)a.n * a.slot_pages, s);
 }
 
 cudaError_t pages_compact(const PageArgs& a, cudaStream_t s) {

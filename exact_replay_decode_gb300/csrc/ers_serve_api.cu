@@ -197,6 +197,25 @@ ers_status ers_pages_own(const ers_page_pool* pool, int32_t n, const int32_t* sl
   return finish(ers::pages_own(a, (flags & ERS_FLAG_COPY) != 0, (cudaStream_t)stream));
 }
 
+ers_status ers_pages_clone(const ers_page_pool* pool, int32_t n, const int32_t* src, const int32_t* dst,
+                           int32_t* read_page, void* workspace, size_t workspace_bytes, ers_stream_t stream,
+                           int32_t* dev_status) {
+  ERS_TRY(check_pool(pool, n, true));
+  if (n == 0) return ERS_OK;
+  ERS_TRY(check_ptr(src, true));
+  ERS_TRY(check_ptr(dst, true));
+  ERS_TRY(check_ptr(read_page, true));
+  ERS_TRY(check_ptr(dev_status, false));
+  if (workspace == nullptr || workspace_bytes < ers_pages_own_workspace_size(pool, n)) return ERS_EWORKSPACE;
+  ERS_TRY(check_ptr(workspace, true));
+  ers::PageArgs a = page_args(pool, n, dev_status);
+  a.src = src;
+  a.dst = dst;
+  a.read_page = read_page;
+  a.ws = static_cast<int32_t*>(workspace);
+  return finish(ers::pages_clone(a, (cudaStream_t)stream));
+}
+
 ers_status ers_pages_free(const ers_page_pool* pool, int32_t n, const int32_t* slot, ers_stream_t stream,
                           int32_t* dev_status) {
   ERS_TRY(check_pool(pool, n, true));

@@ -172,21 +172,33 @@ def pages_copy(arrays: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.Ten
     _finish(code, "ers_pages_copy", st, check)
 
 
+def _pages_clone(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, status: Optional[Status], check: bool) -> torch.Tensor:
+    """Slots dst give up their pages for copies of src's (ers_pages_clone).  Returns src's entries, -2 after an error."""
+    n = dst.numel()
+    s, d = _list_arg(src, "src", n), _list_arg(dst, "dst", n)
+    read = torch.empty(n, pool.slot_pages, dtype=torch.int32, device=dst.device)
+    st = _status(status, check, dst.device)
+    code = _abi.lib().ers_pages_clone(pool._c, n, s, d, read.data_ptr(), pool._work.data_ptr(), pool._work.numel(),
+                                      *_where(dst.device, st))
+    _finish(code, "ers_pages_clone", st, check)
+    return read
+
+
 @_on_stream
 def fork_slots(cache: ReplayCache, src: torch.Tensor, dst: torch.Tensor, status: Optional[Status] = None,
                check: bool = True, stream=None) -> None:
     """Slots dst of a ReplayCache become copies of slots src (distinct, none of them in src): the state, the read
     copy, the position and the buffered rows, so that both decode on from there.  Paged buffers: dst gives up its
-    pages and gets pages of its own from cache.page_pool()."""
+    pages and gets pages of its own from cache.page_pool(), in one decision with everything else: where that finds an
+    error (too few free pages, lists that overlap), no slot is changed."""
     arrays = [t for t in (cache.state, cache.read_copy, cache.read_scale, cache.read_block_scale, cache.pos)
               if t is not None]
     if cache.buf_pages is None:
         arrays += [cache.buf_x, cache.buf_dt, cache.buf_B, cache.buf_C]
     else:
-        pool = cache.page_pool()
-        pages_free(pool, dst, status=status, check=check)
-        pages_fork(pool, src, dst, status=status, check=check)
-        pages_own(pool, dst, True, status=status, check=check)
+        read = _pages_clone(cache.page_pool(), src, dst, status, check)
+        if not check:   # after an error known on the device only: sources that pages_copy leaves out
+            src = torch.where(read[:, 0] == -2, -1, src)
     pages_copy(arrays, src, dst, status=status, check=check)
 
 

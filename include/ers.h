@@ -539,6 +539,9 @@ ERS_API ers_status ers_linattn_decode(const ers_linattn_dims* dims, const float*
  *   read_page [n, slot_pages] receives the entries as they were (-2 throughout on an error).  A page all of whose
  *   owners are listed is free afterwards; its contents stay until a later call hands it out.  With ERS_FLAG_COPY the
  *   new page receives the old one's contents in every array, or zeros where the entry was -1.
+ * ers_pages_clone: ers_pages_free of dst, ers_pages_fork and ers_pages_own with ERS_FLAG_COPY of dst in one decision: row dst[i]
+ *   gives up its pages and gets pages of its own with the contents of row src[i]'s (zeros where that has none).  src may repeat,
+ *   a slot is not both.  read_page [n, slot_pages] receives src's entries (-2 throughout on an error); workspace as ers_pages_own.
  * ers_pages_free: the listed slots give up their pages.
  * ers_pages_compact: with n pages in use, those at n and above move, in ascending order, to the free pages below n, also in
  *   ascending order; contents, refs and table follow.  remap [npages] receives each page's new index
@@ -571,6 +574,10 @@ ERS_API size_t ers_pages_own_workspace_size(const ers_page_pool* pool, int32_t n
 ERS_API ers_status ers_pages_own(const ers_page_pool* pool, int32_t n, const int32_t* slot, uint32_t flags,
                                  int32_t* read_page, void* workspace, size_t workspace_bytes, ers_stream_t stream,
                                  int32_t* dev_status);
+
+ERS_API ers_status ers_pages_clone(const ers_page_pool* pool, int32_t n, const int32_t* src, const int32_t* dst,
+                                   int32_t* read_page, void* workspace, size_t workspace_bytes, ers_stream_t stream,
+                                   int32_t* dev_status);
 
 ERS_API ers_status ers_pages_free(const ers_page_pool* pool, int32_t n, const int32_t* slot, ers_stream_t stream,
                                   int32_t* dev_status);

@@ -6,6 +6,8 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
+BF16 = torch.bfloat16
+
 
 def _ers():
     import exact_replay_decode_gb300 as ers
@@ -282,3 +284,100 @@ def test_forked_replay_slots_decode_with_the_parents_bits(paged):
     assert torch.equal(y[0].view(torch.int16), y_ref[-1].view(torch.int16))
     if paged:
         assert (cache.page_pool().refs[cache.buf_pages.long()] == 1).all()
+
+
+def _replay_arrays(cache):
+    return [t for t in (cache.state, cache.read_copy, cache.read_scale, cache.read_block_scale, cache.pos, cache.buf_x,
+                        cache.buf_dt, cache.buf_B, cache.buf_C, cache.buf_pages) if t is not None]
+
+
+def _filled(paged, **kw):
+    cache = _ers().ReplayCache(4, 4, 2, 64, 128, 16, BF16, paged=paged, **kw)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for t in _replay_arrays(cache):
+        if t is not cache.buf_pages:
+            t.view(torch.uint8).random_(0, 256, generator=g)
+    return cache
+
+
+@pytest.mark.parametrize("paged", [None, (4, 24)], ids=["dense", "paged"])
+@pytest.mark.parametrize("kw", [dict(), dict(read_copy=True), dict(read_copy=True, read_dtype="fp8"),
+                                dict(read_copy=True, read_dtype="nvfp4", anchor="fp16_sr"),
+                                dict(read_copy=True, read_dtype="nvfp4", anchor="nvfp4_sr_shared")], ids=str)
+def test_fork_slots_copies_every_array(paged, kw):
+    """Also the read copies with their scales, byte by byte; other slots keep theirs."""
+    cache = _filled(paged, **kw)
+    before = [t.clone() for t in _replay_arrays(cache)]
+    _ers().fork_slots(cache, _ints([2, 2]), _ints([3, 0]))
+    for t, old in zip(_replay_arrays(cache), before):
+        if t is cache.buf_pages:
+            assert torch.equal(t[[1, 2]], old[[1, 2]]) and t.unique().numel() == t.numel()
+            continue
+        own, was = t, old
+        if paged and t.shape[0] == 24:                       # a slot's rows, through the table now and before
+            own, was = t[cache.buf_pages.long()], old[before[-1].long()]
+        own, was = (y.reshape(4, -1).contiguous().view(torch.uint8) for y in (own, was))
+        for slot, source in enumerate((2, 1, 2, 2)):
+            assert torch.equal(own[slot], was[source])
+
+
+@pytest.mark.parametrize("paged,src,dst,code", [
+    ((4, 18), [0, 1], [2, 3], 0), ((4, 16), [0, 1, 0], [2, 3, 2], 1), ((4, 24), [0, 2], [2, 3], 1), ((4, 24), [0, 4], [2, 3], 8),
+    ((4, 24), [0, 1], [2, -1], 8), ((4, 10), [0], [3], 6), ((4, 10), [0, 1], [2, 3], 6), ((4, 11), [1], [2], 6)], ids=str)
+def test_fork_slots_whole_or_not_at_all(paged, src, dst, code):
+    """Too few free pages (a cache whose later slots share page 0), lists that overlap, slots that are none."""
+    ers = _ers()
+    for check in (True, False):
+        cache = _filled(paged)
+        refs = cache.page_pool().refs
+        before = [t.clone() for t in _replay_arrays(cache) + [refs]]
+        if check and code:
+            with pytest.raises(ers.ErsError):
+                ers.fork_slots(cache, _ints(src), _ints(dst))
+        else:
+            st = ers.Status("cuda")
+            ers.fork_slots(cache, _ints(src), _ints(dst), status=st, check=False)
+            assert st.read() == code
+            if code:                                           # and without a word
+                ers.fork_slots(cache, _ints(src), _ints(dst), check=False)
+        after = _replay_arrays(cache) + [refs]
+        same = [torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(after, before)]
+        assert all(same) if code else not any(same[:2])
+
+
+def test_clone_equals_free_fork_and_own():
+    """One decision, against the model's three; pages that dst gives up are handed out again."""
+    ers = _ers()
+    from exact_replay_decode_gb300 import serve
+    for seed in range(12):
+        pool, model, rng = _pool(seed, 9, 2, 22, [(24,), (3, 5)])
+        ers.pages_own(pool, _ints([8, 1, 4, 0]))
+        model.own([8, 1, 4, 0], True)
+        ers.pages_fork(pool, _ints([1, 1]), _ints([3, 6]))
+        model.fork([1, 1], [3, 6])
+        dst = rng.permutation(9)[:4]
+        src = rng.choice(np.setdiff1d(np.arange(9), dst), 4)
+        read = serve._pages_clone(pool, _ints(src), _ints(dst), None, True)
+        model.free(dst)
+        assert np.array_equal(read.cpu().numpy(), model.table[src])
+        model.fork(src, dst)
+        model.own(dst, True)
+        _same(pool, model)
+
+
+def test_clone_with_entries_that_are_not_counted():
+    ers = _ers()
+    pool, model, _ = _pool(5, 5, 1, 9, [(16,)])
+    ers.pages_own(pool, _ints([0, 1]))
+    model.own([0, 1], True)
+    ers.pages_fork(pool, _ints([0]), _ints([2]))
+    model.fork([0], [2])
+    for page, count in ((0, 1), (1, 0), (0, 0)):               # src and dst name page 0, counted once; dst's page 1 not at all
+        pool.refs[page] = count
+        model.refs[page] = count
+        st = ers.Status("cuda")
+        from exact_replay_decode_gb300 import serve
+        read = serve._pages_clone(pool, _ints([0, 0]), _ints([2, 1]), st, False)
+        assert st.read() == 1 and (read == -2).all()
+        _same(pool, model)
+        pool.refs[page] = model.refs[page] = 2 if page == 0 else 1

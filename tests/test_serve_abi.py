@@ -102,6 +102,21 @@ def test_pages_past_32_bits_are_refused(lib):
 
 
 @needs_no_gpu
+def test_pages_clone_refusals(lib):
+    def clone(n=1, src=FAKE, dst=FAKE, read=FAKE, ws=FAKE, size=1 << 20, **kw):
+        return lib.ers_pages_clone(ctypes.byref(_pool(**kw)), n, src, dst, read, ws, size, None, None)
+
+    assert clone(n=0, src=None, dst=None, read=None, ws=None, size=0) == 0
+    assert clone(n=5) == 1 and clone(n=-1) == 1
+    for kw in (dict(src=None), dict(dst=None), dict(read=None)):
+        assert clone(**kw) == 1, kw
+    for kw in (dict(src=OFF), dict(dst=OFF), dict(read=OFF), dict(ws=OFF)):
+        assert clone(**kw) == 4, kw
+    assert clone(ws=None) == 10 and clone(size=8) == 10
+    assert clone(slot_pages=0) == 2
+
+
+@needs_no_gpu
 def test_logprobs_refusals(lib):
     from exact_replay_decode_gb300 import _abi
 
