@@ -251,6 +251,18 @@ def _seqlens(cu_seqlens: Optional[torch.Tensor], T: int, device):
     return cu_seqlens, S
 
 
+def _longest(cu_seqlens: torch.Tensor, T: int, S: int, H: int, max_seqlen: Optional[int]) -> int:
+    """max_seqlen, or the longest length that cu_seqlens has, which waits for the device (25 us).  T, an upper bound for which
+    the work of several sequences may be split too far, while a stream is captured, and of up to 256 tokens of few heads or of
+    few tokens a sequence (12 x 20 tokens x 16 heads: 22 us by T and 18 by 20; 28 x 9 x 64: 127 and 77, so it is read)."""
+    if max_seqlen is not None:
+        return int(max_seqlen)
+    if S <= 1 or T <= 256 and (S * H <= 304 or T <= 8 * S) or torch.cuda.is_current_stream_capturing():
+        return T
+    at = cu_seqlens.tolist()
+    return min(max(max(b - a for a, b in zip(at, at[1:])), 0), T)   # (whatever cu_seqlens holds)
+
+
 def _out(out: Optional[torch.Tensor], v: torch.Tensor) -> torch.Tensor:
     if out is None:
         return torch.empty_like(v)
@@ -268,7 +280,8 @@ def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
 
     q, k [T,G,dk], v [T,H,dv] (bf16 or fp32; dk, dv 64 or 128), log_decay [H] fp32 (<= 0); cu_seqlens int32 [S+1]
     (default: one sequence); init_state [S,H,dv,dk] fp32 (default zeros).  max_seqlen, the longest sequence's length,
-    only chooses how the work is split (default: T).  Returns (o [T,H,dv], final_state [S,H,dv,dk] fp32)."""
+    only chooses how the work is split (default: read from cu_seqlens, which waits for the device; T for few tokens and while a
+    stream is captured).  Returns (o [T,H,dv], final_state [S,H,dv,dk] fp32)."""
     io = _io_from(q)
     T, G, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
@@ -285,7 +298,7 @@ def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
         _tensor(final, torch.float32, "out[1]", state)
     st = _status(status, check, dev)
     code = _abi.lib().ers_linattn_fwd(_linattn_dims(H, G, dk, dv, io, float(scale)), decay, S, T,
-                                      T if max_seqlen is None else int(max_seqlen), cu_seqlens.data_ptr(), *qkv,
+                                      _longest(cu_seqlens, T, S, H, max_seqlen), cu_seqlens.data_ptr(), *qkv,
                                       init, o.data_ptr(), final.data_ptr(), *_where(dev, st))
     _finish(code, "ers_linattn_fwd", st, check)
     return o, final
@@ -309,7 +322,8 @@ def linattn_prefill(cache: LinAttnCache, q, k, v, log_decay, cu_seqlens: Optiona
                     scale: float = 1.0, max_seqlen: Optional[int] = None, status: Optional[Status] = None,
                     check: bool = True, stream=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Packed prompts that go on from the slots' cached states (ers_linattn_prefill): each state is read from
-    read_page (default: the slot's own page; -1: zeros) and written to the slot's own page.  Returns o [T,H,dv]."""
+    read_page (default: the slot's own page; -1: zeros) and written to the slot's own page.  max_seqlen: as in
+    linattn_fwd.  Returns o [T,H,dv]."""
     T, dev = q.shape[0], q.device
     cu_seqlens, S = _seqlens(cu_seqlens, T, dev)
     decay, qkv = _qkv(q, k, v, log_decay, cache.io, T, cache.H, cache.G, cache.dk, cache.dv)
@@ -317,7 +331,7 @@ def linattn_prefill(cache: LinAttnCache, q, k, v, log_decay, cu_seqlens: Optiona
     st = _status(status, check, dev)
     dims = _linattn_dims(cache.H, cache.G, cache.dk, cache.dv, cache.io, float(scale))
     code = _abi.lib().ers_linattn_prefill(dims, decay, cache._c, S, T,
-                                          T if max_seqlen is None else int(max_seqlen), cu_seqlens.data_ptr(),
+                                          _longest(cu_seqlens, T, S, cache.H, max_seqlen), cu_seqlens.data_ptr(),
                                           _slot(slot, S), _read_arg(read_page, S), *qkv, o.data_ptr(), *_where(dev, st))
     _finish(code, "ers_linattn_prefill", st, check)
     return o

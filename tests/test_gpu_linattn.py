@@ -126,6 +126,20 @@ def test_long_prompts_whatever_the_split(lens, H):
     _check(o, fin, q, k, v, decay, lens, init)
 
 
+@pytest.mark.parametrize("lens,H", [([2048] * 4, 32), ([700, 300, 900], 8), ([1] * 30 + [400, 200], 16)], ids=["even", "few", "short"])
+def test_the_default_call_is_planned_by_its_lengths(lens, H):
+    """Without max_seqlen a call of several sequences gives the bits, and so takes the split, of one with the right length."""
+    ers = _ers()
+    q, k, v, decay = _inputs(H, sum(lens), H, 4, 128, 128, BF16)
+    cu = _cu(lens)
+    o, fin = ers.linattn_fwd(q, k, v, decay, cu, max_seqlen=max(lens))
+    p, fin2 = ers.linattn_fwd(q, k, v, decay, cu)
+    assert torch.equal(o, p) and torch.equal(fin, fin2)
+    cache = ers.LinAttnCache(len(lens), H, 4)
+    p = ers.linattn_prefill(cache, q, k, v, decay, cu)
+    assert torch.equal(o, p) and torch.equal(fin, cache.state)
+
+
 @pytest.mark.parametrize("lens,H", [([129, 1, 0], 2), ([256], 3), ([385, 640], 20), ([512], 8), ([1025, 3, 0, 128], 16),
                                     ([1100] + [1] * 12, 8), ([897], 36)], ids=str)
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
