@@ -245,7 +245,9 @@ def _qkv(q, k, v, log_decay, io, T, H, G, dk, dv):
 
 def _seqlens(cu_seqlens: Optional[torch.Tensor], T: int, device):
     if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=device)
+        # made on the device: a copy from the host would wait, and cannot be captured
+        d = dict(dtype=torch.int32, device=device)
+        cu_seqlens = torch.arange(0, T + 1, T, **d) if T > 0 else torch.zeros(2, **d)
     S = cu_seqlens.numel() - 1
     _tensor(cu_seqlens, torch.int32, "cu_seqlens", (S + 1,))
     return cu_seqlens, S

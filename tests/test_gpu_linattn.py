@@ -321,6 +321,50 @@ def test_another_stream():
     assert torch.equal(o, ref) and torch.equal(f, fin)
 
 
+def test_one_prompt_without_cu_seqlens():
+    ers = _ers()
+    q, k, v, decay = _inputs(23, 300, 4, 4, 128, 128, BF16)
+    for T in (300, 1, 0):
+        one = ers.linattn_fwd(q[:T], k[:T], v[:T], decay)
+        two = ers.linattn_fwd(q[:T], k[:T], v[:T], decay, _cu([T]))
+        assert all(torch.equal(a, b) for a, b in zip(one, two))
+
+
+def test_a_serving_step_is_captured_with_default_arguments():
+    """A prompt, a fork, a token of each branch, their scores, the losers' pages and a compaction as one graph: with
+    check=False no call copies from or waits for the device, and the replay has the eager calls' bits."""
+    ers = _ers()
+    H, V = 4, 5003
+    q, k, v, decay = _inputs(24, 500, H, 2, 128, 128, BF16)
+    qd, kd, vd, _ = _inputs(25, 3, H, 2, 128, 128, BF16)
+    logits = (torch.randn(3, V, device="cuda", generator=_gen(26)) * 3).to(BF16)
+    target = torch.tensor([5, 7, 9], dtype=torch.int32, device="cuda")
+    root = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kids, losers = torch.arange(1, 4, dtype=torch.int32, device="cuda"), torch.tensor([1, 3], dtype=torch.int32, device="cuda")
+    parents = root.repeat(3)
+
+    def step(cache):
+        ers.pages_own(cache.pages, root, check=False)
+        out = [ers.linattn_prefill(cache, q, k, v, decay, slot=root, check=False),
+               *ers.linattn_fwd(q, k, v, decay, check=False)]
+        ers.pages_fork(cache.pages, parents, kids, check=False)
+        read = ers.pages_own(cache.pages, kids, copy=False, check=False)
+        out.append(ers.linattn_decode(cache, qd, kd, vd, decay, kids, read_page=read, check=False))
+        out += ers.token_logprobs(logits, target, top_k=4, check=False)
+        ers.pages_free(cache.pages, losers, check=False)
+        return out + list(ers.pages_compact(cache.pages, check=False)) + [cache.state, cache.pages.table, cache.pages.refs]
+
+    want = step(ers.LinAttnCache(4, H, 2, npages=6))
+    cache = ers.LinAttnCache(4, H, 2, npages=6)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(cache)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_errors_leave_outputs_unwritten():
     ers = _ers()
     cache = ers.LinAttnCache(3, 2, 2)
