@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kStepThreads, sizeof(T) == 2 ? 8 : 1)   // (bf
   else lambda = decay_of(a_h);
   if (level && threadIdx.x < kTok) {
     tiles.in[threadIdx.x] = power_of(a_h, kTok / 2 - 1 - (int)threadIdx.x);
-    tiles.out[threadIdx.x] = a.scale * power_of(a_h, (int)threadIdx.x + 1 - kTok / 2);
+    tiles.out[threadIdx.x] = power_of(a_h, (int)threadIdx.x + 1 - kTok / 2);
   }
   const auto times = [&](Decay d) {
     const uint64_t hi = pair(d.hi, d.hi), lo = pair(d.lo, d.lo);
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kStepThreads, sizeof(T) == 2 ? 8 : 1)   // (bf
           const int u = (first + e) / rows, r = (first + e) % rows;
           if ((whole.value || t + u < n) && j % copies == 0)
             ((T*)a.o)[((size_t)(s.t0 + t0 + t + u) * a.H + h) * a.dv + d0 + warp * rows * side + lane / W + r * side] =
-                from_f<T>((is_level.value ? tiles.out[t + u] : a.scale) * dot[e]);
+                from_f<T>(a.scale * (is_level.value ? tiles.out[t + u] * dot[e] : dot[e]));
         }
       };
       int t = 0;

@@ -586,14 +586,15 @@ struct Cta {
   __device__ __forceinline__ void outputs(int c, uint8_t* stage) const {
     const int t = threadIdx.x, i = c - run.c0;
     const uint32_t at = tb + ((uint32_t)(t & ~31) << 16) + kColO;
-    const uint64_t factor = both(strong ? a.scale : a.scale * expf(a_h * (float)(t - 63)));
+    // one after the other: their product may leave the range that the outputs are in
+    const uint64_t level = both(strong ? 1.f : expf(a_h * (float)(t - 63))), scale = both(a.scale);
+    const auto term = [&](uint32_t x, uint32_t y) { return round2(mul2(mul2(pair(x, y), level), scale)); };
     const bool bad = *reinterpret_cast<const uint64_t*>(hd.bad[i & 1]) != 0;
     tmem_each32(at, DV, [&](int x, uint32_t (&o)[32]) {
       if (bad) spoil(o, hd.first_bad[i & 1][0] + x, hd.first_bad[i & 1][1] + x, t);
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
-        const uint4 v = make_uint4(round2(mul2(pair(o[j], o[j + 1]), factor)), round2(mul2(pair(o[j + 2], o[j + 3]), factor)),
-                                   round2(mul2(pair(o[j + 4], o[j + 5]), factor)), round2(mul2(pair(o[j + 6], o[j + 7]), factor)));
+        const uint4 v = make_uint4(term(o[j], o[j + 1]), term(o[j + 2], o[j + 3]), term(o[j + 4], o[j + 5]), term(o[j + 6], o[j + 7]));
         *reinterpret_cast<uint4*>(stage + sw128(kC, t, x + j)) = v;
       }
     });

@@ -111,6 +111,20 @@ def test_extreme_decays(io):
     _check(o, fin, q, k, v, decay, lens, init)
 
 
+@pytest.mark.parametrize("io", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("power", [-105, -66, -40, 40, 66, 105])
+def test_extreme_scales(io, power):
+    """Outputs that are in range are right although scale times a factor of the sums' level is not."""
+    scale = 2.0 ** power
+    lens = [40, 200, 300]
+    for n in lens:                                      # a tile, a chunk and two, by the recurrence and by chunks
+        q, k, v, _ = _inputs(3, n, 5, 5, 128, 128, io)
+        decay = torch.tensor([-1.0, -0.98, -0.6, -0.1, -5.0], device="cuda")
+        init = torch.randn(1, 5, 128, 128, device="cuda", generator=_gen(3))
+        o, fin = _ers().linattn_fwd(q, k, v, decay, init_state=init, scale=scale)
+        _check(o * 2.0 ** -power, fin, q, k, v, decay, [n], init)
+
+
 @pytest.mark.parametrize("lens,H", [([2500], 1), ([1500, 1], 8), ([900, 1100, 700], 40), ([130] * 30, 8)],
                          ids=["split8", "split", "few", "none"])
 def test_long_prompts_whatever_the_split(lens, H):
