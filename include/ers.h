@@ -487,8 +487,12 @@ ERS_API ers_status ers_conv1d_update(const ers_conv_dims* dims, int32_t nseq, co
  *   page, so a sequence that was forked goes on from its parent's page into its own with no copy in between.  Within
  *   a call no slot's own page may be another sequence's own page or read page.  Decode takes one token per sequence.
  * A NaN or infinity in a token reaches that token and later ones of its sequence and no others.
- * Range: a prompt's sums are held at levels that differ from the results' by up to exp(64 |a|), |a| <= 1 (bf16), or
- *   exp(16 |a|) (fp32): products (q.k) v above 1e10 (fp32: 1e31) may overflow to infinity where a is near -1.
+ * Precision: states are fp32 sums of terms of 24 bits.  In bf16 prompts the masked scores and the state that a chunk's outputs are
+ *   formed from are rounded to 16 bits, which the outputs' own rounding to 8 hides; elsewhere operands keep their bits.
+ * Range: a prompt's sums are held at levels that differ from the results' by up to E = exp(64 |a|), |a| <= 1 (bf16), or exp(16 |a|)
+ *   (fp32).  Products (q.k) v above 3e38 / E may overflow to infinity (a = -1: 5e10; fp32: 4e31).  Small ones keep their 16 (24)
+ *   bits down to 2^-117 E (2^-126 E) and an absolute error of 2^-134 E (2^-150 E) below: scores and states of bf16 prompts under
+ *   4e-8 have fewer bits where a is near -1, and 3e-13 is their error.
  * Device errors: ERS_ESLOT (slot, or a page outside [0, npages)), ERS_EINVAL (cu_seqlens not ascending within
  *   [0, ntokens]): the sequence's outputs are then left unwritten; ERS_ETIMEOUT: they are undefined. */
 typedef struct ers_linattn_dims {

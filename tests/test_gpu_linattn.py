@@ -125,6 +125,25 @@ def test_extreme_scales(io, power):
         _check(o * 2.0 ** -power, fin, q, k, v, decay, [n], init)
 
 
+@pytest.mark.parametrize("power", [-20, -30, -40])
+def test_small_values(power):
+    """States of 1e-6 to 1e-12.  With E = exp(64 |a|), operands (scores, states) of bf16 prompts are off by 2^-134 E besides their
+    16 bits, and sums of up to 512 products by 2^-149 E each: an output by that times the sums of |q| and, over its chunk, of |v|."""
+    T = 300
+    q, k, v, _ = _inputs(3, T, 5, 5, 128, 128, BF16)
+    v = v * 2.0 ** power
+    decay = torch.tensor([-1.0, -0.9, -0.5, -0.1, -5.0], device="cuda")
+    init = torch.randn(1, 5, 128, 128, device="cuda", generator=_gen(3)) * 2.0 ** power
+    o, fin = _ers().linattn_fwd(q, k, v, decay, init_state=init)
+    oe, se = _recurrence(q, k, v, decay, [T], init)
+    oa, sa = _recurrence(q, k, v, decay, [T], init, absolute=True)
+    E = torch.exp(torch.where(decay.abs() <= 1, 64 * decay.abs(), torch.zeros_like(decay)).double())[None, :, None]
+    values = torch.stack([v.double().abs()[c:c + 128].sum(0) for c in range(0, T, 128)]).repeat_interleave(128, 0)[:T]
+    small = E * (2.0 ** -134 * (q.double().abs().sum(-1, keepdim=True) + values) + 512 * 2.0 ** -149)
+    assert ((o.double() - oe).abs() <= (2.0 ** -15 + (T + 256) * 2.0 ** -23) * oa + 2.0 ** -8 * oe.abs() + small).all()
+    assert ((fin.double() - se).abs() <= (T + 256) * 2.0 ** -22 * sa + 1e-30).all()
+
+
 @pytest.mark.parametrize("lens,H", [([2500], 1), ([1500, 1], 8), ([900, 1100, 700], 40), ([130] * 30, 8)],
                          ids=["split8", "split", "few", "none"])
 def test_long_prompts_whatever_the_split(lens, H):
