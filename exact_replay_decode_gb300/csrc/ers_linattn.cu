@@ -5,32 +5,17 @@
 
 #include "ers_common.cuh"
 #include "ers_internal.h"
+#include "f32x2.cuh"
 #include "linattn.cuh"
 #include "tc_common.cuh"
 
 namespace ers {
 namespace {
 
-// ---- pairs of floats, one instruction for two ------------------------------------------------------------
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
 __device__ __forceinline__ float sum_of(uint64_t v) {
   float x, y;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+  unpair(v, x, y);
   return x + y;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 // four consecutive elements as two pairs
 __device__ __forceinline__ void load4(const float* p, uint64_t (&v)[2]) {

@@ -24,6 +24,7 @@
 
 #include "ers_common.cuh"
 #include "ers_internal.h"
+#include "f32x2.cuh"
 #include "tc_common.cuh"
 
 namespace ers {
@@ -54,23 +55,6 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 units in the last p
   return y;
 }
 
-// pairs of floats, one instruction for two
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max_nan(float a, float b) {   // a NaN stays one
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -220,12 +204,6 @@ struct Shared {
   float notes[kNotes][kThreads];   // of each thread
 };
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-  cluster_arrive();
-  cluster_wait();
-}
 template <typename V>
 __device__ __forceinline__ V* at_cta(V* p, int rank) {   // the same object of the cluster's rank-th CTA, which has to be running
   uint64_t r;
@@ -262,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   __shared__ Shared sh;
   const int row = blockIdx.x / split, rank = blockIdx.x % split;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (split > 1) cluster_arrive();   // this CTA runs: waited for before anything is written to another's shared memory
+  if (split > 1) tc::cluster_arrive();   // this CTA runs: waited for before anything is written to another's shared memory
   const T* x0 = (const T*)a.logits + (long long)row * a.stride;
   const Row<T> x(x0, a.vocab);
   const int segs = (x.vectors() + 31) / 32;
@@ -431,12 +409,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
   // ---- the row ---------------------------------------------------------------------------------------------------------
   if (split > 1) {
     __syncwarp();
-    cluster_wait();
+    tc::cluster_wait();
     if (threadIdx.x < split) at_cta(sh.all_top, threadIdx.x)[rank] = top;
     if (threadIdx.x == 0) at_first(sh.all_sums)[rank] = s;
     if (tops && threadIdx.x < a.top_k) at_first(sh.all_best)[rank * a.top_k + threadIdx.x] = sh.best[threadIdx.x];
     __syncwarp();
-    cluster_sync();
+    tc::cluster_sync();
     for (int q = 0; q < split; ++q) top = fmaxf(top, sh.all_top[q]);
   }
   const float most_c = top * c;
@@ -471,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(LogprobArgs a, i
     if (split > 1) {
       if (threadIdx.x == 0) at_first(sh.again)[rank] = s;
       __syncwarp();
-      cluster_sync();
+      tc::cluster_sync();
     }
   }
   if (rank != 0) return;
