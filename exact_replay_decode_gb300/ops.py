@@ -266,14 +266,16 @@ class ReplayCache:
         self._pool = None
 
     def page_pool(self):
-        """The buffers' pages as a PagePool (paged caches only).  It counts the table's entries when first asked for;
-        from then on pages change hands through it."""
+        """The buffers' pages as a PagePool (paged caches only).  It counts the table's entries when first asked for, and
+        again where buf_pages or a buffer is another tensor by then; in between pages change hands through it."""
         if self.buf_pages is None:
             raise ValueError("page_pool() is for paged buffers (paged=(page_rows, npages))")
-        if self._pool is None:
+        arrays = [self.buf_x, self.buf_dt, self.buf_B, self.buf_C]
+        p = self._pool
+        if p is None or p.table is not self.buf_pages or any(x is not y for x, y in zip(p.arrays, arrays)):
             from .serve import PagePool
-            self._pool = PagePool([self.buf_x, self.buf_dt, self.buf_B, self.buf_C], self.buf_pages)
-        return self._pool
+            self._pool = p = PagePool(arrays, self.buf_pages)
+        return p
 
     @property
     def dims(self) -> _abi.Dims:

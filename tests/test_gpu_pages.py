@@ -381,3 +381,21 @@ def test_clone_with_entries_that_are_not_counted():
         assert st.read() == 1 and (read == -2).all()
         _same(pool, model)
         pool.refs[page] = model.refs[page] = 2 if page == 0 else 1
+
+
+def test_page_pool_follows_replaced_tensors():
+    """Every other call reads a cache's tensors when it is made; so does a fork."""
+    ers = _ers()
+    cache = _filled((4, 24))
+    old = cache.page_pool()
+    table = _ints([[4 * s + c for c in range(4)] for s in (5, 4, 3, 2)])
+    kept = cache.buf_pages.clone()
+    cache.buf_pages, cache.buf_x = table, cache.buf_x.clone()
+    was = [cache.buf_x[table.long()].clone(), cache.buf_dt[table.long()].clone()]
+    ers.fork_slots(cache, _ints([1]), _ints([0]))
+    assert cache.page_pool() is not old and cache.page_pool() is cache.page_pool()
+    assert cache.buf_pages[0].tolist() == [0, 1, 2, 3] and torch.equal(old.table, kept)
+    for t, rows in zip((cache.buf_x, cache.buf_dt), was):
+        now = t[cache.buf_pages.long()]
+        for slot, source in enumerate((1, 1, 2, 3)):
+            assert torch.equal(now[slot].view(torch.uint8), rows[source].view(torch.uint8))
