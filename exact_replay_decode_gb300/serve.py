@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
-from typing import List, Optional, Sequence, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -53,10 +53,15 @@ class PagePool:
     arrays: contiguous tensors whose first dimension is the page (the same number in all of them); one page
     index addresses all of them.  table [nslots, slot_pages] int32: the pages of each slot, -1 where it has
     none.  refs [npages] int32: how many table entries name a page; counted from the table when not given.
-    The pool keeps and changes these tensors; from then on pages change hands through the pages_* calls."""
+    The pool keeps and changes these tensors (and cannot be given others: its calls go by where they are); from then on pages
+    change hands through the pages_* calls."""
+
+    arrays = property(lambda self: self._arrays)
+    table = property(lambda self: self._table)
+    refs = property(lambda self: self._refs)
 
     def __init__(self, arrays: Sequence[torch.Tensor], table: torch.Tensor, refs: Optional[torch.Tensor] = None):
-        self.arrays: List[torch.Tensor] = list(arrays)
+        self._arrays: Tuple[torch.Tensor, ...] = tuple(arrays)
         if not 0 < len(self.arrays) <= _abi.PAGE_ARRAYS_MAX:
             raise ValueError(f"a pool has 1 to {_abi.PAGE_ARRAYS_MAX} arrays, got {len(self.arrays)}")
         if table.dim() != 2:
@@ -74,7 +79,7 @@ class PagePool:
             _need(x, x.dtype, f"arrays[{k}]")
             if x.shape[0] != npages:
                 raise ValueError(f"arrays[{k}]: {x.shape[0]} pages, expected {npages}")
-        self.table, self.refs = table, refs
+        self._table, self._refs = table, refs
         self.npages, (self.nslots, self.slot_pages) = npages, table.shape
         self._c = ctypes.byref(_pool_c(self.arrays, table, refs))
         # scratch of the calls on this pool, which have to follow one another anyway
@@ -206,7 +211,11 @@ def fork_slots(cache: ReplayCache, src: torch.Tensor, dst: torch.Tensor, status:
 class LinAttnCache:
     """The states of a linear-attention layer: pages of state [npages, H, dv, dk] fp32 under a table of one page per
     slot (pages: a PagePool).  npages None: as many as slots, slot s starting out with page s (zeros).  Otherwise
-    every page starts out free, and pages_own(cache.pages, slots) hands them out.  state: a tensor to use as the pages."""
+    every page starts out free, and pages_own(cache.pages, slots) hands them out.  state: a tensor to use as the pages (it
+    stays the cache's; another one is another cache)."""
+
+    state = property(lambda self: self._state)
+    pages = property(lambda self: self._pages)
 
     def __init__(self, nslots: int, nheads: int, ngroups: int, dk: int = 128, dv: int = 128,
                  npages: Optional[int] = None, io_dtype: torch.dtype = torch.bfloat16, device="cuda",
@@ -217,13 +226,13 @@ class LinAttnCache:
         if state is None:
             state = torch.zeros(shape, dtype=torch.float32, device=device)
         _need(state, torch.float32, "state", shape)
-        self.state = state
+        self._state = state
         if npages is None:
             table = torch.arange(nslots, dtype=torch.int32, device=state.device).view(nslots, 1)
         else:
             table = torch.full((nslots, 1), -1, dtype=torch.int32, device=state.device)
         refs = torch.full((self.npages,), int(npages is None), dtype=torch.int32, device=state.device)
-        self.pages = PagePool([state], table, refs)
+        self._pages = PagePool([state], table, refs)
         self._c = ctypes.byref(_abi.LinAttnCache(state.data_ptr(), table.data_ptr(), nslots, self.npages))
 
     def nbytes(self) -> int:

@@ -399,3 +399,17 @@ def test_page_pool_follows_replaced_tensors():
         now = t[cache.buf_pages.long()]
         for slot, source in enumerate((1, 1, 2, 3)):
             assert torch.equal(now[slot].view(torch.uint8), rows[source].view(torch.uint8))
+
+
+def test_tensors_of_a_pool_or_a_state_cache_cannot_be_replaced():
+    """Their calls go by where the tensors are, so another one would be passed over in silence."""
+    ers = _ers()
+    cache = ers.LinAttnCache(2, 2, 2)
+    for name in ("state", "pages"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name))
+    for name in ("table", "refs", "arrays"):
+        with pytest.raises(AttributeError):
+            setattr(cache.pages, name, getattr(cache.pages, name))
+    with pytest.raises(TypeError):
+        cache.pages.arrays[0] = cache.state.clone()
