@@ -17,8 +17,8 @@
 // bf16 term would cost half as much again as that rounding) and states all 24.  The state stays in tensor memory in
 // fp32 from chunk to chunk.
 //
-// Measured (128 x 128, kernel alone): 97 tokens x 32 heads 10.5 us, 2048 x 32 33, 32768 x 32 299 (40 % of the measured
-// bandwidth), 4096 x 128 119 (46 %; tensor pipe 49 % busy).
+// Measured (128 x 128, kernel alone): 97 tokens x 32 heads 9.5 us (13.5 from given states), 2048 x 32 33, 32768 x 32 303 (39 % of
+// the measured bandwidth), 4096 x 128 112 (54 %; tensor pipe 49 % busy).
 //
 // What bounds it: at one CTA per SM a chunk moves 128 KB (2.9 us of an SM's share of the memory), 64 MMAs of 64 cycles
 // and some 2500 issue slots of operand making per scheduler, in one dependent loop through the state.  So the warps are

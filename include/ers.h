@@ -596,7 +596,7 @@ ERS_API ers_status ers_pages_copy(const ers_page_pool* pool, int32_t n, const in
 /* ---------------------------------------------------------------------------------------------
  * Log probabilities of given tokens, with the distribution's entropy and its top alternatives: what a draft, a
  * branch or a sample is scored by.  Per row r of logits [nrows, vocab] (row_stride elements apart; bf16 or
- * fp32), with m = max_j x_j, d_j = scale (x_j - m), z = sum_j exp(d_j), in fp32:
+ * fp32), with m = max_j x_j, d_j = scale (x_j - m), z = sum_j exp(d_j), in fp32 (exponentials to 2 units in the last place):
  *     logprob[r]      = d_target - log z
  *     entropy[r]      = log z - sum_j exp(d_j) d_j / z                          (nats)
  *     top_id[r][0..k) = the k highest logits, highest first, the lowest index first among equals
