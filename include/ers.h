@@ -487,8 +487,10 @@ ERS_API ers_status ers_conv1d_update(const ers_conv_dims* dims, int32_t nseq, co
  *   page, so a sequence that was forked goes on from its parent's page into its own with no copy in between.  Within
  *   a call no slot's own page may be another sequence's own page or read page.  Decode takes one token per sequence.
  * A NaN or infinity in a token reaches that token and later ones of its sequence and no others.
- * Precision: states are fp32 sums of terms of 24 bits.  In bf16 prompts the masked scores and the state that a chunk's outputs are
- *   formed from are rounded to 16 bits, which the outputs' own rounding to 8 hides; elsewhere operands keep their bits.
+ * Precision: states are fp32 sums of terms of 24 bits.  bf16 prompts add them on the tensor cores, which cut a sum's 25th bit off
+ *   24 times in 128 tokens: a state is low by 1e-6 of itself where it remembers 256 tokens, 5e-6 at 4096 and 6e-5 at 32768 (fp32
+ *   prompts and single tokens round to nearest: 1e-6 at 4096).  In bf16 prompts the masked scores and the state that a chunk's
+ *   outputs are formed from are rounded to 16 bits, which the outputs' own rounding to 8 hides; elsewhere operands keep theirs.
  * Range: a prompt's sums are held at levels that differ from the results' by up to E = exp(64 |a|), |a| <= 1 (bf16), or exp(16 |a|)
  *   (fp32).  Products (q.k) v above 3e38 / E may overflow to infinity (a = -1: 5e10; fp32: 4e31).  Small ones keep their 16 (24)
  *   bits down to 2^-117 E (2^-126 E) and an absolute error of 2^-134 E (2^-150 E) below: scores and states of bf16 prompts under

@@ -125,6 +125,21 @@ def test_extreme_scales(io, power):
         _check(o * 2.0 ** -power, fin, q, k, v, decay, [n], init)
 
 
+@pytest.mark.parametrize("sign", ["any", "positive"])
+def test_states_that_forget_little(sign):
+    """A prompt's state is added up by 24 truncated sums in 128 tokens, each off by at most 2^-23 of the sum so far."""
+    T = 8192
+    q, k, v, _ = _inputs(21, T, 4, 1, 128, 128, BF16)
+    if sign == "positive":
+        k, v = k.abs(), v.abs()
+    decay = torch.tensor([0.0, -1e-5, -1e-4, -1e-3], device="cuda")
+    o, fin = _ers().linattn_fwd(q, k, v, decay)
+    oe, se = _recurrence(q, k, v, decay, [T])
+    for h in range(4):
+        assert _norm(fin[0, h], se[0, h]) <= T * 24 / 128 * 2.0 ** -23 + 2e-6
+    assert _norm(o, oe) <= 2.2e-3
+
+
 @pytest.mark.parametrize("power", [-20, -30, -40])
 def test_small_values(power):
     """States of 1e-6 to 1e-12.  With E = exp(64 |a|), operands (scores, states) of bf16 prompts are off by 2^-134 E besides their
