@@ -311,6 +311,28 @@ def test_prefill_and_decode_through_the_cache():
 
 @pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
 @pytest.mark.parametrize("io", [BF16, F32], ids=["bf16", "f32"])
+def test_prompts_on_the_cache_have_the_bits_of_prompts_alone(dk, dv, io):
+    """Every shape and type, from other slots' pages, zeros or the slot's own, into scattered pages."""
+    ers = _ers()
+    H, G, lens = 6, 2, [150, 0, 40, 1]
+    cache = ers.LinAttnCache(6, H, G, dk, dv, npages=9, io_dtype=io)
+    cache.state.copy_(torch.randn(cache.state.shape, device="cuda", generator=_gen(7)))
+    cache.pages.table.copy_(torch.tensor([[7], [1], [0], [5], [3], [8]], dtype=torch.int32))
+    slots = torch.tensor([4, 0, 2, 5], dtype=torch.int32, device="cuda")       # pages 3, 7, 0 and 8
+    q, k, v, decay = _inputs(dk + dv, sum(lens), H, G, dk, dv, io)
+    for read in ([5, 6, -1, 8], None):
+        before = cache.state.clone()
+        init = torch.stack([before[p] if p >= 0 else torch.zeros_like(before[0]) for p in (read or [3, 7, 0, 8])])
+        o = ers.linattn_prefill(cache, q, k, v, decay, _cu(lens), slots, max_seqlen=150,
+                                read_page=None if read is None else torch.tensor(read, dtype=torch.int32, device="cuda"))
+        want, fin = ers.linattn_fwd(q, k, v, decay, _cu(lens), init_state=init, max_seqlen=150)
+        assert torch.equal(o, want) and torch.equal(cache.state[[3, 7, 0, 8]], fin)
+        assert torch.equal(cache.state[[1, 2, 4, 5, 6]], before[[1, 2, 4, 5, 6]])
+        _check(o, fin, q, k, v, decay, lens, init)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("io", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("B,H", [(1, 2), (7, 6), (200, 4)])
 def test_decode_matches_the_recurrence(B, H, dk, dv, io):
     ers = _ers()
