@@ -45,7 +45,8 @@ EXPORTS = (
     "ers_spec_verify_exact_workspace_size", "ers_spec_verify_exact", "ers_commit_exact",
     "ers_linattn_fwd", "ers_linattn_prefill", "ers_linattn_decode", "ers_pages_fork", "ers_pages_own_workspace_size",
     "ers_pages_own", "ers_pages_clone", "ers_pages_free", "ers_pages_compact_workspace_size", "ers_pages_compact", "ers_pages_copy",
-    "ers_token_logprobs",
+    "ers_token_logprobs", "ers_gdn_fwd_workspace_size", "ers_gdn_fwd", "ers_gdn_prefill", "ers_gdn_decode",
+    "ers_attn_verify_workspace_size", "ers_attn_verify", "ers_attn_append", "ers_attn_commit",
 )
 
 
@@ -102,6 +103,17 @@ class LinAttnCache(ctypes.Structure):
                 ("npages", ctypes.c_int32)]
 
 
+class AttnDims(ctypes.Structure):
+    _fields_ = [("nheads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class AttnCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("nslots", ctypes.c_int32), ("slot_pages", ctypes.c_int32),
+                ("npages", ctypes.c_int32), ("page_tokens", ctypes.c_int32)]
+
+
 class PagePool(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("nslots", ctypes.c_int32),
                 ("slot_pages", ctypes.c_int32), ("npages", ctypes.c_int32), ("narrays", ctypes.c_int32),
@@ -122,6 +134,8 @@ _CACHE = ctypes.POINTER(Cache)
 _LDIMS = ctypes.POINTER(LinAttnDims)
 _LCACHE = ctypes.POINTER(LinAttnCache)
 _POOL = ctypes.POINTER(PagePool)
+_ADIMS = ctypes.POINTER(AttnDims)
+_ACACHE = ctypes.POINTER(AttnCache)
 
 _SIGS = {
     "ers_status_str": ([_I32], ctypes.c_char_p),
@@ -159,6 +173,14 @@ _SIGS = {
     "ers_pages_compact": ([_POOL, _P, _P, _P, _SZ, _P, _P], _I32),
     "ers_pages_copy": ([_POOL, _I32, _P, _P, _P, _P], _I32),
     "ers_token_logprobs": ([_I32, _I32, _I32, _I64, _P, _P, ctypes.c_float, _I32, _P, _P, _P, _P, _P, _P], _I32),
+    "ers_gdn_fwd_workspace_size": ([_LDIMS, _I32, _I64, _I32], _SZ),
+    "ers_gdn_fwd": ([_LDIMS, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I32),
+    "ers_gdn_prefill": ([_LDIMS, _LCACHE, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I32),
+    "ers_gdn_decode": ([_LDIMS, _LCACHE, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P], _I32),
+    "ers_attn_verify_workspace_size": ([_ADIMS, _I32, _I32, _I32], _SZ),
+    "ers_attn_verify": ([_ADIMS, _ACACHE, _I32, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I32),
+    "ers_attn_append": ([_ADIMS, _ACACHE, _I32, _I64, _P, _P, _P, _P, _P, _P], _I32),
+    "ers_attn_commit": ([_ADIMS, _ACACHE, _I32, _P, _I32, _P, _P, _P, _P, _P, _P], _I32),
     "ers_gdn_refresh": ([ctypes.POINTER(GdnDims), ctypes.POINTER(GdnCache), _I32, _P, _I32, _P, _P], _I32),
 }
 

@@ -231,6 +231,68 @@ cudaError_t pages_free(const PageArgs& a, cudaStream_t s);
 cudaError_t pages_compact(const PageArgs& a, cudaStream_t s);          // ws: 1 + 2 npages
 cudaError_t pages_copy(const PageArgs& a, cudaStream_t s);
 
+// the gated delta rule over states, ers_gdn_state.cu
+struct DeltaArgs {
+  int H, G, dk, dv, io;
+  float scale;
+  int nseq, max_len;
+  long long ntokens;
+  const int32_t* cu;        // prompts: [nseq + 1]
+  const void* q;            // [T, G, dk]
+  const void* k;
+  const void* v;            // [T, H, dv]
+  const float* g;           // [T, H]
+  const float* beta;
+  void* o;
+  // states by sequence (init may be null: zeros) ...
+  const float* init;
+  float* final_state;
+  // ... or in the pages of a pool (pool not null)
+  float* pool;              // [npages, H, dv, dk]
+  const int32_t* table;     // [nslots] page of a slot
+  const int32_t* slot;
+  const int32_t* read_page;
+  int nslots, npages;
+  void* ws;
+  int32_t* status;
+};
+cudaError_t gdn_fwd(const DeltaArgs& a, cudaStream_t s);      // prompts
+cudaError_t gdn_decode(const DeltaArgs& a, cudaStream_t s);   // one token per sequence
+size_t gdn_fwd_workspace(const DeltaArgs& a);                 // (by io, H, dk, dv, nseq, ntokens, max_len)
+
+// attention over a paged cache of keys and values, ers_attn.cu
+struct AttnArgs {
+  int H, KV, D, io;
+  float scale;
+  int nseq, T;
+  int nsplit;               // CTAs that share a sequence's past,
+  int per;                  // tokens of each (the last: to the end)
+  const void* q;            // [nseq, T, H, D]
+  const void* k;            // new rows: [nseq, T, KV, D], or packed [ntokens, KV, D]
+  const void* v;
+  const int32_t* parent;    // [nseq, T] or null: a chain
+  void* o;
+  void* k_pages;            // [npages, page_tokens, KV, D]
+  void* v_pages;
+  const int32_t* table;     // [nslots, slot_pages]
+  const int32_t* refs;      // [npages]
+  int32_t* pos;             // [nslots]
+  int nslots, slot_pages, npages, page_tokens;
+  const int32_t* slot;
+  float* part;              // nsplit > 1: [nseq, T, H, nsplit] (max, sum), then [nseq, T, H, nsplit, D] outputs
+  const int32_t* cu;        // append: [nseq + 1]
+  long long ntokens;
+  const int32_t* path;      // commit: [nseq, T] or null: the first drafts
+  const int32_t* accepted;  // [nseq]
+  int32_t* status;
+};
+constexpr int kMaxDrafts = 64;
+void attn_plan(AttnArgs* a, int max_len);                       // nsplit and per
+size_t attn_workspace(const AttnArgs& a);
+cudaError_t attn_verify(const AttnArgs& a, cudaStream_t s);
+cudaError_t attn_append(const AttnArgs& a, cudaStream_t s);
+cudaError_t attn_commit(const AttnArgs& a, cudaStream_t s);
+
 // log probabilities of given tokens, ers_logprobs.cu
 struct LogprobArgs {
   int io, nrows, vocab, top_k;

@@ -530,6 +530,99 @@ ERS_API ers_status ers_linattn_decode(const ers_linattn_dims* dims, const float*
                                       ers_stream_t stream, int32_t* dev_status);
 
 /* ---------------------------------------------------------------------------------------------
+ * The gated delta rule over states: prompts and single tokens of a GDN layer (ers_gdn_verify's rule, with a scale).  Per
+ * head h (key group h / (H/G)), token t, a_t = exp(g_t):
+ *     u_t = beta_t (v_t - a_t S k_t),   S <- a_t S + u_t k_t^T   (S is [dv x dk], fp32),   o_t = scale * S q_t
+ *
+ *   dims, cache, slot, read_page, cu_seqlens, max_seqlen: as for linear attention (the state is laid out as the GDN anchors
+ *     are: a final state may be copied into ers_gdn_cache.anchor, and its bf16 cast into read_copy).
+ *   q, k [T, G, dk], v, o [T, H, dv] in the io dtype, g (log of the gate, <= 0), beta [T, H] fp32.  The rule forgets as long as
+ *     beta |k|^2 <= 2; beyond that states grow, as they do in exact arithmetic.
+ *   workspace: a 16-byte aligned buffer of the size that the query returns for the call's sizes (may be 0: then NULL will do).
+ * ers_gdn_fwd: prompts from init_state [nseq, H, dv, dk] (NULL: zeros) to final_state (may be init_state itself).
+ * ers_gdn_prefill / ers_gdn_decode: states in the pages of a pool, prompts or one token per sequence.
+ * A NaN or infinity in a token reaches that token and later ones of its sequence and no others.
+ * Device errors: ERS_ESLOT, ERS_EINVAL as for linear attention: the sequence's outputs are then left unwritten;
+ *   ERS_ETIMEOUT: they are undefined. */
+ERS_API size_t ers_gdn_fwd_workspace_size(const ers_linattn_dims* dims, int32_t nseq, int64_t ntokens, int32_t max_seqlen);
+ERS_API ers_status ers_gdn_fwd(const ers_linattn_dims* dims, int32_t nseq, int64_t ntokens, int32_t max_seqlen,
+                               const int32_t* cu_seqlens, const void* q, const void* k, const void* v, const float* g,
+                               const float* beta, const float* init_state, void* o, float* final_state, void* workspace,
+                               size_t workspace_bytes, ers_stream_t stream, int32_t* dev_status);
+
+/* (the workspace of ers_gdn_fwd for the same sizes) */
+ERS_API ers_status ers_gdn_prefill(const ers_linattn_dims* dims, const ers_linattn_cache* cache, int32_t nseq,
+                                   int64_t ntokens, int32_t max_seqlen, const int32_t* cu_seqlens, const int32_t* slot,
+                                   const int32_t* read_page, const void* q, const void* k, const void* v, const float* g,
+                                   const float* beta, void* o, void* workspace, size_t workspace_bytes,
+                                   ers_stream_t stream, int32_t* dev_status);
+
+ERS_API ers_status ers_gdn_decode(const ers_linattn_dims* dims, const ers_linattn_cache* cache, int32_t nseq,
+                                  const int32_t* slot, const int32_t* read_page, const void* q, const void* k,
+                                  const void* v, const float* g, const float* beta, void* o, ers_stream_t stream,
+                                  int32_t* dev_status);
+
+/* ---------------------------------------------------------------------------------------------
+ * Attention of a tree of drafts over a paged cache: the attention layers of a hybrid under speculation.  Outputs only, as
+ * ers_spec_verify: the drafts' own keys and values come with the call, and the cache receives what is accepted.
+ *
+ *   dims: head_dim D 64 or 128, nheads % kv_heads == 0 (heads of a group share a head of keys), io_dtype for
+ *     q, k, v, o and the pages; scale multiplies the products q.k in fp32.
+ *   cache: k, v [npages, page_tokens, kv_heads, D]; table [nslots, slot_pages] the pages of a slot in the order of its
+ *     tokens (-1: none), refs [npages] as for the page calls (k and v are arrays of such a pool); pos [nslots] tokens in use.
+ * ers_attn_verify: T drafts per sequence (1 <= T <= 64), q, o [nseq, T, H, D], k, v [nseq, T, kv_heads, D].  parent [nseq, T]
+ *   (NULL: a chain): the place of the draft that a draft follows, one before its own; -1: it follows the slot's last token;
+ *   -2: the place is empty, its output zeros.  A draft attends to the slot's pos tokens, the drafts of its path and itself:
+ *     o = sum_j softmax_j(scale q.k_j) v_j,  in fp32 with one rounding at the end (bf16: the weights are rounded to bf16 once,
+ *   relative to the largest).  What is not attended to may hold anything: other drafts, what pages hold behind pos.
+ *   A NaN or infinity in a draft's v makes the outputs of its path from there on NaN.  A row whose every product is -inf has zeros.
+ *   max_len: the most tokens of any slot as the caller knows it (>= 0): it chooses how the work is split, never what is
+ *   computed; a split changes the order of fp32 sums.  workspace: 16-byte aligned, of the size that the query returns.
+ * ers_attn_append: rows of packed new tokens, k, v [ntokens, kv_heads, D] by cu_seqlens [nseq+1], go behind their
+ *   slots' tokens and pos moves on.
+ * ers_attn_commit: of k, v [nseq, T, kv_heads, D], the drafts path[i][0 .. accepted[i]) (NULL: 0, 1, ...) go behind the slot's
+ *   tokens and pos moves on.  path [nseq, T].
+ *   Both: a page that receives rows has to be the slot's alone (refs 1), and slots within a call are distinct.  A sequence
+ *   that has an error is left as it was.
+ * Device errors: ERS_ESLOT (slot, or a page outside [0, npages): a verify's outputs are then undefined), ERS_EALIGN (pos
+ *   outside the table), ERS_EINVAL (a parent that is neither an earlier place in use nor -1 or -2; a shared page or a
+ *   slot listed twice; cu_seqlens not ascending within [0, ntokens]: nothing is appended at all), ERS_EOVERFLOW (no room in
+ *   the table), ERS_ECOMMIT (accepted outside [0, T], a path outside [0, T)). */
+typedef struct ers_attn_dims {
+  int32_t nheads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t io_dtype;
+  float scale;
+} ers_attn_dims;
+
+typedef struct ers_attn_cache {
+  void* k;
+  void* v;
+  const int32_t* table;
+  const int32_t* refs;
+  int32_t* pos;
+  int32_t nslots;
+  int32_t slot_pages;
+  int32_t npages;
+  int32_t page_tokens;
+} ers_attn_cache;
+
+ERS_API size_t ers_attn_verify_workspace_size(const ers_attn_dims* dims, int32_t nseq, int32_t T, int32_t max_len);
+ERS_API ers_status ers_attn_verify(const ers_attn_dims* dims, const ers_attn_cache* cache, int32_t nseq,
+                                   const int32_t* slot, int32_t T, int32_t max_len, const void* q, const void* k,
+                                   const void* v, const int32_t* parent, void* o, void* workspace,
+                                   size_t workspace_bytes, ers_stream_t stream, int32_t* dev_status);
+
+ERS_API ers_status ers_attn_append(const ers_attn_dims* dims, const ers_attn_cache* cache, int32_t nseq, int64_t ntokens,
+                                   const int32_t* cu_seqlens, const int32_t* slot, const void* k, const void* v,
+                                   ers_stream_t stream, int32_t* dev_status);
+
+ERS_API ers_status ers_attn_commit(const ers_attn_dims* dims, const ers_attn_cache* cache, int32_t nseq,
+                                   const int32_t* slot, int32_t T, const int32_t* path, const int32_t* accepted,
+                                   const void* k, const void* v, ers_stream_t stream, int32_t* dev_status);
+
+/* ---------------------------------------------------------------------------------------------
  * Pages of a cache: counted references to the pages of a pool, under a table of pages per slot.
  *
  *   table [nslots, slot_pages] int32: the pages of a slot, -1 where it has none; refs [npages] int32: how many
