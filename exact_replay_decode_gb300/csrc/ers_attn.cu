@@ -8,12 +8,13 @@ namespace ers {
 namespace {
 
 // ---- drafts -----------------------------------------------------------------------------------------------
-// The query rows of a sequence that share a head of keys, T drafts x H/KV heads, kRows of them a CTA, each warp four; tokens
+// fp32: the query rows of a sequence that share a head of keys, T drafts x H/KV heads, kRows of them a CTA, each warp four; tokens
 // come through shared memory 32 at a time, one a lane, with a running maximum and sum a row.
 constexpr int kRows = 16, kTile = 32, kWarps = 4, kEach = kRows / kWarps;
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(32 * kWarps) k_attn_rows(const __grid_constant__ AttnArgs a) {
+  using T = float;
   constexpr int C = D / 32;                    // output columns of a lane
   __shared__ __align__(16) float sq[kRows][D];
   __shared__ __align__(16) float sk[kTile][D + 4];
@@ -185,9 +186,14 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ 
 
 template <typename T, int D>
 cudaError_t verify(const AttnArgs& a, cudaStream_t s) {
-  const int tiles = (a.T * (a.H / a.KV) + kRows - 1) / kRows;
-  k_attn_rows<T, D><<<dim3((unsigned)(a.nseq * a.nsplit), tiles * a.KV), 32 * kWarps, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (a.io == ERS_DTYPE_BF16) {
+    e = attn_tiles(a, s);
+  } else {
+    const int tiles = (a.T * (a.H / a.KV) + kRows - 1) / kRows;
+    k_attn_rows<D><<<dim3((unsigned)(a.nseq * a.nsplit), tiles * a.KV), 32 * kWarps, 0, s>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess || a.nsplit == 1) return e;
   const size_t rows = (size_t)a.nseq * a.T * a.H, each = kThreads / 32;
   k_attn_join<T, D><<<(unsigned)((rows + each - 1) / each), kThreads, 0, s>>>(a);
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_commit(const __grid_constant_
 }  // namespace
 
 void attn_plan(AttnArgs* a, int max_len) {
-  const int tiles = (a->T * (a->H / a->KV) + kRows - 1) / kRows;
+  const int each = a->io == ERS_DTYPE_BF16 ? 128 : kRows, tiles = (a->T * (a->H / a->KV) + each - 1) / each;
   const long long units = (long long)a->nseq * a->KV * tiles;
   const long long blocks = (max_len + 255) / 256;
   long long n = 608 / (units < 1 ? 1 : units);

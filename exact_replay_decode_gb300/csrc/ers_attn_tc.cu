@@ -1,0 +1,352 @@
+// Attention of drafts over a paged cache, bf16, on the tensor cores.
+//
+// A CTA takes 128 query rows that share a head of keys (drafts x heads of the group; the rest of the tile is zeros) and a run of
+// the sequence's past, in tiles of 64 tokens, then the drafts themselves:
+//   S = Q K^T   (A, B from shared memory)      P = exp(c S - m), rounded to bf16, over S in tensor memory
+//   O += P V    (A from tensor memory)         l += sum P, of the rounded ones: O / l is an average of values
+// with c = scale log2 e (P by powers of two) and m a running maximum that moves, and O with it, only when a row's maximum has
+// risen by more than 2^8: P then stays below 2^8, which costs no bits.
+//
+// Four warps own the rows, a thread each (a tile's scores of a row stay in its registers), four load tiles (any page size:
+// 16-byte copies that fill with zeros behind the last token), one issues the MMAs: S of the next tile before P V of this one, so
+// that the tensor core works under the exponentials.  Two CTAs per SM (two stages of 32 KB each at D 128, 256 columns of tensor
+// memory) run beside each other: one loads while the other computes.
+#include <mutex>
+
+#include "attn_cache.cuh"
+#include "ers_common.cuh"
+#include "ers_internal.h"
+#include "tc_common.cuh"
+#include "tc_terms.cuh"
+
+namespace ers {
+namespace {
+
+using namespace tc;
+using bf16 = __nv_bfloat16;
+
+constexpr int kM = 128, kTokens = 64, kStages = 2;
+constexpr int kLoadThread = 128, kLoaders = 128, kIssueThread = 256, kBlock = 288;
+constexpr uint32_t kColS = 0, kColO = 128, kCols = 256;   // two tiles' scores, the outputs
+constexpr float kRise = 8.f;
+
+struct Hdr {
+  uint64_t full[kStages], empty[kStages], s_ready[2], p_ready, o_done;
+  uint64_t bad;                      // drafts whose values are not finite
+  int32_t parent[kMaxDrafts];
+  uint32_t tmem;
+  int dead;                          // a wait gave up: no further wait waits, no copy or MMA is issued
+};
+
+template <int D>
+struct Shape {
+  static constexpr uint32_t qtile = kM * D * 2, tile = kTokens * D * 2, smem = qtile + kStages * 2 * tile + sizeof(Hdr) + 1024;
+  static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+__device__ __forceinline__ bool wait(Hdr& hd, uint64_t* bar, uint32_t parity, int32_t* status) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  while (!mbar_try(bar, parity & 1u)) {
+    const uint64_t now = globaltimer();
+    if (*(volatile int*)&hd.dead != 0) return false;
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      if (status != nullptr) atomicCAS(status, 0, ERS_ETIMEOUT);
+      *(volatile int*)&hd.dead = 1;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool dead(const Hdr& hd) { return *(const volatile int*)&hd.dead != 0; }
+
+__device__ __forceinline__ float exp2_of(float x) {   // 2 units in the last place; 0 below 2^-126
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void copy16(void* to, const void* from, bool there) {   // zeros where there is nothing
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Where a bf16 pair is not finite: its exponent is all ones.
+__device__ __forceinline__ bool not_finite(uint32_t u) {
+  return (u & 0x7f800000u) == 0x7f800000u || (u & 0x7f80u) == 0x7f80u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant__ AttnArgs a) {
+  using Sh = Shape<D>;
+  extern __shared__ uint8_t attn_smem[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(attn_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t* stages = base + Sh::qtile;          // K, V, K, V
+  Hdr& hd = *reinterpret_cast<Hdr*>(stages + kStages * 2 * Sh::tile);
+  const int split = blockIdx.x % a.nsplit, i = blockIdx.x / a.nsplit, kv = blockIdx.y % a.KV, row0 = blockIdx.y / a.KV * kM;
+  const int rep = a.H / a.KV, nrows = a.T * rep, tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0);
+  const int row = row0 + tid;                  // of the threads that own rows
+  const auto out_row = [&](int r) { return ((size_t)i * a.T + r / rep) * a.H + kv * rep + r % rep; };
+  AttnSeq s;
+  int32_t err = attn_seq(a, i, &s);
+  if (a.parent != nullptr && tid < a.T) hd.parent[tid] = a.parent[(size_t)i * a.T + tid];
+  if (tid == 0) hd.bad = 0;
+  __syncthreads();
+  const int32_t* parent = a.parent != nullptr ? hd.parent : nullptr;
+  bool wrong = false;
+  if (tid < a.T) path_of(parent, tid, &wrong);
+  if (__syncthreads_or(wrong) && err == ERS_OK) err = ERS_EINVAL;
+  if (err != ERS_OK) {
+    if (tid == 0) report(a.status, err);
+    if (a.nsplit > 1 && tid < kM && row < nrows)
+      reinterpret_cast<float2*>(a.part)[out_row(row) * a.nsplit + split] = make_float2(0.f, -1.f);
+    return;
+  }
+  const bool last = split == a.nsplit - 1;
+  const long long begin = (long long)split * a.per;
+  const int end = last ? s.pos : (int)min((long long)s.pos, begin + a.per);
+  const int past = begin < end ? (int)((end - begin + kTokens - 1) / kTokens) : 0, tiles = past + (last ? 1 : 0);
+  if (tiles == 0) {                            // nothing of the past is this CTA's
+    if (tid < kM && row < nrows) reinterpret_cast<float2*>(a.part)[out_row(row) * a.nsplit + split] = make_float2(0.f, 0.f);
+    return;
+  }
+  if (warp == kIssueThread / 32) tmem_alloc(&hd.tmem, kCols);
+  if (tid == kLoadThread) {
+    for (int b = 0; b < kStages; ++b) {
+      mbar_init(&hd.full[b], kLoaders);
+      mbar_init(&hd.empty[b], 1);
+      mbar_init(&hd.s_ready[b], 1);
+    }
+    mbar_init(&hd.p_ready, kM);
+    mbar_init(&hd.o_done, 1);
+    fence_mbar_init();
+    hd.dead = 0;
+  }
+  if (tid < kM) {
+    const bf16* q = (const bf16*)a.q + (row < nrows ? out_row(row) * D : 0);
+#pragma unroll
+    for (int x = 0; x < D; x += 8)
+      *reinterpret_cast<uint4*>(base + sw128(kM, tid, x)) = row < nrows ? *reinterpret_cast<const uint4*>(q + x) : make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
+  before_sync();
+  __syncthreads();
+  after_sync();
+  const uint32_t tb = __shfl_sync(kFull, hd.tmem, 0);
+
+  if (tid >= kIssueThread) {
+    // ---- the issuing warp -------------------------------------------------------------------------------
+    constexpr uint32_t id_s = idesc_bf16(kM, kTokens, false, false), id_o = idesc_bf16(kM, D, false, true);
+    const bool leader = elected();
+    const auto scores = [&](int n) {
+      const int b = n % kStages;
+      if (!wait(hd, &hd.full[b], n / kStages, a.status)) return false;
+      after_sync();
+      fence_async_smem();
+      const uint32_t kt = smem_u32(stages + b * 2 * Sh::tile), qt = smem_u32(base);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        if (leader)
+          mma(tb + kColS + (n & 1) * kTokens, sdesc(qt + (k >> 2) * kM * 128 + (k & 3) * 32, 16, 1024),
+              sdesc(kt + (k >> 2) * kTokens * 128 + (k & 3) * 32, 16, 1024), id_s, k > 0);
+      if (leader) commit(&hd.s_ready[n & 1]);
+      return true;
+    };
+    bool ok = scores(0);
+#pragma unroll 1
+    for (int n = 0; ok && n < tiles; ++n) {
+      if (n + 1 < tiles && !scores(n + 1)) break;
+      if (!wait(hd, &hd.p_ready, n, a.status)) break;
+      after_sync();
+      const int b = n % kStages;
+      const uint64_t vd = sdesc(smem_u32(stages + b * 2 * Sh::tile + Sh::tile), kTokens * 128, 1024);
+#pragma unroll
+      for (int k = 0; k < kTokens / 16; ++k)
+        if (leader) mma_ts(tb + kColO, tb + kColS + (n & 1) * kTokens + 8 * k, vd + k * (16 * 128 / 16), id_o, n > 0 || k > 0);
+      if (leader) {
+        commit(&hd.empty[b]);
+        commit(&hd.o_done);
+      }
+    }
+  } else if (tid >= kLoadThread) {
+    // ---- the loading warps: a tile's rows by 8 (D 64) or 16 neighbouring threads --------------------------
+    constexpr int kPer = D / 8, kStep = kLoaders / kPer;
+    const int t = tid - kLoadThread, c = t % kPer * 8, r0 = t / kPer;
+    for (int n = 0; n <= tiles; ++n) {
+      if (n > 0) {                             // the tile before this one has arrived: told before any wait for its stage's turn
+        copies_wait();
+        fence_async_smem();
+        mbar_arrive(&hd.full[(n - 1) % kStages]);
+      }
+      if (n < tiles) {
+        const int b = n % kStages;
+        if (n >= kStages) wait(hd, &hd.empty[b], n / kStages - 1, a.status);
+        uint8_t *kt = stages + b * 2 * Sh::tile, *vt = kt + Sh::tile;
+        if (dead(hd)) {
+        } else if (n < past) {
+          const int t0 = (int)begin + n * kTokens;
+#pragma unroll
+          for (int x = 0; x < kTokens / kStep; ++x) {
+            const int r = r0 + x * kStep;
+            const long long at = t0 + r < end ? attn_row(a, s.pages, t0 + r) : -1;
+            if (at < 0 && t0 + r < end) report(a.status, ERS_ESLOT);
+            const size_t from = at < 0 ? 0 : ((size_t)at * a.KV + kv) * D + c;
+            copy16(kt + sw128(kTokens, r, c), (const bf16*)a.k_pages + from, at >= 0);
+            copy16(vt + sw128(kTokens, r, c), (const bf16*)a.v_pages + from, at >= 0);
+          }
+        } else {
+          // Drafts: a value that is not finite would reach rows that do not see it as 0 x infinity, so it is left out, and
+          // those that see it are made NaN at the end.
+          for (int r = r0; r < kTokens; r += kStep) {
+            uint4 k = make_uint4(0, 0, 0, 0), v = k;
+            if (r < a.T) {
+              const size_t from = (((size_t)i * a.T + r) * a.KV + kv) * D + c;
+              k = *reinterpret_cast<const uint4*>((const bf16*)a.k + from);
+              v = *reinterpret_cast<const uint4*>((const bf16*)a.v + from);
+              if (not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w)) {
+                atomicOr(reinterpret_cast<unsigned long long*>(&hd.bad), 1ull << r);
+                v = make_uint4(0, 0, 0, 0);
+              }
+            }
+            *reinterpret_cast<uint4*>(kt + sw128(kTokens, r, c)) = k;
+            *reinterpret_cast<uint4*>(vt + sw128(kTokens, r, c)) = v;
+          }
+        }
+      }
+    }
+  } else {
+    // ---- the rows -------------------------------------------------------------------------------------------
+    const float c = a.scale * 1.44269504088896340736f;
+    bool unused = false;
+    const uint64_t path = row < nrows ? path_of(parent, row / rep, &unused) : 0;
+    const uint32_t at = tb + ((uint32_t)(tid & ~31) << 16);
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int n = 0; n < tiles; ++n) {
+      wait(hd, &hd.s_ready[n & 1], n >> 1, a.status);
+      __syncwarp();
+      after_sync();
+      const uint32_t sc = at + kColS + (n & 1) * kTokens;
+      uint32_t u[2][32];
+      tmem_ld32_begin(sc, u[0]);
+      tmem_ld32_begin(sc + 32, u[1]);
+      arrived(u[0]);
+      arrived(u[1]);
+      uint64_t seen = path;
+      if (n < past) {
+        const int count = end - ((int)begin + n * kTokens);
+        seen = path == 0 ? 0 : count >= kTokens ? ~0ull : (1ull << count) - 1;
+      }
+      float top = -INFINITY;
+      if (__all_sync(kFull, seen == ~0ull)) {
+#pragma unroll
+        for (int x = 0; x < 64; ++x) {
+          const float y = __uint_as_float(u[x / 32][x % 32]) * c;
+          u[x / 32][x % 32] = __float_as_uint(y);
+          top = fmaxf(top, y);
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 64; ++x) {
+          const float y = seen >> x & 1u ? __uint_as_float(u[x / 32][x % 32]) * c : -INFINITY;
+          u[x / 32][x % 32] = __float_as_uint(y);
+          top = fmaxf(top, y);
+        }
+      }
+      // (a row that has seen nothing rises from -inf; one that still sees nothing does not)
+      const bool rise = top > m + kRise || (m == -INFINITY && top > m);
+      const float next = rise ? top : m, factor = rise ? exp2_of(m - next) : 1.f;   // from -inf: 0
+      const float down = next == -INFINITY ? 0.f : next;
+      uint32_t p[32];
+      float sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        p[x] = pack_bf16x2(exp2_of(__uint_as_float(u[x / 16][x % 16 * 2]) - down), exp2_of(__uint_as_float(u[x / 16][x % 16 * 2 + 1]) - down));
+        sum += __uint_as_float(p[x] << 16) + __uint_as_float(p[x] & 0xffff0000u);
+      }
+      l = fmaf(l, factor, sum);
+      m = next;
+      if (n > 0) {
+        wait(hd, &hd.o_done, n - 1, a.status);
+        __syncwarp();
+        after_sync();
+        if (__any_sync(kFull, rise)) {
+#pragma unroll 1
+          for (int x = 0; x < D; x += 32) {
+            uint32_t o[32];
+            tmem_ld32_begin(at + kColO + x, o);
+            arrived(o);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * factor);
+            tmem_st32(at + kColO + x, o);
+          }
+        }
+      }
+      tmem_st32(sc, p);
+      tmem_wait_st();
+      before_sync();
+      mbar_arrive(&hd.p_ready);
+    }
+    wait(hd, &hd.o_done, tiles - 1, a.status);
+    __syncwarp();
+    after_sync();
+    const bool spoiled = last && (path & *(volatile uint64_t*)&hd.bad) != 0;
+    if (spoiled) l = __int_as_float(0x7fffffff);
+    const size_t out = row < nrows ? out_row(row) : 0, part = out * a.nsplit + split, all = (size_t)a.nseq * a.T * a.H * a.nsplit;
+    if (row < nrows && a.nsplit > 1) reinterpret_cast<float2*>(a.part)[part] = make_float2(m * 0.69314718055994530942f, l);
+    const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+    for (int x = 0; x < D; x += 32) {
+      uint32_t o[32];
+      tmem_ld32_begin(at + kColO + x, o);
+      arrived(o);
+      if (row >= nrows) continue;
+      if (a.nsplit > 1) {
+        float* to = a.part + 2 * all + part * D + x;
+#pragma unroll
+        for (int y = 0; y < 32; y += 4) *reinterpret_cast<uint4*>(to + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+      } else {
+        bf16* to = (bf16*)a.o + out * D + x;
+        uint32_t w[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y)
+          w[y] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
+#pragma unroll
+        for (int y = 0; y < 16; y += 4) *reinterpret_cast<uint4*>(to + 2 * y) = make_uint4(w[y], w[y + 1], w[y + 2], w[y + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  if (tid == kIssueThread && dead(hd)) {       // no MMA may be left in flight: 2 ms are a thousand times what one takes
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000) {}
+  }
+  before_sync();
+  __syncthreads();
+  if (warp == kIssueThread / 32) tmem_dealloc(tb, kCols);
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      e = cudaFuncSetAttribute(k_attn_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::smem);
+      if (e != cudaSuccess) return e;
+      done[dev] = true;
+    }
+  }
+  const int tiles = (a.T * (a.H / a.KV) + kM - 1) / kM;
+  k_attn_tiles<D><<<dim3((unsigned)(a.nseq * a.nsplit), tiles * a.KV), kBlock, Shape<D>::smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attn_tiles(const AttnArgs& a, cudaStream_t s) { return a.D == 64 ? launch<64>(a, s) : launch<128>(a, s); }
+
+}  // namespace ers

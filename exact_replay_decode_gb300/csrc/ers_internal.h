@@ -290,6 +290,7 @@ constexpr int kMaxDrafts = 64;
 void attn_plan(AttnArgs* a, int max_len);                       // nsplit and per
 size_t attn_workspace(const AttnArgs& a);
 cudaError_t attn_verify(const AttnArgs& a, cudaStream_t s);
+cudaError_t attn_tiles(const AttnArgs& a, cudaStream_t s);      // verify's rows on the tensor cores (bf16), ers_attn_tc.cu
 cudaError_t attn_append(const AttnArgs& a, cudaStream_t s);
 cudaError_t attn_commit(const AttnArgs& a, cudaStream_t s);
 
