@@ -225,7 +225,12 @@ cudaError_t decode(const DeltaArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// bf16 prompts of more tokens than these go by chunks.
+constexpr int kFewTokens = 24;
+static bool by_chunks(const DeltaArgs& a) { return a.io == ERS_DTYPE_BF16 && a.max_len > kFewTokens; }
+
 cudaError_t gdn_fwd(const DeltaArgs& a, cudaStream_t s) {
+  if (by_chunks(a)) return gdn_tc(a, s);
   if (a.io == ERS_DTYPE_BF16) return a.dk == 64 ? steps<__nv_bfloat16, 64>(a, s) : steps<__nv_bfloat16, 128>(a, s);
   return a.dk == 64 ? steps<float, 64>(a, s) : steps<float, 128>(a, s);
 }
@@ -235,6 +240,6 @@ cudaError_t gdn_decode(const DeltaArgs& a, cudaStream_t s) {
   return a.dk == 64 ? decode<float, 64>(a, s) : decode<float, 128>(a, s);
 }
 
-size_t gdn_fwd_workspace(const DeltaArgs&) { return 0; }
+size_t gdn_fwd_workspace(const DeltaArgs& a) { return by_chunks(a) ? gdn_tc_workspace(a) : 0; }
 
 }  // namespace ers

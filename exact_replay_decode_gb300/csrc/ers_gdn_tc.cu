@@ -1,0 +1,688 @@
+// The gated delta rule over prompts in chunks of 64 tokens, bf16, on the tensor cores.
+//
+// With G_i the sum of a chunk's log-gates up to token i, S the state before it and C its last token:
+//   A_ij = beta_i e^(G_i - G_j) k_i.k_j (j < i),   T = (I + A)^-1,   T' = T diag(beta)
+//   W = T' diag(e^G) K,   U0 = T' V,   M_ij = e^(G_i - G_j) q_i.k_j (j <= i)            of the chunk alone
+//   U = U0 - W S^T,   O = scale (diag(e^G) Q S^T + M U),   S <- e^(G_C) S + (diag(e^(G_C - G)) U)^T K   through the state
+// Differences of G are taken between sums held as two floats, so that no gate, however strong, costs the others bits; every
+// exponent is <= 0.  The first line depends on no other chunk: k_gdn_inside forms it for all chunks at once, a CTA for a chunk and
+// head, and leaves W, M (as two bf16 terms), U0 (fp32) and the factors in the workspace, with Q and K as padded operand tiles.
+// k_gdn_through walks a sequence's chunks, a CTA for 64 rows of a head's state.
+//
+// Precision: q, k and v are exact operands.  T' is taken as three bf16 terms (24 bits); W, S, M, U and the decayed U as
+// two (16 bits and more: each is off by at most 2^-17, in the mean 2^-18.7; a third term of all of them would double the products of the
+// serial loop).  The state itself is fp32 in registers, one rounded multiply-add a chunk.
+#include <mutex>
+
+#include "ers_common.cuh"
+#include "ers_internal.h"
+#include "gdn_rule.cuh"
+#include "tc_common.cuh"
+#include "tc_terms.cuh"
+
+namespace ers {
+namespace {
+
+using namespace tc;
+using bf16 = __nv_bfloat16;
+
+constexpr int kC = 64;                       // tokens of a chunk
+constexpr int kPart = 64;                    // state rows of a CTA
+constexpr uint32_t kAtom = kC * 128;         // 64 rows of 64 bf16 columns
+constexpr float kLeast = -200.f;             // a lower log-gate is e^-200 = 0 in fp32 as well
+
+// The factors of a chunk.
+struct Factors {
+  float since[kC];                           // e^(G_i)
+  float left[kC];                            // e^(G_C - G_i)
+  float whole;                               // e^(G_C)
+  int bad;                                   // the first token with something that is not finite (kC: none)
+  float pad[126];
+};
+static_assert(sizeof(Factors) == 1024, "whole copies");
+
+// What k_gdn_inside leaves of a chunk: a block for each head, and Q and K for each group.
+struct Layout {
+  uint32_t w, m, f, u, head;                 // offsets of W (hi, lo), M (hi, lo), factors, U0 [64, dv]; bytes of a block
+  uint32_t group;                            // bytes of Q, then K
+  size_t chunk;                              // bytes of a chunk's: heads, then groups
+  __host__ __device__ Layout(int H, int G, int dk, int dv) {
+    w = 0;
+    m = 2 * kC * dk * 2;
+    f = m + 2 * kAtom;
+    u = f + (uint32_t)sizeof(Factors);
+    head = u + kC * dv * 4;
+    group = 2 * kC * dk * 2;
+    chunk = (size_t)H * head + (size_t)G * group;
+  }
+};
+
+// Sequence i's chunks are numbers t0 / kC + i on: as many as there can be lie between those of two neighbours.
+__host__ __device__ __forceinline__ long long chunk_numbers(long long ntokens, int nseq) { return ntokens / kC + nseq; }
+
+// Whether the sequences' borders ascend within [0, ntokens], all of them: chunks are found by them.  By all threads.
+__device__ __forceinline__ bool ascending(const DeltaArgs& a) {
+  bool ok = true;
+  for (int x = threadIdx.x; x < a.nseq; x += blockDim.x) {
+    const int t0 = a.cu[x], t1 = a.cu[x + 1];
+    ok &= 0 <= t0 && t0 <= t1 && t1 <= a.ntokens;
+  }
+  return __syncthreads_and(ok);
+}
+
+__device__ __forceinline__ bool not_finite(uint4 v) {
+  const auto bad = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u || (u & 0x7f80u) == 0x7f80u; };
+  return bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
+}
+
+// 32 fp32 values as N bf16 terms: word j of term n holds values 2 j and 2 j + 1.
+template <int N>
+__device__ __forceinline__ void terms_of(const float (&v)[32], uint32_t (&t)[N][16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    uint64_t p = pair(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) t[n][j] = n == N - 1 ? round2(p) : take_term(p);
+  }
+}
+// 32 columns of a row of an operand tile
+__device__ __forceinline__ void row_to(uint8_t* tile, uint32_t rows, uint32_t r, uint32_t x, const uint32_t (&t)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 4)
+    *reinterpret_cast<uint4*>(tile + sw128(rows, r, x + 2 * j)) = make_uint4(t[j], t[j + 1], t[j + 2], t[j + 3]);
+}
+__device__ __forceinline__ void tmem_values(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  tmem_ld32_begin(at, r);
+  arrived(r);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+}
+
+// ---- inside the chunks ------------------------------------------------------------------------------------------
+// Two CTAs per SM: one's exponentials and substitutions under the other's products.
+constexpr int kInside = 128, kLd = kC + 1;
+constexpr uint32_t kColD = 0, kColT = 128, kInsideCols = 256;
+
+template <int DK, int DV>
+struct InsideSmem {
+  alignas(1024) uint8_t qk[2 * kC * DK * 2];   // rows 0-63 Q, 64-127 K
+  alignas(1024) uint8_t v[kC * DV * 2];
+  float a[kC][kLd], t[kC][kLd], x[32][33];
+  float hi[kC], lo[kC], beta[kC], since[kC];
+  uint64_t bar;
+  uint32_t tmem;
+  int bad;
+};
+
+// T's block at (r0, c0), s x s, below two diagonal blocks that are done: -T22 (A21 T11).  n products side by side, the next
+// pair of blocks 2 s further on; thread by thread `each` neighbouring columns of a row.
+template <int s, int pairs>
+__device__ __forceinline__ void join_blocks(float (&a)[kC][kLd], float (&t)[kC][kLd], float (&x)[32][33]) {
+  constexpr int each = pairs * s * s / kInside, per = s / each;   // threads of a row
+  const int p = threadIdx.x / (kInside / pairs), e = threadIdx.x % (kInside / pairs), r = e / per, c = e % per * each;
+  const int b = p * 2 * s;
+  float acc[each] = {};
+#pragma unroll 4
+  for (int k = 0; k < s; ++k) {
+    const float f = a[b + s + r][b + k];
+#pragma unroll
+    for (int j = 0; j < each; ++j) acc[j] = fmaf(f, t[b + k][b + c + j], acc[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < each; ++j) x[p * 16 + r][c + j] = acc[j];
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < each; ++j) acc[j] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < s; ++k) {
+    const float f = t[b + s + r][b + s + k];
+#pragma unroll
+    for (int j = 0; j < each; ++j) acc[j] = fmaf(f, x[p * 16 + k][c + j], acc[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < each; ++j) t[b + s + r][b + c + j] = -acc[j];
+  __syncthreads();
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant__ DeltaArgs a) {
+  extern __shared__ __align__(1024) uint8_t gdn_smem[];
+  InsideSmem<DK, DV>& sm = *reinterpret_cast<InsideSmem<DK, DV>*>(gdn_smem);
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0), lane = tid % 32, h = blockIdx.y, rep = a.H / a.G, g = h / rep;
+  if (!ascending(a) || (smem_u32(gdn_smem) & 1023u) != 0) return;   // (the next launch reports it)
+  int i = 0;
+  for (int hi = a.nseq - 1; i < hi;) {         // the last sequence whose chunks start at or before this one
+    const int mid = (i + hi + 1) / 2;
+    if ((long long)(a.cu[mid] / kC) + mid <= blockIdx.x) i = mid;
+    else hi = mid - 1;
+  }
+  const int s0 = a.cu[i], len = a.cu[i + 1] - s0;
+  const long long c0 = ((long long)blockIdx.x - (s0 / kC + i)) * kC;
+  if (c0 >= len) return;
+  const int t0 = s0 + (int)c0, n = min(kC, len - (int)c0);
+  const Layout lay(a.H, a.G, DK, DV);
+  uint8_t* chunk = static_cast<uint8_t*>(a.ws) + blockIdx.x * lay.chunk;
+  uint8_t *mine = chunk + (size_t)h * lay.head, *shared = chunk + (size_t)a.H * lay.head + (size_t)g * lay.group;
+
+  if (warp == 0) tmem_alloc(&sm.tmem, kInsideCols);
+  if (tid == 32) {
+    mbar_init(&sm.bar, 1);
+    fence_mbar_init();
+    sm.bad = kC;
+  }
+  __syncthreads();
+  // Tiles, zeros behind the last token and in place of what is not finite.
+  for (int e = tid; e < kC * (DK / 8); e += kInside) {
+    const int r = e / (DK / 8), x = e % (DK / 8) * 8;
+    uint4 q = make_uint4(0, 0, 0, 0), k = q;
+    if (r < n) {
+      const size_t from = ((size_t)(t0 + r) * a.G + g) * DK + x;
+      q = *reinterpret_cast<const uint4*>((const bf16*)a.q + from);
+      k = *reinterpret_cast<const uint4*>((const bf16*)a.k + from);
+      if (not_finite(q) || not_finite(k)) {
+        atomicMin(&sm.bad, r);
+        q = k = make_uint4(0, 0, 0, 0);
+      }
+    }
+    *reinterpret_cast<uint4*>(sm.qk + sw128(2 * kC, r, x)) = q;
+    *reinterpret_cast<uint4*>(sm.qk + sw128(2 * kC, kC + r, x)) = k;
+    if (h % rep == 0) {
+      *reinterpret_cast<uint4*>(shared + sw128(kC, r, x)) = q;
+      *reinterpret_cast<uint4*>(shared + kC * DK * 2 + sw128(kC, r, x)) = k;
+    }
+  }
+  for (int e = tid; e < kC * (DV / 8); e += kInside) {
+    const int r = e / (DV / 8), x = e % (DV / 8) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < n) {
+      v = *reinterpret_cast<const uint4*>((const bf16*)a.v + ((size_t)(t0 + r) * a.H + h) * DV + x);
+      if (not_finite(v)) {
+        atomicMin(&sm.bad, r);
+        v = make_uint4(0, 0, 0, 0);
+      }
+    }
+    *reinterpret_cast<uint4*>(sm.v + sw128(kC, r, x)) = v;
+  }
+  if (tid < n) {
+    const size_t at = (size_t)(t0 + tid) * a.H + h;
+    const float gate = a.g[at], beta = a.beta[at];
+    if (!(fabsf(beta) < INFINITY) || !(gate < INFINITY)) atomicMin(&sm.bad, tid);
+    sm.hi[tid] = fmaxf(gate, kLeast);
+    sm.beta[tid] = beta;
+  }
+  fence_async_smem();
+  before_sync();
+  __syncthreads();
+  after_sync();
+  const uint32_t tb = __shfl_sync(kFull, sm.tmem, 0), quarter = tb + ((uint32_t)(32 * warp) << 16);
+  const bool leader = warp == 0 && elected();
+  const uint32_t qk = smem_u32(sm.qk);
+  if (leader) {                                // rows 0-63 Q K^T, 64-127 K K^T
+#pragma unroll
+    for (int k = 0; k < DK / 16; ++k) {
+      const uint32_t at = qk + (k >> 2) * 2 * kAtom + (k & 3) * 32;
+      mma(tb + kColD, sdesc(at, 16, 1024), sdesc(at + kAtom, 16, 1024), idesc_bf16(128, kC, false, false), k > 0);
+    }
+    commit(&sm.bar);
+  }
+  const int used = min(n, sm.bad);             // tokens from a bad one on count as none: beta 0, gate 1
+  if (warp == 3) {                             // sums of gates: two tokens a lane
+    const auto gate = [&](int t) { return t < used ? sm.hi[t] : 0.f; };
+    const df g0 = {gate(2 * lane), 0.f}, g1 = {gate(2 * lane + 1), 0.f};
+    df sum = df_add(g0, g1);
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+      const df o = {__shfl_up_sync(kFull, sum.hi, off), __shfl_up_sync(kFull, sum.lo, off)};
+      if (lane >= off) sum = df_add(o, sum);
+    }
+    df before = {__shfl_up_sync(kFull, sum.hi, 1), __shfl_up_sync(kFull, sum.lo, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const df first = df_add(before, g0), all = {__shfl_sync(kFull, sum.hi, 31), __shfl_sync(kFull, sum.lo, 31)};
+    __syncwarp();
+    Factors& f = *reinterpret_cast<Factors*>(mine + lay.f);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int t = 2 * lane + x;
+      const df s = x == 0 ? first : sum;
+      sm.hi[t] = s.hi;
+      sm.lo[t] = s.lo;
+      if (t >= used) sm.beta[t] = 0.f;
+      f.since[t] = sm.since[t] = expf(s.hi + s.lo);
+      f.left[t] = expf(df_diff(all, s));
+    }
+    if (lane == 0) {
+      f.whole = expf(all.hi + all.lo);
+      f.bad = sm.bad;
+    }
+  }
+  __syncthreads();
+  bool ok = mbar_wait(&sm.bar, 0, a.status);
+  __syncwarp();
+  after_sync();
+  {
+    const int r = tid % kC;
+    const df mine_g = {sm.hi[r], sm.lo[r]};
+#pragma unroll 1
+    for (int x = 0; x < kC; x += 32) {
+      float v[32];
+      tmem_values(quarter + kColD + x, v);
+      if (tid < kC) {                          // M
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = x + j <= r ? v[j] * expf(df_diff(mine_g, {sm.hi[x + j], sm.lo[x + j]})) : 0.f;
+        uint32_t t[2][16];
+        terms_of<2>(v, t);
+        row_to(mine + lay.m, kC, r, x, t[0]);
+        row_to(mine + lay.m + kAtom, kC, r, x, t[1]);
+      } else {                                 // A, in the lower triangle
+        const float beta = sm.beta[r];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          sm.a[r][x + j] = x + j < r ? beta * (v[j] * expf(df_diff(mine_g, {sm.hi[x + j], sm.lo[x + j]}))) : 0.f;
+      }
+    }
+    before_sync();
+  }
+  __syncthreads();
+  // T: blocks of 16 on the diagonal by forward substitution, a column each thread, then pairs of blocks joined.
+  for (int e = tid; e < kC * kC; e += kInside) sm.t[e / kC][e % kC] = 0.f;
+  __syncthreads();
+  if (tid < kC) {
+    const int b = tid / 16 * 16, c = tid % 16;
+    float x[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float acc = 0.f;
+#pragma unroll
+      for (int l = 0; l < r; ++l) acc = fmaf(sm.a[b + r][b + l], x[l], acc);
+      x[r] = r < c ? 0.f : r == c ? 1.f : -acc;
+      sm.t[b + r][b + c] = x[r];
+    }
+  }
+  __syncthreads();
+  join_blocks<16, 2>(sm.a, sm.t, sm.x);
+  join_blocks<32, 1>(sm.a, sm.t, sm.x);
+  {                                            // rows 0-63 T', 64-127 T' diag(e^G), three terms
+    const int r = tid % kC;
+#pragma unroll 1
+    for (int x = 0; x < kC; x += 32) {
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float f = sm.t[r][x + j] * sm.beta[x + j];
+        v[j] = x + j <= r ? (tid < kC ? f : f * sm.since[x + j]) : 0.f;
+      }
+      uint32_t t[3][16];
+      terms_of<3>(v, t);
+      uint32_t both_terms[32];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        both_terms[j] = t[0][j];
+        both_terms[16 + j] = t[1][j];
+      }
+      // columns: 32 of the half x, hi and mid; then lo
+      tmem_st32(quarter + kColT + x, both_terms);
+      uint32_t low[32] = {};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) low[j] = t[2][j];
+      tmem_st32(quarter + kColT + 64 + x, low);
+    }
+    tmem_wait_st();
+    before_sync();
+  }
+  __syncthreads();
+  after_sync();
+  // U0 = T' V from rows 0-63, W = (T' diag(e^G)) K from rows 64-127
+  const auto product = [&](uint32_t tile, uint32_t lbo, uint32_t N) {
+    uint32_t more = 0;
+#pragma unroll
+    for (int k = 0; k < kC / 16; ++k)
+#pragma unroll
+      for (int term = 0; term < 3; ++term, more = 1)
+        mma_ts(tb + kColD, tb + kColT + k / 2 * 32 + (term < 2 ? 16 * term : 64) + k % 2 * 8, sdesc(tile + k * 2048, lbo, 1024),
+               idesc_bf16(128, N, false, true), more);
+    commit(&sm.bar);
+  };
+  if (ok && leader) product(smem_u32(sm.v), kAtom, DV);
+  ok = ok && mbar_wait(&sm.bar, 1, a.status);
+  __syncwarp();
+  after_sync();
+  if (tid < kC) {
+    float* u = reinterpret_cast<float*>(mine + lay.u) + tid * DV;
+#pragma unroll 1
+    for (int x = 0; x < DV; x += 32) {
+      float v[32];
+      tmem_values(quarter + kColD + x, v);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(u + x + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    }
+  }
+  before_sync();
+  __syncthreads();
+  after_sync();
+  if (ok && leader) product(qk + kAtom, 2 * kAtom, DK);
+  ok = ok && mbar_wait(&sm.bar, 0, a.status);
+  __syncwarp();
+  after_sync();
+  if (tid >= kC) {
+    const int r = tid - kC;
+#pragma unroll 1
+    for (int x = 0; x < DK; x += 32) {
+      float v[32];
+      tmem_values(quarter + kColD + x, v);
+      uint32_t t[2][16];
+      terms_of<2>(v, t);
+      row_to(mine + lay.w, kC, r, x, t[0]);
+      row_to(mine + lay.w + kC * DK * 2, kC, r, x, t[1]);
+    }
+  }
+  if (!ok && tid == 0) {                       // a wait gave up: no MMA may be left in flight
+    const uint64_t start = globaltimer();
+    while (globaltimer() - start < 2000000) {}
+  }
+  before_sync();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tb, kInsideCols);
+}
+
+// ---- through the state ----------------------------------------------------------------------------------------------
+// Warps 0-7 own the state S^T, thread by thread one k (lane quarter warp % 4) and 32 of the 64 rows (warp / 4); those of quarters
+// 2 and 3 make U, those of 0 and 1 the outputs.  Warp 8 loads, warp 9 issues.
+constexpr int kOwners = 256, kLoadThread = 256, kThrough = 320;
+constexpr uint32_t kCol1 = 0, kCol2 = 64, kColO = 128, kCol3 = 192, kThroughCols = 256;
+
+struct Hdr {
+  uint64_t full[2], empty[2], s_ready, u_ready, u_written, s_done, o_done, o_free;
+  uint32_t tmem;
+  int dead;                                  // a wait gave up: no further wait waits, no copy or MMA is issued
+};
+
+// Shared memory: two stages, S^T as two terms [dk x 64], U and the decayed U as two terms each [64 x 64].
+// A stage: for each 64 columns Q's and W hi's atoms, one A operand of 128 rows; W lo's, as rows 64-127 of one whose other rows are
+// whatever lies before; M hi and lo, rows 0-63 of two whose others are what lies behind; K; the factors.
+template <int DK>
+struct Stage {
+  static constexpr uint32_t atoms = DK / 64, wlo = 2 * atoms * kAtom, m = wlo + atoms * kAtom, k = m + 2 * kAtom,
+                            f = k + atoms * kAtom, size = f + sizeof(Factors);
+  static constexpr uint32_t bytes = size;      // all of it arrives by copies
+  static constexpr uint32_t s = 2 * size, u = s + 2 * DK * 128, hdr = u + 4 * kAtom, smem = hdr + sizeof(Hdr);
+  static_assert(smem <= 227 * 1024 && size % 1024 == 0, "one CTA's shared memory; whole swizzle groups");
+};
+
+__device__ __forceinline__ bool wait(Hdr& hd, uint64_t* bar, uint32_t parity, int32_t* status) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  while (!mbar_try(bar, parity & 1u)) {
+    const uint64_t now = globaltimer();
+    if (*(volatile int*)&hd.dead != 0) return false;
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      if (status != nullptr) atomicCAS(status, 0, ERS_ETIMEOUT);
+      *(volatile int*)&hd.dead = 1;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool dead(const Hdr& hd) { return *(const volatile int*)&hd.dead != 0; }
+
+template <int DK>
+__global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_constant__ DeltaArgs a) {
+  using St = Stage<DK>;
+  extern __shared__ __align__(1024) uint8_t gdn_smem[];
+  Hdr& hd = *reinterpret_cast<Hdr*>(gdn_smem + St::hdr);
+  const int parts = a.dv / kPart, part = blockIdx.x % parts, unit = blockIdx.x / parts, i = unit / a.H, h = unit % a.H;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0), lane = tid % 32;
+  if (!ascending(a) || (smem_u32(gdn_smem) & 1023u) != 0) {
+    if (tid == 0) report(a.status, (smem_u32(gdn_smem) & 1023u) != 0 ? ERS_ECUDA : ERS_EINVAL);
+    return;
+  }
+  DeltaSeq seq;
+  if (!delta_seq(a, i, h, &seq)) return;
+  const int chunks = (seq.len + kC - 1) / kC, d0 = part * kPart;
+  const Layout lay(a.H, a.G, DK, a.dv);
+  const uint8_t* first = static_cast<const uint8_t*>(a.ws) + (seq.t0 / kC + i) * lay.chunk;
+  const uint8_t *mine = first + (size_t)h * lay.head, *shared = first + (size_t)a.H * lay.head + (size_t)(h / (a.H / a.G)) * lay.group;
+
+  if (warp == 9) tmem_alloc(&hd.tmem, kThroughCols);
+  if (tid == kLoadThread) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&hd.full[b], 1);
+      mbar_init(&hd.empty[b], 1 + kOwners);
+    }
+    mbar_init(&hd.s_ready, kOwners);
+    mbar_init(&hd.u_ready, 1);
+    mbar_init(&hd.u_written, kOwners / 2);
+    mbar_init(&hd.s_done, 1);
+    mbar_init(&hd.o_done, 1);
+    mbar_init(&hd.o_free, kOwners / 2);
+    fence_mbar_init();
+    hd.dead = 0;
+  }
+  before_sync();
+  __syncthreads();
+  after_sync();
+  const uint32_t tb = __shfl_sync(kFull, hd.tmem, 0);
+
+  if (warp == 8) {
+    // ---- loads -----------------------------------------------------------------------------------------------
+    if (lane == 0) {
+      for (int c = 0; c < chunks; ++c) {
+        const int b = c & 1;
+        if (c >= 2) wait(hd, &hd.empty[b], (c >> 1) - 1, a.status);
+        if (dead(hd)) break;
+        uint8_t* to = gdn_smem + b * St::size;
+        const uint8_t *w = mine + c * lay.chunk, *qk = shared + c * lay.chunk;
+        uint64_t* bar = &hd.full[b];
+        mbar_arrive_expect_tx(bar, St::bytes);
+        for (uint32_t x = 0; x < St::atoms; ++x) {
+          bulk_g2s(to + 2 * x * kAtom, qk + x * kAtom, kAtom, bar);
+          bulk_g2s(to + (2 * x + 1) * kAtom, w + x * kAtom, kAtom, bar);
+        }
+        bulk_g2s(to + St::wlo, w + St::atoms * kAtom, St::atoms * kAtom, bar);
+        bulk_g2s(to + St::m, w + lay.m, 2 * kAtom, bar);
+        bulk_g2s(to + St::k, qk + St::atoms * kAtom, St::atoms * kAtom, bar);
+        bulk_g2s(to + St::f, w + lay.f, sizeof(Factors), bar);
+      }
+    }
+  } else if (warp == 9) {
+    // ---- products --------------------------------------------------------------------------------------------
+    constexpr uint32_t id1 = idesc_bf16(128, kPart, false, true), id3 = idesc_bf16(128, kPart, true, true);
+    const bool leader = elected();
+    const uint32_t st = smem_u32(gdn_smem + St::s), ut = smem_u32(gdn_smem + St::u);
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t base = smem_u32(gdn_smem + (c & 1) * St::size);
+      if (!wait(hd, &hd.full[c & 1], c >> 1, a.status) || !wait(hd, &hd.s_ready, c, a.status)) break;
+      after_sync();
+      if (leader) {
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int k = 0; k < DK / 16; ++k)    // rows 0-63 Q S^T, 64-127 W S^T
+            mma(tb + kCol1, sdesc(base + (k >> 2) * 2 * kAtom + (k & 3) * 32, 16, 1024),
+                sdesc(st + term * DK * 128 + k * 2048, DK * 128, 1024), id1, term > 0 || k > 0);
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k)      // rows 64-127
+          mma(tb + kCol2, sdesc(base + St::wlo - kAtom + (k >> 2) * kAtom + (k & 3) * 32, 16, 1024),
+              sdesc(st + k * 2048, DK * 128, 1024), id1, k > 0);
+        commit(&hd.u_ready);
+      }
+      if (!wait(hd, &hd.u_written, c, a.status)) break;
+      after_sync();
+      if (leader) {
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int k = 0; k < kC / 16; ++k)    // K^T U'
+            mma(tb + kCol3, sdesc(base + St::k + k * 2048, kAtom, 1024), sdesc(ut + (2 + term) * kAtom + k * 2048, kAtom, 1024), id3,
+                term > 0 || k > 0);
+        commit(&hd.s_done);
+      }
+      if (c > 0 && !wait(hd, &hd.o_free, c - 1, a.status)) break;
+      after_sync();
+      if (leader) {
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int k = 0; k < kC / 16; ++k)    // M U: hi hi, hi lo, lo hi
+            mma(tb + kColO, sdesc(base + St::m + (x == 2 ? kAtom : 0) + k * 32, 16, 1024),
+                sdesc(ut + (x == 1 ? kAtom : 0) + k * 2048, kAtom, 1024), id1, x > 0 || k > 0);
+        commit(&hd.o_done);
+        commit(&hd.empty[c & 1]);
+      }
+    }
+  } else {
+    // ---- the state, U and the outputs ------------------------------------------------------------------------
+    const int r = tid % 128, x0 = tid / 128 * 32, row = r % kC;   // k of the state; token of U or the outputs
+    const bool makes_u = r >= kC, holds = r < DK;
+    const uint32_t quarter = tb + ((uint32_t)(r & ~31) << 16);
+    float s[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j] = holds && seq.in != nullptr ? seq.in[(size_t)(d0 + x0 + j) * DK + r] : 0.f;
+    bool poisoned = false;
+    float qs[32], since = 0.f;                 // the last chunk's Q S^T and its rows' factors
+    int bad = kC;
+    bool spoiled = false;
+    const auto outputs = [&](int c) {          // of chunk c
+      wait(hd, &hd.o_done, c, a.status);
+      __syncwarp();
+      after_sync();
+      float o[32];
+      tmem_values(quarter + kColO + x0, o);
+      before_sync();
+      mbar_arrive(&hd.o_free);
+      if (row >= seq.len - c * kC || dead(hd)) return;
+      bf16* to = (bf16*)a.o + ((size_t)(seq.t0 + c * kC + row) * a.H + h) * a.dv + d0 + x0;
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        w[j] = spoiled ? 0x7fff7fffu : pack_bf16x2(a.scale * fmaf(since, qs[2 * j], o[2 * j]), a.scale * fmaf(since, qs[2 * j + 1], o[2 * j + 1]));
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) *reinterpret_cast<uint4*>(to + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+    };
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      // the state as an operand
+      if (holds) {
+        uint32_t t[2][16];
+        terms_of<2>(s, t);
+        row_to(gdn_smem + St::s, DK, r, x0, t[0]);
+        row_to(gdn_smem + St::s + DK * 128, DK, r, x0, t[1]);
+      }
+      fence_async_smem();
+      before_sync();
+      mbar_arrive(&hd.s_ready);
+      if (!makes_u && c > 0) outputs(c - 1);
+      float u[32];
+      if (makes_u) {                           // on its way while the product is
+        const float* u0 = reinterpret_cast<const float*>(mine + c * lay.chunk + lay.u) + row * a.dv + d0 + x0;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(u0 + j);
+          u[j] = v.x;
+          u[j + 1] = v.y;
+          u[j + 2] = v.z;
+          u[j + 3] = v.w;
+        }
+      }
+      wait(hd, &hd.full[c & 1], c >> 1, a.status);
+      const Factors& f = *reinterpret_cast<const Factors*>(gdn_smem + (c & 1) * St::size + St::f);
+      const float whole = f.whole, left = f.left[row];
+      since = f.since[row];
+      bad = f.bad;
+      mbar_arrive(&hd.empty[c & 1]);
+      spoiled = poisoned || row >= bad;
+      poisoned = poisoned || bad < kC;
+      wait(hd, &hd.u_ready, c, a.status);
+      __syncwarp();
+      after_sync();
+      if (makes_u) {
+        float v[32];
+        tmem_values(quarter + kCol1 + x0, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) u[j] -= v[j];
+        tmem_values(quarter + kCol2 + x0, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) u[j] -= v[j];
+        if (c > 0) wait(hd, &hd.o_done, c - 1, a.status);   // U's tiles have been read
+        uint32_t t[2][16];
+        terms_of<2>(u, t);
+        row_to(gdn_smem + St::u, kC, row, x0, t[0]);
+        row_to(gdn_smem + St::u + kAtom, kC, row, x0, t[1]);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) u[j] *= left;
+        terms_of<2>(u, t);
+        row_to(gdn_smem + St::u + 2 * kAtom, kC, row, x0, t[0]);
+        row_to(gdn_smem + St::u + 3 * kAtom, kC, row, x0, t[1]);
+        fence_async_smem();
+        before_sync();
+        mbar_arrive(&hd.u_written);
+      } else {
+        tmem_values(quarter + kCol1 + x0, qs);
+        before_sync();
+      }
+      wait(hd, &hd.s_done, c, a.status);
+      __syncwarp();
+      after_sync();
+      float v[32];
+      tmem_values(quarter + kCol3 + x0, v);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s[j] = fmaf(whole, s[j], v[j]);
+      before_sync();
+    }
+    if (chunks > 0 && !makes_u) outputs(chunks - 1);
+    if (holds && !dead(hd)) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) seq.out[(size_t)(d0 + x0 + j) * DK + r] = poisoned ? __int_as_float(0x7fffffff) : s[j];
+    }
+  }
+  __syncwarp();
+  if (tid == kLoadThread && dead(hd)) {        // no copy or MMA may be left in flight: 2 ms are a thousand times what one takes
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000) {}
+  }
+  before_sync();
+  __syncthreads();
+  if (warp == 9) tmem_dealloc(tb, kThroughCols);
+}
+
+// ---- host side ---------------------------------------------------------------------------------------------------------
+template <typename F>
+cudaError_t allow(F kernel, int smem, bool (&done)[64], std::mutex& mu) {   // its shared memory, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
+template <int DK, int DV>
+cudaError_t launch(const DeltaArgs& a, cudaStream_t s) {
+  static std::mutex mu;
+  static bool inside[64] = {}, through[64] = {};
+  cudaError_t e = allow(k_gdn_inside<DK, DV>, sizeof(InsideSmem<DK, DV>), inside, mu);
+  if (e == cudaSuccess) e = allow(k_gdn_through<DK>, Stage<DK>::smem, through, mu);
+  if (e != cudaSuccess) return e;
+  k_gdn_inside<DK, DV><<<dim3((unsigned)chunk_numbers(a.ntokens, a.nseq), a.H), kInside, sizeof(InsideSmem<DK, DV>), s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  k_gdn_through<DK><<<(unsigned)((long long)a.nseq * a.H * (DV / kPart)), kThrough, Stage<DK>::smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t gdn_tc_workspace(const DeltaArgs& a) {
+  return align256(Layout(a.H, a.G, a.dk, a.dv).chunk * chunk_numbers(a.ntokens, a.nseq));
+}
+
+cudaError_t gdn_tc(const DeltaArgs& a, cudaStream_t s) {
+  if (a.dk == 64) return a.dv == 64 ? launch<64, 64>(a, s) : launch<64, 128>(a, s);
+  return a.dv == 64 ? launch<128, 64>(a, s) : launch<128, 128>(a, s);
+}
+
+}  // namespace ers

@@ -258,7 +258,9 @@ struct DeltaArgs {
 };
 cudaError_t gdn_fwd(const DeltaArgs& a, cudaStream_t s);      // prompts
 cudaError_t gdn_decode(const DeltaArgs& a, cudaStream_t s);   // one token per sequence
-size_t gdn_fwd_workspace(const DeltaArgs& a);                 // (by io, H, dk, dv, nseq, ntokens, max_len)
+size_t gdn_fwd_workspace(const DeltaArgs& a);                 // (by io, H, G, dk, dv, nseq, ntokens, max_len)
+cudaError_t gdn_tc(const DeltaArgs& a, cudaStream_t s);       // chunks on the tensor cores (bf16), ers_gdn_tc.cu
+size_t gdn_tc_workspace(const DeltaArgs& a);
 
 // attention over a paged cache of keys and values, ers_attn.cu
 struct AttnArgs {
