@@ -13,6 +13,7 @@
 // two (16 bits and more: each is off by at most 2^-17, in the mean 2^-18.7; a third term of all of them would double the products of the
 // serial loop).  The state itself is fp32 in registers, one rounded multiply-add a chunk.
 #include <mutex>
+#include <type_traits>
 
 #include "ers_common.cuh"
 #include "ers_internal.h"
@@ -99,47 +100,75 @@ __device__ __forceinline__ void tmem_values(uint32_t at, float (&v)[32]) {
   for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
 }
 
+// the sums of 32 columns and those 64 further on
+__device__ __forceinline__ void tmem_sums(uint32_t at, float (&v)[32]) {
+  uint32_t r[32], q[32];
+  tmem_ld32_begin(at, r);
+  tmem_ld32_begin(at + 64, q);
+  arrived(r);
+  arrived(q);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) + __uint_as_float(q[j]);
+}
+
 // ---- inside the chunks ------------------------------------------------------------------------------------------
-// Two CTAs per SM: one's exponentials and substitutions under the other's products.
-constexpr int kInside = 128, kLd = kC + 1;
+// Two CTAs per SM: one's exponentials and substitutions under the other's products.  A thread owns a lane of tensor memory (a
+// row: of Q K^T and T' V below 64, of K K^T and W from there) and the columns x0 .. + 31 of every 64.
+constexpr int kInside = 256, kLd = kC + 4;
 constexpr uint32_t kColD = 0, kColT = 128, kInsideCols = 256;
 
 template <int DK, int DV>
 struct InsideSmem {
   alignas(1024) uint8_t qk[2 * kC * DK * 2];   // rows 0-63 Q, 64-127 K
   alignas(1024) uint8_t v[kC * DV * 2];
-  float a[kC][kLd], t[kC][kLd], x[32][33];
-  float hi[kC], lo[kC], beta[kC], since[kC];
+  alignas(16) float a[kC][kLd];
+  alignas(16) float t[kC][kLd];
+  alignas(16) float x[32][36];
+  alignas(16) float2 sum[kC];                  // of gates up to a token, as two floats, times log2 e
+  alignas(16) float beta[kC];
+  alignas(16) float since[kC];
+  float gate[kC];
   uint64_t bar;
   uint32_t tmem;
   int bad;
 };
 
-// T's block at (r0, c0), s x s, below two diagonal blocks that are done: -T22 (A21 T11).  n products side by side, the next
-// pair of blocks 2 s further on; thread by thread `each` neighbouring columns of a row.
+__device__ __forceinline__ float exp2_of(float x) {   // 2 units in the last place; 0 below 2^-126
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// T's blocks below pairs of diagonal blocks that are done, s x s each: -T22 (A21 T11).  A thread takes neighbouring columns of a row.
 template <int s, int pairs>
-__device__ __forceinline__ void join_blocks(float (&a)[kC][kLd], float (&t)[kC][kLd], float (&x)[32][33]) {
-  constexpr int each = pairs * s * s / kInside, per = s / each;   // threads of a row
+__device__ __forceinline__ void join_blocks(float (&a)[kC][kLd], float (&t)[kC][kLd], float (&x)[32][36]) {
+  constexpr int each = pairs * s * s / kInside, per = s / each;   // columns of a thread, threads of a row
+  static_assert(each == 2 || each == 4, "vectors");
+  using Vec = typename std::conditional<each == 2, float2, float4>::type;
   const int p = threadIdx.x / (kInside / pairs), e = threadIdx.x % (kInside / pairs), r = e / per, c = e % per * each;
   const int b = p * 2 * s;
-  float acc[each] = {};
-#pragma unroll 4
-  for (int k = 0; k < s; ++k) {
-    const float f = a[b + s + r][b + k];
+  const auto multiply = [&](const float* left, const float* right, int ld, float (&acc)[each]) {
 #pragma unroll
-    for (int j = 0; j < each; ++j) acc[j] = fmaf(f, t[b + k][b + c + j], acc[j]);
-  }
+    for (int j = 0; j < each; ++j) acc[j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < s; k += 4) {
+      const float4 f4 = *reinterpret_cast<const float4*>(left + k);
+      const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const Vec v = *reinterpret_cast<const Vec*>(right + (k + y) * ld);
+        const float* w = reinterpret_cast<const float*>(&v);
+#pragma unroll
+        for (int j = 0; j < each; ++j) acc[j] = fmaf(f[y], w[j], acc[j]);
+      }
+    }
+  };
+  float acc[each];
+  multiply(&a[b + s + r][b], &t[b][b + c], kLd, acc);
 #pragma unroll
   for (int j = 0; j < each; ++j) x[p * 16 + r][c + j] = acc[j];
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < each; ++j) acc[j] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < s; ++k) {
-    const float f = t[b + s + r][b + s + k];
-#pragma unroll
-    for (int j = 0; j < each; ++j) acc[j] = fmaf(f, x[p * 16 + k][c + j], acc[j]);
-  }
+  multiply(&t[b + s + r][b + s], &x[p * 16][c], 36, acc);
 #pragma unroll
   for (int j = 0; j < each; ++j) t[b + s + r][b + c + j] = -acc[j];
   __syncthreads();
@@ -165,6 +194,29 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
   uint8_t* chunk = static_cast<uint8_t*>(a.ws) + blockIdx.x * lay.chunk;
   uint8_t *mine = chunk + (size_t)h * lay.head, *shared = chunk + (size_t)a.H * lay.head + (size_t)g * lay.group;
 
+  // Tiles, zeros behind the last token and in place of what is not finite; all of a thread's loads under way at once.
+  constexpr int kQ = kC * (DK / 8) / kInside, kV = kC * (DV / 8) / kInside;
+  uint4 q[kQ], k[kQ], v[kV];
+#pragma unroll
+  for (int y = 0; y < kQ; ++y) {
+    const int e = tid + y * kInside, r = e / (DK / 8), x = e % (DK / 8) * 8;
+    q[y] = k[y] = make_uint4(0, 0, 0, 0);
+    if (r < n) {
+      const size_t from = ((size_t)(t0 + r) * a.G + g) * DK + x;
+      q[y] = *reinterpret_cast<const uint4*>((const bf16*)a.q + from);
+      k[y] = *reinterpret_cast<const uint4*>((const bf16*)a.k + from);
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < kV; ++y) {
+    const int e = tid + y * kInside, r = e / (DV / 8), x = e % (DV / 8) * 8;
+    v[y] = r < n ? *reinterpret_cast<const uint4*>((const bf16*)a.v + ((size_t)(t0 + r) * a.H + h) * DV + x) : make_uint4(0, 0, 0, 0);
+  }
+  float gate = 0.f, beta = 0.f;
+  if (tid < n) {
+    gate = a.g[(size_t)(t0 + tid) * a.H + h];
+    beta = a.beta[(size_t)(t0 + tid) * a.H + h];
+  }
   if (warp == 0) tmem_alloc(&sm.tmem, kInsideCols);
   if (tid == 32) {
     mbar_init(&sm.bar, 1);
@@ -172,50 +224,39 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
     sm.bad = kC;
   }
   __syncthreads();
-  // Tiles, zeros behind the last token and in place of what is not finite.
-  for (int e = tid; e < kC * (DK / 8); e += kInside) {
-    const int r = e / (DK / 8), x = e % (DK / 8) * 8;
-    uint4 q = make_uint4(0, 0, 0, 0), k = q;
-    if (r < n) {
-      const size_t from = ((size_t)(t0 + r) * a.G + g) * DK + x;
-      q = *reinterpret_cast<const uint4*>((const bf16*)a.q + from);
-      k = *reinterpret_cast<const uint4*>((const bf16*)a.k + from);
-      if (not_finite(q) || not_finite(k)) {
-        atomicMin(&sm.bad, r);
-        q = k = make_uint4(0, 0, 0, 0);
-      }
+#pragma unroll
+  for (int y = 0; y < kQ; ++y) {
+    const int e = tid + y * kInside, r = e / (DK / 8), x = e % (DK / 8) * 8;
+    if (not_finite(q[y]) || not_finite(k[y])) {
+      atomicMin(&sm.bad, r);
+      q[y] = k[y] = make_uint4(0, 0, 0, 0);
     }
-    *reinterpret_cast<uint4*>(sm.qk + sw128(2 * kC, r, x)) = q;
-    *reinterpret_cast<uint4*>(sm.qk + sw128(2 * kC, kC + r, x)) = k;
+    *reinterpret_cast<uint4*>(sm.qk + sw128(2 * kC, r, x)) = q[y];
+    *reinterpret_cast<uint4*>(sm.qk + sw128(2 * kC, kC + r, x)) = k[y];
     if (h % rep == 0) {
-      *reinterpret_cast<uint4*>(shared + sw128(kC, r, x)) = q;
-      *reinterpret_cast<uint4*>(shared + kC * DK * 2 + sw128(kC, r, x)) = k;
+      *reinterpret_cast<uint4*>(shared + sw128(kC, r, x)) = q[y];
+      *reinterpret_cast<uint4*>(shared + kC * DK * 2 + sw128(kC, r, x)) = k[y];
     }
   }
-  for (int e = tid; e < kC * (DV / 8); e += kInside) {
-    const int r = e / (DV / 8), x = e % (DV / 8) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < n) {
-      v = *reinterpret_cast<const uint4*>((const bf16*)a.v + ((size_t)(t0 + r) * a.H + h) * DV + x);
-      if (not_finite(v)) {
-        atomicMin(&sm.bad, r);
-        v = make_uint4(0, 0, 0, 0);
-      }
+#pragma unroll
+  for (int y = 0; y < kV; ++y) {
+    const int e = tid + y * kInside, r = e / (DV / 8), x = e % (DV / 8) * 8;
+    if (not_finite(v[y])) {
+      atomicMin(&sm.bad, r);
+      v[y] = make_uint4(0, 0, 0, 0);
     }
-    *reinterpret_cast<uint4*>(sm.v + sw128(kC, r, x)) = v;
+    *reinterpret_cast<uint4*>(sm.v + sw128(kC, r, x)) = v[y];
   }
-  if (tid < n) {
-    const size_t at = (size_t)(t0 + tid) * a.H + h;
-    const float gate = a.g[at], beta = a.beta[at];
+  if (tid < kC) {
     if (!(fabsf(beta) < INFINITY) || !(gate < INFINITY)) atomicMin(&sm.bad, tid);
-    sm.hi[tid] = fmaxf(gate, kLeast);
+    sm.gate[tid] = fmaxf(gate, kLeast) * 1.44269504088896340736f;
     sm.beta[tid] = beta;
   }
   fence_async_smem();
   before_sync();
   __syncthreads();
   after_sync();
-  const uint32_t tb = __shfl_sync(kFull, sm.tmem, 0), quarter = tb + ((uint32_t)(32 * warp) << 16);
+  const uint32_t tb = __shfl_sync(kFull, sm.tmem, 0), quarter = tb + ((uint32_t)(tid & 96) << 16);
   const bool leader = warp == 0 && elected();
   const uint32_t qk = smem_u32(sm.qk);
   if (leader) {                                // rows 0-63 Q K^T, 64-127 K K^T
@@ -228,8 +269,8 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
   }
   const int used = min(n, sm.bad);             // tokens from a bad one on count as none: beta 0, gate 1
   if (warp == 3) {                             // sums of gates: two tokens a lane
-    const auto gate = [&](int t) { return t < used ? sm.hi[t] : 0.f; };
-    const df g0 = {gate(2 * lane), 0.f}, g1 = {gate(2 * lane + 1), 0.f};
+    const auto gate_of = [&](int t) { return t < used ? sm.gate[t] : 0.f; };
+    const df g0 = {gate_of(2 * lane), 0.f}, g1 = {gate_of(2 * lane + 1), 0.f};
     df sum = df_add(g0, g1);
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
@@ -239,54 +280,58 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
     df before = {__shfl_up_sync(kFull, sum.hi, 1), __shfl_up_sync(kFull, sum.lo, 1)};
     if (lane == 0) before = {0.f, 0.f};
     const df first = df_add(before, g0), all = {__shfl_sync(kFull, sum.hi, 31), __shfl_sync(kFull, sum.lo, 31)};
-    __syncwarp();
     Factors& f = *reinterpret_cast<Factors*>(mine + lay.f);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int t = 2 * lane + x;
       const df s = x == 0 ? first : sum;
-      sm.hi[t] = s.hi;
-      sm.lo[t] = s.lo;
+      sm.sum[t] = make_float2(s.hi, s.lo);
       if (t >= used) sm.beta[t] = 0.f;
-      f.since[t] = sm.since[t] = expf(s.hi + s.lo);
-      f.left[t] = expf(df_diff(all, s));
+      f.since[t] = sm.since[t] = exp2f(s.hi + s.lo);
+      f.left[t] = exp2f(df_diff(all, s));
     }
     if (lane == 0) {
-      f.whole = expf(all.hi + all.lo);
+      f.whole = exp2f(all.hi + all.lo);
       f.bad = sm.bad;
     }
   }
+  for (int e = tid; e < kC * kLd / 4; e += kInside) reinterpret_cast<float4*>(sm.t)[e] = make_float4(0, 0, 0, 0);
   __syncthreads();
   bool ok = mbar_wait(&sm.bar, 0, a.status);
   __syncwarp();
   after_sync();
+  const int r = tid % kC, x0 = tid / 128 * 32;
+  const bool upper = tid % 128 < kC;           // lanes 0-63
   {
-    const int r = tid % kC;
-    const df mine_g = {sm.hi[r], sm.lo[r]};
-#pragma unroll 1
-    for (int x = 0; x < kC; x += 32) {
-      float v[32];
-      tmem_values(quarter + kColD + x, v);
-      if (tid < kC) {                          // M
+    float v[32];
+    if (x0 <= (r | 31)) {                      // (a whole warp: beyond the diagonal all is zero)
+      tmem_values(quarter + kColD + x0, v);
+      const df own = {sm.sum[r].x, sm.sum[r].y};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = x + j <= r ? v[j] * expf(df_diff(mine_g, {sm.hi[x + j], sm.lo[x + j]})) : 0.f;
-        uint32_t t[2][16];
-        terms_of<2>(v, t);
-        row_to(mine + lay.m, kC, r, x, t[0]);
-        row_to(mine + lay.m + kAtom, kC, r, x, t[1]);
-      } else {                                 // A, in the lower triangle
-        const float beta = sm.beta[r];
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          sm.a[r][x + j] = x + j < r ? beta * (v[j] * expf(df_diff(mine_g, {sm.hi[x + j], sm.lo[x + j]}))) : 0.f;
+      for (int j = 0; j < 32; j += 2) {
+        const float4 o = *reinterpret_cast<const float4*>(&sm.sum[x0 + j]);
+        v[j] *= exp2_of(df_diff(own, {o.x, o.y}));
+        v[j + 1] *= exp2_of(df_diff(own, {o.z, o.w}));
       }
+    }
+    const int keep = upper ? r - x0 : r - x0 - 1;   // the last column that is kept: with or without the diagonal
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = j <= keep ? v[j] : 0.f;
+    if (upper) {                               // M
+      uint32_t t[2][16];
+      terms_of<2>(v, t);
+      row_to(mine + lay.m, kC, r, x0, t[0]);
+      row_to(mine + lay.m + kAtom, kC, r, x0, t[1]);
+    } else {                                   // A
+      const float beta = sm.beta[r];
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4*>(&sm.a[r][x0 + j]) = make_float4(beta * v[j], beta * v[j + 1], beta * v[j + 2], beta * v[j + 3]);
     }
     before_sync();
   }
   __syncthreads();
   // T: blocks of 16 on the diagonal by forward substitution, a column each thread, then pairs of blocks joined.
-  for (int e = tid; e < kC * kC; e += kInside) sm.t[e / kC][e % kC] = 0.f;
-  __syncthreads();
   if (tid < kC) {
     const int b = tid / 16 * 16, c = tid % 16;
     float x[16];
@@ -294,7 +339,13 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
     for (int r = 0; r < 16; ++r) {
       float acc = 0.f;
 #pragma unroll
-      for (int l = 0; l < r; ++l) acc = fmaf(sm.a[b + r][b + l], x[l], acc);
+      for (int l = 0; l < r; l += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&sm.a[b + r][b + l]);
+        acc = fmaf(f.x, x[l], acc);
+        if (l + 1 < r) acc = fmaf(f.y, x[l + 1], acc);
+        if (l + 2 < r) acc = fmaf(f.z, x[l + 2], acc);
+        if (l + 3 < r) acc = fmaf(f.w, x[l + 3], acc);
+      }
       x[r] = r < c ? 0.f : r == c ? 1.f : -acc;
       sm.t[b + r][b + c] = x[r];
     }
@@ -303,30 +354,31 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
   join_blocks<16, 2>(sm.a, sm.t, sm.x);
   join_blocks<32, 1>(sm.a, sm.t, sm.x);
   {                                            // rows 0-63 T', 64-127 T' diag(e^G), three terms
-    const int r = tid % kC;
-#pragma unroll 1
-    for (int x = 0; x < kC; x += 32) {
-      float v[32];
+    float v[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float f = sm.t[r][x + j] * sm.beta[x + j];
-        v[j] = x + j <= r ? (tid < kC ? f : f * sm.since[x + j]) : 0.f;
-      }
-      uint32_t t[3][16];
-      terms_of<3>(v, t);
-      uint32_t both_terms[32];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        both_terms[j] = t[0][j];
-        both_terms[16 + j] = t[1][j];
-      }
-      // columns: 32 of the half x, hi and mid; then lo
-      tmem_st32(quarter + kColT + x, both_terms);
-      uint32_t low[32] = {};
-#pragma unroll
-      for (int j = 0; j < 16; ++j) low[j] = t[2][j];
-      tmem_st32(quarter + kColT + 64 + x, low);
+    for (int j = 0; j < 32; j += 4) {
+      const float4 t = *reinterpret_cast<const float4*>(&sm.t[r][x0 + j]), b = *reinterpret_cast<const float4*>(&sm.beta[x0 + j]);
+      float4 f = *reinterpret_cast<const float4*>(&sm.since[x0 + j]);
+      if (upper) f = make_float4(1.f, 1.f, 1.f, 1.f);
+      v[j] = t.x * b.x * f.x;
+      v[j + 1] = t.y * b.y * f.y;
+      v[j + 2] = t.z * b.z * f.z;
+      v[j + 3] = t.w * b.w * f.w;
     }
+    uint32_t t[3][16], c[32];
+    terms_of<3>(v, t);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      c[j] = t[0][j];
+      c[16 + j] = t[1][j];
+    }
+    tmem_st32(quarter + kColT + x0, c);        // of 32 columns hi and mid; behind those of all, lo
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      c[j] = t[2][j];
+      c[16 + j] = 0;
+    }
+    tmem_st32(quarter + kColT + 64 + x0, c);
     tmem_wait_st();
     before_sync();
   }
@@ -347,10 +399,10 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
   ok = ok && mbar_wait(&sm.bar, 1, a.status);
   __syncwarp();
   after_sync();
-  if (tid < kC) {
-    float* u = reinterpret_cast<float*>(mine + lay.u) + tid * DV;
-#pragma unroll 1
-    for (int x = 0; x < DV; x += 32) {
+  if (upper) {
+    float* u = reinterpret_cast<float*>(mine + lay.u) + r * DV;
+#pragma unroll
+    for (int x = x0; x < DV; x += 64) {
       float v[32];
       tmem_values(quarter + kColD + x, v);
 #pragma unroll
@@ -364,10 +416,9 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
   ok = ok && mbar_wait(&sm.bar, 0, a.status);
   __syncwarp();
   after_sync();
-  if (tid >= kC) {
-    const int r = tid - kC;
-#pragma unroll 1
-    for (int x = 0; x < DK; x += 32) {
+  if (!upper) {
+#pragma unroll
+    for (int x = x0; x < DK; x += 64) {
       float v[32];
       tmem_values(quarter + kColD + x, v);
       uint32_t t[2][16];
@@ -389,10 +440,12 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
 // Warps 0-7 own the state S^T, thread by thread one k (lane quarter warp % 4) and 32 of the 64 rows (warp / 4); those of quarters
 // 2 and 3 make U, those of 0 and 1 the outputs.  Warp 8 loads, warp 9 issues.
 constexpr int kOwners = 256, kLoadThread = 256, kThrough = 320;
-constexpr uint32_t kCol1 = 0, kCol2 = 64, kColO = 128, kCol3 = 192, kThroughCols = 256;
+// Products with an operand of two terms take both as 128 columns: the other operand is read once, and the halves are added
+// up by those who read them.
+constexpr uint32_t kCol1 = 0, kCol2 = 128, kCol3 = 192, kColO = 320, kThroughCols = 512;
 
 struct Hdr {
-  uint64_t full[2], empty[2], s_ready, u_ready, u_written, s_done, o_done, o_free;
+  uint64_t full[2], empty[2], s_ready, u_ready, u_decayed, u_written, s_done, o_done, o_free;
   uint32_t tmem;
   int dead;                                  // a wait gave up: no further wait waits, no copy or MMA is issued
 };
@@ -451,6 +504,7 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
     }
     mbar_init(&hd.s_ready, kOwners);
     mbar_init(&hd.u_ready, 1);
+    mbar_init(&hd.u_decayed, kOwners / 2);
     mbar_init(&hd.u_written, kOwners / 2);
     mbar_init(&hd.s_done, 1);
     mbar_init(&hd.o_done, 1);
@@ -486,7 +540,8 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
     }
   } else if (warp == 9) {
     // ---- products --------------------------------------------------------------------------------------------
-    constexpr uint32_t id1 = idesc_bf16(128, kPart, false, true), id3 = idesc_bf16(128, kPart, true, true);
+    constexpr uint32_t id = idesc_bf16(128, kPart, false, true), id2 = idesc_bf16(128, 2 * kPart, false, true),
+                       id3 = idesc_bf16(128, 2 * kPart, true, true);
     const bool leader = elected();
     const uint32_t st = smem_u32(gdn_smem + St::s), ut = smem_u32(gdn_smem + St::u);
 #pragma unroll 1
@@ -496,37 +551,31 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       after_sync();
       if (leader) {
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
-#pragma unroll
-          for (int k = 0; k < DK / 16; ++k)    // rows 0-63 Q S^T, 64-127 W S^T
-            mma(tb + kCol1, sdesc(base + (k >> 2) * 2 * kAtom + (k & 3) * 32, 16, 1024),
-                sdesc(st + term * DK * 128 + k * 2048, DK * 128, 1024), id1, term > 0 || k > 0);
+        for (int k = 0; k < DK / 16; ++k)      // rows 0-63 Q S^T, 64-127 W S^T
+          mma(tb + kCol1, sdesc(base + (k >> 2) * 2 * kAtom + (k & 3) * 32, 16, 1024), sdesc(st + k * 2048, DK * 128, 1024), id2, k > 0);
 #pragma unroll
         for (int k = 0; k < DK / 16; ++k)      // rows 64-127
           mma(tb + kCol2, sdesc(base + St::wlo - kAtom + (k >> 2) * kAtom + (k & 3) * 32, 16, 1024),
-              sdesc(st + k * 2048, DK * 128, 1024), id1, k > 0);
+              sdesc(st + k * 2048, DK * 128, 1024), id, k > 0);
         commit(&hd.u_ready);
       }
-      if (!wait(hd, &hd.u_written, c, a.status)) break;
+      if (!wait(hd, &hd.u_decayed, c, a.status)) break;
       after_sync();
       if (leader) {
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
-#pragma unroll
-          for (int k = 0; k < kC / 16; ++k)    // K^T U'
-            mma(tb + kCol3, sdesc(base + St::k + k * 2048, kAtom, 1024), sdesc(ut + (2 + term) * kAtom + k * 2048, kAtom, 1024), id3,
-                term > 0 || k > 0);
+        for (int k = 0; k < kC / 16; ++k)      // K^T U'
+          mma(tb + kCol3, sdesc(base + St::k + k * 2048, kAtom, 1024), sdesc(ut + 2 * kAtom + k * 2048, kAtom, 1024), id3, k > 0);
         commit(&hd.s_done);
       }
-      if (c > 0 && !wait(hd, &hd.o_free, c - 1, a.status)) break;
+      if (!wait(hd, &hd.u_written, c, a.status) || (c > 0 && !wait(hd, &hd.o_free, c - 1, a.status))) break;
       after_sync();
       if (leader) {
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
+        for (int k = 0; k < kC / 16; ++k)      // M hi U
+          mma(tb + kColO, sdesc(base + St::m + k * 32, 16, 1024), sdesc(ut + k * 2048, kAtom, 1024), id2, k > 0);
 #pragma unroll
-          for (int k = 0; k < kC / 16; ++k)    // M U: hi hi, hi lo, lo hi
-            mma(tb + kColO, sdesc(base + St::m + (x == 2 ? kAtom : 0) + k * 32, 16, 1024),
-                sdesc(ut + (x == 1 ? kAtom : 0) + k * 2048, kAtom, 1024), id1, x > 0 || k > 0);
+        for (int k = 0; k < kC / 16; ++k)      // M lo U hi
+          mma(tb + kColO, sdesc(base + St::m + kAtom + k * 32, 16, 1024), sdesc(ut + k * 2048, kAtom, 1024), id, 1);
         commit(&hd.o_done);
         commit(&hd.empty[c & 1]);
       }
@@ -540,7 +589,7 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
 #pragma unroll
     for (int j = 0; j < 32; ++j) s[j] = holds && seq.in != nullptr ? seq.in[(size_t)(d0 + x0 + j) * DK + r] : 0.f;
     bool poisoned = false;
-    float qs[32], since = 0.f;                 // the last chunk's Q S^T and its rows' factors
+    float u[32], since = 0.f;                  // U, or the last chunk's Q S^T, and its rows' factors
     int bad = kC;
     bool spoiled = false;
     const auto outputs = [&](int c) {          // of chunk c
@@ -548,7 +597,7 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       __syncwarp();
       after_sync();
       float o[32];
-      tmem_values(quarter + kColO + x0, o);
+      tmem_sums(quarter + kColO + x0, o);
       before_sync();
       mbar_arrive(&hd.o_free);
       if (row >= seq.len - c * kC || dead(hd)) return;
@@ -556,7 +605,7 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       uint32_t w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        w[j] = spoiled ? 0x7fff7fffu : pack_bf16x2(a.scale * fmaf(since, qs[2 * j], o[2 * j]), a.scale * fmaf(since, qs[2 * j + 1], o[2 * j + 1]));
+        w[j] = spoiled ? 0x7fff7fffu : pack_bf16x2(a.scale * fmaf(since, u[2 * j], o[2 * j]), a.scale * fmaf(since, u[2 * j + 1], o[2 * j + 1]));
 #pragma unroll
       for (int j = 0; j < 16; j += 4) *reinterpret_cast<uint4*>(to + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
     };
@@ -573,7 +622,6 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       before_sync();
       mbar_arrive(&hd.s_ready);
       if (!makes_u && c > 0) outputs(c - 1);
-      float u[32];
       if (makes_u) {                           // on its way while the product is
         const float* u0 = reinterpret_cast<const float*>(mine + c * lay.chunk + lay.u) + row * a.dv + d0 + x0;
 #pragma unroll
@@ -598,34 +646,37 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       after_sync();
       if (makes_u) {
         float v[32];
-        tmem_values(quarter + kCol1 + x0, v);
+        tmem_sums(quarter + kCol1 + x0, v);
 #pragma unroll
         for (int j = 0; j < 32; ++j) u[j] -= v[j];
         tmem_values(quarter + kCol2 + x0, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) u[j] -= v[j];
-        if (c > 0) wait(hd, &hd.o_done, c - 1, a.status);   // U's tiles have been read
-        uint32_t t[2][16];
-        terms_of<2>(u, t);
-        row_to(gdn_smem + St::u, kC, row, x0, t[0]);
-        row_to(gdn_smem + St::u + kAtom, kC, row, x0, t[1]);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) u[j] *= left;
-        terms_of<2>(u, t);
+        for (int j = 0; j < 32; ++j) {
+          u[j] -= v[j];
+          v[j] = u[j] * left;
+        }
+        uint32_t t[2][16];                     // first what the state waits for
+        terms_of<2>(v, t);
         row_to(gdn_smem + St::u + 2 * kAtom, kC, row, x0, t[0]);
         row_to(gdn_smem + St::u + 3 * kAtom, kC, row, x0, t[1]);
         fence_async_smem();
         before_sync();
+        mbar_arrive(&hd.u_decayed);
+        if (c > 0) wait(hd, &hd.o_done, c - 1, a.status);   // U's tiles have been read
+        terms_of<2>(u, t);
+        row_to(gdn_smem + St::u, kC, row, x0, t[0]);
+        row_to(gdn_smem + St::u + kAtom, kC, row, x0, t[1]);
+        fence_async_smem();
         mbar_arrive(&hd.u_written);
       } else {
-        tmem_values(quarter + kCol1 + x0, qs);
+        tmem_sums(quarter + kCol1 + x0, u);
         before_sync();
       }
       wait(hd, &hd.s_done, c, a.status);
       __syncwarp();
       after_sync();
       float v[32];
-      tmem_values(quarter + kCol3 + x0, v);
+      tmem_sums(quarter + kCol3 + x0, v);
 #pragma unroll
       for (int j = 0; j < 32; ++j) s[j] = fmaf(whole, s[j], v[j]);
       before_sync();
