@@ -7,7 +7,7 @@
 // Differences of G are taken between sums held as two floats, so that no gate, however strong, costs the others bits; every
 // exponent is <= 0.  The first line depends on no other chunk: k_gdn_inside forms it for all chunks at once, a CTA for a chunk and
 // head, and leaves W, M (as two bf16 terms), U0 (fp32) and the factors in the workspace, with Q and K as padded operand tiles.
-// k_gdn_through walks a sequence's chunks, a CTA for 64 rows of a head's state.
+// k_gdn_through walks a sequence's chunks, a CTA for 64 or 32 rows of a head's state.
 //
 // Precision: q, k and v are exact operands.  T' is taken as three bf16 terms (24 bits); W, S, M, U and the decayed U as
 // two (16 bits and more: each is off by at most 2^-17, in the mean 2^-18.7; a third term of all of them would double the products of the
@@ -28,7 +28,6 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 64;                       // tokens of a chunk
-constexpr int kPart = 64;                    // state rows of a CTA
 constexpr uint32_t kAtom = kC * 128;         // 64 rows of 64 bf16 columns
 constexpr float kLeast = -200.f;             // a lower log-gate is e^-200 = 0 in fp32 as well
 
@@ -44,7 +43,7 @@ static_assert(sizeof(Factors) == 1024, "whole copies");
 
 // What k_gdn_inside leaves of a chunk: a block for each head, and Q and K for each group.
 struct Layout {
-  uint32_t w, m, f, u, head;                 // offsets of W (hi, lo), M (hi, lo), factors, U0 [64, dv]; bytes of a block
+  uint32_t w, m, f, u, head;                 // offsets of W (hi, lo), M (hi, lo), factors, U0 [dv / 4, 64, 4]; bytes of a block
   uint32_t group;                            // bytes of Q, then K
   size_t chunk;                              // bytes of a chunk's: heads, then groups
   __host__ __device__ Layout(int H, int G, int dk, int dv) {
@@ -76,20 +75,21 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
   return bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
 }
 
-// 32 fp32 values as N bf16 terms: word j of term n holds values 2 j and 2 j + 1.
-template <int N>
-__device__ __forceinline__ void terms_of(const float (&v)[32], uint32_t (&t)[N][16]) {
+// X fp32 values as N bf16 terms: word j of term n holds values 2 j and 2 j + 1.
+template <int N, int X>
+__device__ __forceinline__ void terms_of(const float (&v)[X], uint32_t (&t)[N][X / 2]) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < X / 2; ++j) {
     uint64_t p = pair(v[2 * j], v[2 * j + 1]);
 #pragma unroll
     for (int n = 0; n < N; ++n) t[n][j] = n == N - 1 ? round2(p) : take_term(p);
   }
 }
-// 32 columns of a row of an operand tile
-__device__ __forceinline__ void row_to(uint8_t* tile, uint32_t rows, uint32_t r, uint32_t x, const uint32_t (&t)[16]) {
+// columns x on of a row of an operand tile
+template <int W>
+__device__ __forceinline__ void row_to(uint8_t* tile, uint32_t rows, uint32_t r, uint32_t x, const uint32_t (&t)[W]) {
 #pragma unroll
-  for (int j = 0; j < 16; j += 4)
+  for (int j = 0; j < W; j += 4)
     *reinterpret_cast<uint4*>(tile + sw128(rows, r, x + 2 * j)) = make_uint4(t[j], t[j + 1], t[j + 2], t[j + 3]);
 }
 __device__ __forceinline__ void tmem_values(uint32_t at, float (&v)[32]) {
@@ -100,16 +100,12 @@ __device__ __forceinline__ void tmem_values(uint32_t at, float (&v)[32]) {
   for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
 }
 
-// the sums of 32 columns and those 64 further on
-__device__ __forceinline__ void tmem_sums(uint32_t at, float (&v)[32]) {
-  uint32_t r[32], q[32];
-  tmem_ld32_begin(at, r);
-  tmem_ld32_begin(at + 64, q);
-  arrived(r);
-  arrived(q);
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) + __uint_as_float(q[j]);
+__device__ __forceinline__ void tmem_values(uint32_t at, float (&v)[16]) { tmem_ld16(at, v); }
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // ---- inside the chunks ------------------------------------------------------------------------------------------
 // Two CTAs per SM: one's exponentials and substitutions under the other's products.  A thread owns a lane of tensor memory (a
@@ -121,6 +117,7 @@ template <int DK, int DV>
 struct InsideSmem {
   alignas(1024) uint8_t qk[2 * kC * DK * 2];   // rows 0-63 Q, 64-127 K
   alignas(1024) uint8_t v[kC * DV * 2];
+  alignas(1024) uint8_t m[2 * kAtom];          // M hi, lo on their way out (W goes by the place of Q and K)
   alignas(16) float a[kC][kLd];
   alignas(16) float t[kC][kLd];
   alignas(16) float x[32][36];
@@ -139,38 +136,44 @@ __device__ __forceinline__ float exp2_of(float x) {   // 2 units in the last pla
   return y;
 }
 
-// T's blocks below pairs of diagonal blocks that are done, s x s each: -T22 (A21 T11).  A thread takes neighbouring columns of a row.
-template <int s, int pairs>
+// T's blocks below pairs of diagonal blocks that are done, s x s each: -T22 (A21 T11), 2 x 4 outputs a thread.
+template <int s>
 __device__ __forceinline__ void join_blocks(float (&a)[kC][kLd], float (&t)[kC][kLd], float (&x)[32][36]) {
-  constexpr int each = pairs * s * s / kInside, per = s / each;   // columns of a thread, threads of a row
-  static_assert(each == 2 || each == 4, "vectors");
-  using Vec = typename std::conditional<each == 2, float2, float4>::type;
-  const int p = threadIdx.x / (kInside / pairs), e = threadIdx.x % (kInside / pairs), r = e / per, c = e % per * each;
-  const int b = p * 2 * s;
-  const auto multiply = [&](const float* left, const float* right, int ld, float (&acc)[each]) {
+  constexpr int pairs = kC / (2 * s), threads = s * s / 8;   // of a pair
+  const int p = threadIdx.x / threads, e = threadIdx.x % threads, r = e / (s / 4) * 2, c = e % (s / 4) * 4, b = p * 2 * s;
+  float acc[2][4];
+  const auto multiply = [&](const float* left, const float* right, int ld) {
 #pragma unroll
-    for (int j = 0; j < each; ++j) acc[j] = 0.f;
-#pragma unroll 4
+    for (int j = 0; j < 8; ++j) acc[j / 4][j % 4] = 0.f;
+#pragma unroll
     for (int k = 0; k < s; k += 4) {
-      const float4 f4 = *reinterpret_cast<const float4*>(left + k);
-      const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+      const float4 f = *reinterpret_cast<const float4*>(left + k), g = *reinterpret_cast<const float4*>(left + kLd + k);
+      const float l[2][4] = {{f.x, f.y, f.z, f.w}, {g.x, g.y, g.z, g.w}};
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const Vec v = *reinterpret_cast<const Vec*>(right + (k + y) * ld);
-        const float* w = reinterpret_cast<const float*>(&v);
+        const float4 v = *reinterpret_cast<const float4*>(right + (k + y) * ld);
 #pragma unroll
-        for (int j = 0; j < each; ++j) acc[j] = fmaf(f[y], w[j], acc[j]);
+        for (int j = 0; j < 2; ++j) {
+          acc[j][0] = fmaf(l[j][y], v.x, acc[j][0]);
+          acc[j][1] = fmaf(l[j][y], v.y, acc[j][1]);
+          acc[j][2] = fmaf(l[j][y], v.z, acc[j][2]);
+          acc[j][3] = fmaf(l[j][y], v.w, acc[j][3]);
+        }
       }
     }
   };
-  float acc[each];
-  multiply(&a[b + s + r][b], &t[b][b + c], kLd, acc);
+  if (p < pairs) {
+    multiply(&a[b + s + r][b], &t[b][b + c], kLd);
 #pragma unroll
-  for (int j = 0; j < each; ++j) x[p * 16 + r][c + j] = acc[j];
+    for (int j = 0; j < 2; ++j) *reinterpret_cast<float4*>(&x[p * s + r + j][c]) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+  }
   __syncthreads();
-  multiply(&t[b + s + r][b + s], &x[p * 16][c], 36, acc);
+  if (p < pairs) {
+    multiply(&t[b + s + r][b + s], &x[p * s][c], 36);
 #pragma unroll
-  for (int j = 0; j < each; ++j) t[b + s + r][b + c + j] = -acc[j];
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<float4*>(&t[b + s + r + j][b + c]) = make_float4(-acc[j][0], -acc[j][1], -acc[j][2], -acc[j][3]);
+  }
   __syncthreads();
 }
 
@@ -320,8 +323,9 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
     if (upper) {                               // M
       uint32_t t[2][16];
       terms_of<2>(v, t);
-      row_to(mine + lay.m, kC, r, x0, t[0]);
-      row_to(mine + lay.m + kAtom, kC, r, x0, t[1]);
+      row_to(sm.m, kC, r, x0, t[0]);
+      row_to(sm.m + kAtom, kC, r, x0, t[1]);
+      fence_async_smem();
     } else {                                   // A
       const float beta = sm.beta[r];
 #pragma unroll
@@ -331,28 +335,29 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
     before_sync();
   }
   __syncthreads();
-  // T: blocks of 16 on the diagonal by forward substitution, a column each thread, then pairs of blocks joined.
+  if (tid == 128) {
+    bulk_s2g(mine + lay.m, sm.m, 2 * kAtom);
+    bulk_commit();
+  }
+  // T: blocks of 8 on the diagonal by forward substitution, a column each thread, then pairs of blocks joined.
   if (tid < kC) {
-    const int b = tid / 16 * 16, c = tid % 16;
-    float x[16];
+    const int b = tid / 8 * 8, c = tid % 8;
+    float x[8];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
+    for (int r = 0; r < 8; ++r) {
+      const float4 f = *reinterpret_cast<const float4*>(&sm.a[b + r][b]), g = *reinterpret_cast<const float4*>(&sm.a[b + r][b + 4]);
+      const float l[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
       float acc = 0.f;
 #pragma unroll
-      for (int l = 0; l < r; l += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&sm.a[b + r][b + l]);
-        acc = fmaf(f.x, x[l], acc);
-        if (l + 1 < r) acc = fmaf(f.y, x[l + 1], acc);
-        if (l + 2 < r) acc = fmaf(f.z, x[l + 2], acc);
-        if (l + 3 < r) acc = fmaf(f.w, x[l + 3], acc);
-      }
+      for (int y = 0; y < r; ++y) acc = fmaf(l[y], x[y], acc);
       x[r] = r < c ? 0.f : r == c ? 1.f : -acc;
       sm.t[b + r][b + c] = x[r];
     }
   }
   __syncthreads();
-  join_blocks<16, 2>(sm.a, sm.t, sm.x);
-  join_blocks<32, 1>(sm.a, sm.t, sm.x);
+  join_blocks<8>(sm.a, sm.t, sm.x);
+  join_blocks<16>(sm.a, sm.t, sm.x);
+  join_blocks<32>(sm.a, sm.t, sm.x);
   {                                            // rows 0-63 T', 64-127 T' diag(e^G), three terms
     float v[32];
 #pragma unroll
@@ -400,13 +405,13 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
   __syncwarp();
   after_sync();
   if (upper) {
-    float* u = reinterpret_cast<float*>(mine + lay.u) + r * DV;
+    float4* u = reinterpret_cast<float4*>(mine + lay.u) + r;
 #pragma unroll
     for (int x = x0; x < DV; x += 64) {
       float v[32];
       tmem_values(quarter + kColD + x, v);
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(u + x + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      for (int j = 0; j < 32; j += 4) u[(x + j) / 4 * kC] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     }
   }
   before_sync();
@@ -423,9 +428,16 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
       tmem_values(quarter + kColD + x, v);
       uint32_t t[2][16];
       terms_of<2>(v, t);
-      row_to(mine + lay.w, kC, r, x, t[0]);
-      row_to(mine + lay.w + kC * DK * 2, kC, r, x, t[1]);
+      row_to(sm.qk, kC, r, x, t[0]);
+      row_to(sm.qk + kC * DK * 2, kC, r, x, t[1]);
     }
+    fence_async_smem();
+  }
+  __syncthreads();
+  if (tid == 128) {
+    bulk_s2g(mine + lay.w, sm.qk, 2 * kC * DK * 2);
+    bulk_commit();
+    bulk_wait_read();
   }
   if (!ok && tid == 0) {                       // a wait gave up: no MMA may be left in flight
     const uint64_t start = globaltimer();
@@ -437,12 +449,25 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
 }
 
 // ---- through the state ----------------------------------------------------------------------------------------------
-// Warps 0-7 own the state S^T, thread by thread one k (lane quarter warp % 4) and 32 of the 64 rows (warp / 4); those of quarters
-// 2 and 3 make U, those of 0 and 1 the outputs.  Warp 8 loads, warp 9 issues.
+// P rows of a head's state a CTA.  Warps 0-7 own the state S^T, thread by thread one k (lane quarter warp % 4) and half of the rows
+// (warp / 4); those of quarters 2 and 3 make U, those of 0 and 1 the outputs.  Warp 8 loads, warp 9 issues.
 constexpr int kOwners = 256, kLoadThread = 256, kThrough = 320;
-// Products with an operand of two terms take both as 128 columns: the other operand is read once, and the halves are added
+// Products with an operand of two terms take both as 2 P columns: the other operand is read once, and the halves are added
 // up by those who read them.
-constexpr uint32_t kCol1 = 0, kCol2 = 128, kCol3 = 192, kColO = 320, kThroughCols = 512;
+template <int P>
+struct Cols {
+  static constexpr uint32_t one = 0, two = 2 * P, three = 3 * P, out = 5 * P, all = P == 64 ? 512 : 256;
+};
+
+// the sums of columns and those P further on
+template <int P, int X>
+__device__ __forceinline__ void tmem_sums(uint32_t at, float (&v)[X]) {
+  float w[X];
+  tmem_values(at, v);
+  tmem_values(at + P, w);
+#pragma unroll
+  for (int j = 0; j < X; ++j) v[j] += w[j];
+}
 
 struct Hdr {
   uint64_t full[2], empty[2], s_ready, u_ready, u_decayed, u_written, s_done, o_done, o_free;
@@ -450,15 +475,16 @@ struct Hdr {
   int dead;                                  // a wait gave up: no further wait waits, no copy or MMA is issued
 };
 
-// Shared memory: two stages, S^T as two terms [dk x 64], U and the decayed U as two terms each [64 x 64].
+// Shared memory: two stages, S^T as two terms side by side [dk x 2 P], U and the decayed U as two terms each [64 x 2 P].
 // A stage: for each 64 columns Q's and W hi's atoms, one A operand of 128 rows; W lo's, as rows 64-127 of one whose other rows are
 // whatever lies before; M hi and lo, rows 0-63 of two whose others are what lies behind; K; the factors.
-template <int DK>
+template <int DK, int P>
 struct Stage {
   static constexpr uint32_t atoms = DK / 64, wlo = 2 * atoms * kAtom, m = wlo + atoms * kAtom, k = m + 2 * kAtom,
                             f = k + atoms * kAtom, size = f + sizeof(Factors);
   static constexpr uint32_t bytes = size;      // all of it arrives by copies
-  static constexpr uint32_t s = 2 * size, u = s + 2 * DK * 128, hdr = u + 4 * kAtom, smem = hdr + sizeof(Hdr);
+  static constexpr uint32_t term = P / 32 * kAtom;                 // both terms of U
+  static constexpr uint32_t s = 2 * size, u = s + P / 32 * DK * 128, hdr = u + 2 * term, smem = hdr + sizeof(Hdr);
   static_assert(smem <= 227 * 1024 && size % 1024 == 0, "one CTA's shared memory; whole swizzle groups");
 };
 
@@ -478,12 +504,14 @@ __device__ __forceinline__ bool wait(Hdr& hd, uint64_t* bar, uint32_t parity, in
 }
 __device__ __forceinline__ bool dead(const Hdr& hd) { return *(const volatile int*)&hd.dead != 0; }
 
-template <int DK>
+template <int DK, int P>
 __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_constant__ DeltaArgs a) {
-  using St = Stage<DK>;
+  using St = Stage<DK, P>;
+  using Col = Cols<P>;
+  constexpr int X = P / 2;                     // state rows of a thread
   extern __shared__ __align__(1024) uint8_t gdn_smem[];
   Hdr& hd = *reinterpret_cast<Hdr*>(gdn_smem + St::hdr);
-  const int parts = a.dv / kPart, part = blockIdx.x % parts, unit = blockIdx.x / parts, i = unit / a.H, h = unit % a.H;
+  const int parts = a.dv / P, part = blockIdx.x % parts, unit = blockIdx.x / parts, i = unit / a.H, h = unit % a.H;
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0), lane = tid % 32;
   if (!ascending(a) || (smem_u32(gdn_smem) & 1023u) != 0) {
     if (tid == 0) report(a.status, (smem_u32(gdn_smem) & 1023u) != 0 ? ERS_ECUDA : ERS_EINVAL);
@@ -491,12 +519,12 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
   }
   DeltaSeq seq;
   if (!delta_seq(a, i, h, &seq)) return;
-  const int chunks = (seq.len + kC - 1) / kC, d0 = part * kPart;
+  const int chunks = (seq.len + kC - 1) / kC, d0 = part * P;
   const Layout lay(a.H, a.G, DK, a.dv);
   const uint8_t* first = static_cast<const uint8_t*>(a.ws) + (seq.t0 / kC + i) * lay.chunk;
   const uint8_t *mine = first + (size_t)h * lay.head, *shared = first + (size_t)a.H * lay.head + (size_t)(h / (a.H / a.G)) * lay.group;
 
-  if (warp == 9) tmem_alloc(&hd.tmem, kThroughCols);
+  if (warp == 9) tmem_alloc(&hd.tmem, Col::all);
   if (tid == kLoadThread) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&hd.full[b], 1);
@@ -540,8 +568,8 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
     }
   } else if (warp == 9) {
     // ---- products --------------------------------------------------------------------------------------------
-    constexpr uint32_t id = idesc_bf16(128, kPart, false, true), id2 = idesc_bf16(128, 2 * kPart, false, true),
-                       id3 = idesc_bf16(128, 2 * kPart, true, true);
+    constexpr uint32_t id = idesc_bf16(128, P, false, true), id2 = idesc_bf16(128, 2 * P, false, true),
+                       id3 = idesc_bf16(128, 2 * P, true, true);
     const bool leader = elected();
     const uint32_t st = smem_u32(gdn_smem + St::s), ut = smem_u32(gdn_smem + St::u);
 #pragma unroll 1
@@ -552,10 +580,10 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       if (leader) {
 #pragma unroll
         for (int k = 0; k < DK / 16; ++k)      // rows 0-63 Q S^T, 64-127 W S^T
-          mma(tb + kCol1, sdesc(base + (k >> 2) * 2 * kAtom + (k & 3) * 32, 16, 1024), sdesc(st + k * 2048, DK * 128, 1024), id2, k > 0);
+          mma(tb + Col::one, sdesc(base + (k >> 2) * 2 * kAtom + (k & 3) * 32, 16, 1024), sdesc(st + k * 2048, DK * 128, 1024), id2, k > 0);
 #pragma unroll
         for (int k = 0; k < DK / 16; ++k)      // rows 64-127
-          mma(tb + kCol2, sdesc(base + St::wlo - kAtom + (k >> 2) * kAtom + (k & 3) * 32, 16, 1024),
+          mma(tb + Col::two, sdesc(base + St::wlo - kAtom + (k >> 2) * kAtom + (k & 3) * 32, 16, 1024),
               sdesc(st + k * 2048, DK * 128, 1024), id, k > 0);
         commit(&hd.u_ready);
       }
@@ -564,7 +592,7 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       if (leader) {
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k)      // K^T U'
-          mma(tb + kCol3, sdesc(base + St::k + k * 2048, kAtom, 1024), sdesc(ut + 2 * kAtom + k * 2048, kAtom, 1024), id3, k > 0);
+          mma(tb + Col::three, sdesc(base + St::k + k * 2048, kAtom, 1024), sdesc(ut + St::term + k * 2048, kAtom, 1024), id3, k > 0);
         commit(&hd.s_done);
       }
       if (!wait(hd, &hd.u_written, c, a.status) || (c > 0 && !wait(hd, &hd.o_free, c - 1, a.status))) break;
@@ -572,61 +600,61 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       if (leader) {
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k)      // M hi U
-          mma(tb + kColO, sdesc(base + St::m + k * 32, 16, 1024), sdesc(ut + k * 2048, kAtom, 1024), id2, k > 0);
+          mma(tb + Col::out, sdesc(base + St::m + k * 32, 16, 1024), sdesc(ut + k * 2048, kAtom, 1024), id2, k > 0);
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k)      // M lo U hi
-          mma(tb + kColO, sdesc(base + St::m + kAtom + k * 32, 16, 1024), sdesc(ut + k * 2048, kAtom, 1024), id, 1);
+          mma(tb + Col::out, sdesc(base + St::m + kAtom + k * 32, 16, 1024), sdesc(ut + k * 2048, kAtom, 1024), id, 1);
         commit(&hd.o_done);
         commit(&hd.empty[c & 1]);
       }
     }
   } else {
     // ---- the state, U and the outputs ------------------------------------------------------------------------
-    const int r = tid % 128, x0 = tid / 128 * 32, row = r % kC;   // k of the state; token of U or the outputs
+    const int r = tid % 128, x0 = tid / 128 * X, row = r % kC;   // k of the state; token of U or the outputs
     const bool makes_u = r >= kC, holds = r < DK;
     const uint32_t quarter = tb + ((uint32_t)(r & ~31) << 16);
-    float s[32];
+    float s[X];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) s[j] = holds && seq.in != nullptr ? seq.in[(size_t)(d0 + x0 + j) * DK + r] : 0.f;
+    for (int j = 0; j < X; ++j) s[j] = holds && seq.in != nullptr ? seq.in[(size_t)(d0 + x0 + j) * DK + r] : 0.f;
     bool poisoned = false;
-    float u[32], since = 0.f;                  // U, or the last chunk's Q S^T, and its rows' factors
+    float u[X], since = 0.f;                  // U, or the last chunk's Q S^T, and its rows' factors
     int bad = kC;
     bool spoiled = false;
     const auto outputs = [&](int c) {          // of chunk c
       wait(hd, &hd.o_done, c, a.status);
       __syncwarp();
       after_sync();
-      float o[32];
-      tmem_sums(quarter + kColO + x0, o);
+      float o[X];
+      tmem_sums<P>(quarter + Col::out + x0, o);
       before_sync();
       mbar_arrive(&hd.o_free);
       if (row >= seq.len - c * kC || dead(hd)) return;
       bf16* to = (bf16*)a.o + ((size_t)(seq.t0 + c * kC + row) * a.H + h) * a.dv + d0 + x0;
-      uint32_t w[16];
+      uint32_t w[X / 2];
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
+      for (int j = 0; j < X / 2; ++j)
         w[j] = spoiled ? 0x7fff7fffu : pack_bf16x2(a.scale * fmaf(since, u[2 * j], o[2 * j]), a.scale * fmaf(since, u[2 * j + 1], o[2 * j + 1]));
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) *reinterpret_cast<uint4*>(to + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+      for (int j = 0; j < X / 2; j += 4) *reinterpret_cast<uint4*>(to + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
     };
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       // the state as an operand
       if (holds) {
-        uint32_t t[2][16];
+        uint32_t t[2][X / 2];
         terms_of<2>(s, t);
         row_to(gdn_smem + St::s, DK, r, x0, t[0]);
-        row_to(gdn_smem + St::s + DK * 128, DK, r, x0, t[1]);
+        row_to(gdn_smem + St::s, DK, r, P + x0, t[1]);
       }
       fence_async_smem();
       before_sync();
       mbar_arrive(&hd.s_ready);
       if (!makes_u && c > 0) outputs(c - 1);
       if (makes_u) {                           // on its way while the product is
-        const float* u0 = reinterpret_cast<const float*>(mine + c * lay.chunk + lay.u) + row * a.dv + d0 + x0;
+        const float4* u0 = reinterpret_cast<const float4*>(mine + c * lay.chunk + lay.u) + (d0 + x0) / 4 * kC + row;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(u0 + j);
+        for (int j = 0; j < X; j += 4) {
+          const float4 v = u0[j / 4 * kC];
           u[j] = v.x;
           u[j + 1] = v.y;
           u[j + 2] = v.z;
@@ -645,46 +673,46 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       __syncwarp();
       after_sync();
       if (makes_u) {
-        float v[32];
-        tmem_sums(quarter + kCol1 + x0, v);
+        float v[X];
+        tmem_sums<P>(quarter + Col::one + x0, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) u[j] -= v[j];
-        tmem_values(quarter + kCol2 + x0, v);
+        for (int j = 0; j < X; ++j) u[j] -= v[j];
+        tmem_values(quarter + Col::two + x0, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < X; ++j) {
           u[j] -= v[j];
           v[j] = u[j] * left;
         }
-        uint32_t t[2][16];                     // first what the state waits for
+        uint32_t t[2][X / 2];                     // first what the state waits for
         terms_of<2>(v, t);
-        row_to(gdn_smem + St::u + 2 * kAtom, kC, row, x0, t[0]);
-        row_to(gdn_smem + St::u + 3 * kAtom, kC, row, x0, t[1]);
+        row_to(gdn_smem + St::u + St::term, kC, row, x0, t[0]);
+        row_to(gdn_smem + St::u + St::term, kC, row, P + x0, t[1]);
         fence_async_smem();
         before_sync();
         mbar_arrive(&hd.u_decayed);
         if (c > 0) wait(hd, &hd.o_done, c - 1, a.status);   // U's tiles have been read
         terms_of<2>(u, t);
         row_to(gdn_smem + St::u, kC, row, x0, t[0]);
-        row_to(gdn_smem + St::u + kAtom, kC, row, x0, t[1]);
+        row_to(gdn_smem + St::u, kC, row, P + x0, t[1]);
         fence_async_smem();
         mbar_arrive(&hd.u_written);
       } else {
-        tmem_sums(quarter + kCol1 + x0, u);
+        tmem_sums<P>(quarter + Col::one + x0, u);
         before_sync();
       }
       wait(hd, &hd.s_done, c, a.status);
       __syncwarp();
       after_sync();
-      float v[32];
-      tmem_sums(quarter + kCol3 + x0, v);
+      float v[X];
+      tmem_sums<P>(quarter + Col::three + x0, v);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) s[j] = fmaf(whole, s[j], v[j]);
+      for (int j = 0; j < X; ++j) s[j] = fmaf(whole, s[j], v[j]);
       before_sync();
     }
     if (chunks > 0 && !makes_u) outputs(chunks - 1);
     if (holds && !dead(hd)) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) seq.out[(size_t)(d0 + x0 + j) * DK + r] = poisoned ? __int_as_float(0x7fffffff) : s[j];
+      for (int j = 0; j < X; ++j) seq.out[(size_t)(d0 + x0 + j) * DK + r] = poisoned ? __int_as_float(0x7fffffff) : s[j];
     }
   }
   __syncwarp();
@@ -694,7 +722,7 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
   }
   before_sync();
   __syncthreads();
-  if (warp == 9) tmem_dealloc(tb, kThroughCols);
+  if (warp == 9) tmem_dealloc(tb, Col::all);
 }
 
 // ---- host side ---------------------------------------------------------------------------------------------------------
@@ -711,18 +739,26 @@ cudaError_t allow(F kernel, int smem, bool (&done)[64], std::mutex& mu) {   // i
   return e;
 }
 
+template <int DK, int P>
+cudaError_t launch_through(const DeltaArgs& a, cudaStream_t s) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  const cudaError_t e = allow(k_gdn_through<DK, P>, Stage<DK, P>::smem, done, mu);
+  if (e != cudaSuccess) return e;
+  k_gdn_through<DK, P><<<(unsigned)((long long)a.nseq * a.H * (a.dv / P)), kThrough, Stage<DK, P>::smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <int DK, int DV>
 cudaError_t launch(const DeltaArgs& a, cudaStream_t s) {
   static std::mutex mu;
-  static bool inside[64] = {}, through[64] = {};
-  cudaError_t e = allow(k_gdn_inside<DK, DV>, sizeof(InsideSmem<DK, DV>), inside, mu);
-  if (e == cudaSuccess) e = allow(k_gdn_through<DK>, Stage<DK>::smem, through, mu);
+  static bool done[64] = {};
+  cudaError_t e = allow(k_gdn_inside<DK, DV>, sizeof(InsideSmem<DK, DV>), done, mu);
   if (e != cudaSuccess) return e;
   k_gdn_inside<DK, DV><<<dim3((unsigned)chunk_numbers(a.ntokens, a.nseq), a.H), kInside, sizeof(InsideSmem<DK, DV>), s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  k_gdn_through<DK><<<(unsigned)((long long)a.nseq * a.H * (DV / kPart)), kThrough, Stage<DK>::smem, s>>>(a);
-  return cudaGetLastError();
+  return (long long)a.nseq * a.H * (DV / 32) <= 152 ? launch_through<DK, 32>(a, s) : launch_through<DK, 64>(a, s);
 }
 
 }  // namespace
