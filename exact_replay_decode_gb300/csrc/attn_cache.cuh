@@ -21,9 +21,14 @@ __device__ __forceinline__ int32_t attn_seq(const AttnArgs& a, int i, AttnSeq* s
   return ERS_OK;
 }
 
+// The page of a slot that token `at` is in
+__device__ __forceinline__ int page_of(const AttnArgs& a, int at) {
+  return (int)((__umulhi(a.page_magic, (uint32_t)at) + (uint32_t)at) >> a.page_shift);
+}
+
 // The pool's row of token `at` of a slot, of those that the table has room for; -1 where its page is none of the pool's.
 __device__ __forceinline__ long long attn_row(const AttnArgs& a, const int32_t* pages, int at) {
-  const int n = at / a.page_tokens, page = pages[n];
+  const int n = page_of(a, at), page = pages[n];
   return page < 0 || page >= a.npages ? -1 : (long long)page * a.page_tokens + (at - n * a.page_tokens);
 }
 

@@ -211,7 +211,7 @@ __device__ __forceinline__ int32_t room_for(const AttnArgs& a, int i, const Attn
   if (s.pos + (long long)n > (long long)a.slot_pages * a.page_tokens) {
     err = ERS_EOVERFLOW;
   } else if (n > 0) {
-    const int first = s.pos / a.page_tokens, last = (s.pos + n - 1) / a.page_tokens;
+    const int first = page_of(a, s.pos), last = page_of(a, s.pos + n - 1);
     for (int x = first + threadIdx.x; x <= last; x += blockDim.x) {
       const int page = s.pages[x];
       if (page < 0 || page >= a.npages) err = ERS_ESLOT;

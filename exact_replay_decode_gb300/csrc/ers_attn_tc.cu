@@ -7,10 +7,13 @@
 // with c = scale log2 e (P by powers of two) and m a running maximum that moves, and O with it, only when a row's maximum has
 // risen by more than 2^8: P then stays below 2^8, which costs no bits.
 //
-// Four warps own the rows, a thread each (a tile's scores of a row stay in its registers), four load tiles (any page size:
-// 16-byte copies that fill with zeros behind the last token), one issues the MMAs: S of the next tile before P V of this one, so
-// that the tensor core works under the exponentials.  Two CTAs per SM (two stages of 32 KB each at D 128, 256 columns of tensor
+// Four warps own the rows, a thread each (a tile's scores of a row stay in its registers), two load tiles, one issues the MMAs: S
+// of the next tile before P V of this one if the tile is there, so that the tensor core works under the exponentials.  Whole
+// tiles of pages whose tokens are a multiple of 8 come by TMA, `box` tokens at a time; others, and the last one (zeros behind
+// the last token: a page may hold anything there), by 16-byte copies of both warps.  Two CTAs per SM (two stages of 32 KB each at D 128, 256 columns of tensor
 // memory) run beside each other: one loads while the other computes.
+#include <string.h>
+
 #include <mutex>
 
 #include "attn_cache.cuh"
@@ -18,6 +21,7 @@
 #include "ers_internal.h"
 #include "tc_common.cuh"
 #include "tc_terms.cuh"
+#include "tma_host.h"
 
 namespace ers {
 namespace {
@@ -26,7 +30,7 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kM = 128, kTokens = 64, kStages = 2;
-constexpr int kLoadThread = 128, kLoaders = 128, kIssueThread = 256, kBlock = 288;
+constexpr int kLoadThread = 128, kLoaders = 64, kIssueThread = 192, kBlock = 224;   // (nine warps would have 96 registers each, and spill)
 constexpr uint32_t kColS = 0, kColO = 128, kCols = 256;   // two tiles' scores, the outputs
 constexpr float kRise = 8.f;
 
@@ -60,6 +64,14 @@ __device__ __forceinline__ bool wait(Hdr& hd, uint64_t* bar, uint32_t parity, in
 }
 __device__ __forceinline__ bool dead(const Hdr& hd) { return *(const volatile int*)&hd.dead != 0; }
 
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {   // without waiting
+  uint32_t done;
+  asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(done)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ float exp2_of(float x) {   // 2 units in the last place; 0 below 2^-126
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -74,8 +86,13 @@ __device__ __forceinline__ bool not_finite(uint32_t u) {
   return (u & 0x7f800000u) == 0x7f800000u || (u & 0x7f80u) == 0x7f80u;
 }
 
+struct Maps {
+  CUtensorMap k, v;
+};
+
+// box: tokens of a TMA copy, a divisor of a page's and of a tile's; 0: none
 template <int D>
-__global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant__ AttnArgs a, const __grid_constant__ Maps maps, int box) {
   using Sh = Shape<D>;
   extern __shared__ uint8_t attn_smem[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(attn_smem) + 1023) & ~uintptr_t(1023));
@@ -153,7 +170,9 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
     bool ok = scores(0);
 #pragma unroll 1
     for (int n = 0; ok && n < tiles; ++n) {
-      if (n + 1 < tiles && !scores(n + 1)) break;
+      bool ahead = n + 1 < tiles;
+      if (ahead && !__all_sync(kFull, mbar_test(&hd.full[(n + 1) % kStages], (n + 1) / kStages & 1))) ahead = false;
+      if (ahead && !scores(n + 1)) break;
       if (!wait(hd, &hd.p_ready, n, a.status)) break;
       after_sync();
       const int b = n % kStages;
@@ -165,53 +184,97 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
         commit(&hd.empty[b]);
         commit(&hd.o_done);
       }
+      if (!ahead && n + 1 < tiles && !scores(n + 1)) break;
     }
   } else if (tid >= kLoadThread) {
     // ---- the loading warps: a tile's rows by 8 (D 64) or 16 neighbouring threads --------------------------
     constexpr int kPer = D / 8, kStep = kLoaders / kPer;
+    constexpr int kEach = kTokens / kStep;     // a thread's rows; at least the 8 boxes that a tile may be of
+    static_assert(kEach >= 8, "pages of all boxes");
     const int t = tid - kLoadThread, c = t % kPer * 8, r0 = t / kPer;
-    for (int n = 0; n <= tiles; ++n) {
-      if (n > 0) {                             // the tile before this one has arrived: told before any wait for its stage's turn
-        copies_wait();
-        fence_async_smem();
-        mbar_arrive(&hd.full[(n - 1) % kStages]);
-      }
-      if (n < tiles) {
-        const int b = n % kStages;
-        if (n >= kStages) wait(hd, &hd.empty[b], n / kStages - 1, a.status);
-        uint8_t *kt = stages + b * 2 * Sh::tile, *vt = kt + Sh::tile;
-        if (dead(hd)) {
-        } else if (n < past) {
-          const int t0 = (int)begin + n * kTokens;
+    // Pages are looked up a tile ahead, all at once: one after the other they took longer than the copies.
+    const int boxes = box > 0 ? kTokens / box : 0, whole = box > 0 && begin < end ? (int)((end - begin) / kTokens) : 0;
+    int page[kEach];
+    bool missing = false;
+    const auto look_up = [&](int n) {
 #pragma unroll
-          for (int x = 0; x < kTokens / kStep; ++x) {
-            const int r = r0 + x * kStep;
-            const long long at = t0 + r < end ? attn_row(a, s.pages, t0 + r) : -1;
-            if (at < 0 && t0 + r < end) report(a.status, ERS_ESLOT);
-            const size_t from = at < 0 ? 0 : ((size_t)at * a.KV + kv) * D + c;
-            copy16(kt + sw128(kTokens, r, c), (const bf16*)a.k_pages + from, at >= 0);
-            copy16(vt + sw128(kTokens, r, c), (const bf16*)a.v_pages + from, at >= 0);
+      for (int x = 0; x < kEach; ++x) {
+        const int at = (int)begin + n * kTokens + (n < whole ? x * box : r0 + x * kStep);
+        page[x] = n < past && at < end && (n >= whole || x < boxes) ? s.pages[page_of(a, at)] : -1;
+      }
+    };
+    look_up(0);
+    bool pending = false;                      // this thread's copies of the tile before
+    const auto arrive = [&](int n) {
+      if (!pending) return;
+      copies_wait();
+      fence_async_smem();
+      mbar_arrive(&hd.full[n % kStages]);
+      pending = false;
+    };
+    for (int n = 0; n < tiles; ++n) {
+      arrive(n - 1);                           // told before any wait for its stage's turn
+      const int b = n % kStages;
+      if (n >= kStages) wait(hd, &hd.empty[b], n / kStages - 1, a.status);
+      uint8_t *kt = stages + b * 2 * Sh::tile, *vt = kt + Sh::tile;
+      if (n < whole) {
+        if (t == 0 && !dead(hd)) {
+          uint32_t count = 0;
+#pragma unroll
+          for (int x = 0; x < kEach; ++x) count += page[x] >= 0 && page[x] < a.npages;
+          missing |= count < (uint32_t)boxes;
+          mbar_arrive_expect_tx(&hd.full[b], count * box * D * 4);
+#pragma unroll
+          for (int x = 0; x < kEach; ++x) {
+            if (page[x] < 0 || page[x] >= a.npages) continue;
+            const int at = (int)begin + n * kTokens + x * box, row = page[x] * a.page_tokens + (at - page_of(a, at) * a.page_tokens);
+#pragma unroll
+            for (int d = 0; d < D; d += 64) {
+              tma_load_3d(kt + d * kTokens * 2 + x * box * 128, &maps.k, d, kv, row, &hd.full[b]);
+              tma_load_3d(vt + d * kTokens * 2 + x * box * 128, &maps.v, d, kv, row, &hd.full[b]);
+            }
           }
         } else {
-          // Drafts: a value that is not finite would reach rows that do not see it as 0 x infinity, so it is left out, and
-          // those that see it are made NaN at the end.
-          for (int r = r0; r < kTokens; r += kStep) {
-            uint4 k = make_uint4(0, 0, 0, 0), v = k;
-            if (r < a.T) {
-              const size_t from = (((size_t)i * a.T + r) * a.KV + kv) * D + c;
-              k = *reinterpret_cast<const uint4*>((const bf16*)a.k + from);
-              v = *reinterpret_cast<const uint4*>((const bf16*)a.v + from);
-              if (not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w)) {
-                atomicOr(reinterpret_cast<unsigned long long*>(&hd.bad), 1ull << r);
-                v = make_uint4(0, 0, 0, 0);
-              }
-            }
-            *reinterpret_cast<uint4*>(kt + sw128(kTokens, r, c)) = k;
-            *reinterpret_cast<uint4*>(vt + sw128(kTokens, r, c)) = v;
+          mbar_arrive(&hd.full[b]);
+        }
+        look_up(n + 1);
+        continue;
+      }
+      pending = true;
+      if (dead(hd)) continue;
+      if (n < past) {
+#pragma unroll
+        for (int x = 0; x < kEach; ++x) {
+          const int r = r0 + x * kStep, at = (int)begin + n * kTokens + r;
+          const bool there = page[x] >= 0 && page[x] < a.npages;
+          missing |= !there && at < end;
+          const size_t row = there ? (size_t)page[x] * a.page_tokens + (at - page_of(a, at) * a.page_tokens) : 0;
+          const size_t from = (row * a.KV + kv) * D + c;
+          copy16(kt + sw128(kTokens, r, c), (const bf16*)a.k_pages + from, there);
+          copy16(vt + sw128(kTokens, r, c), (const bf16*)a.v_pages + from, there);
+        }
+        look_up(n + 1);
+        continue;
+      }
+      // Drafts: a value that is not finite would reach rows that do not see it as 0 x infinity, so it is left out, and
+      // those that see it are made NaN at the end.
+      for (int r = r0; r < kTokens; r += kStep) {
+        uint4 k = make_uint4(0, 0, 0, 0), v = k;
+        if (r < a.T) {
+          const size_t from = (((size_t)i * a.T + r) * a.KV + kv) * D + c;
+          k = *reinterpret_cast<const uint4*>((const bf16*)a.k + from);
+          v = *reinterpret_cast<const uint4*>((const bf16*)a.v + from);
+          if (not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w)) {
+            atomicOr(reinterpret_cast<unsigned long long*>(&hd.bad), 1ull << r);
+            v = make_uint4(0, 0, 0, 0);
           }
         }
+        *reinterpret_cast<uint4*>(kt + sw128(kTokens, r, c)) = k;
+        *reinterpret_cast<uint4*>(vt + sw128(kTokens, r, c)) = v;
       }
     }
+    arrive(tiles - 1);
+    if (missing) report(a.status, ERS_ESLOT);
   } else {
     // ---- the rows -------------------------------------------------------------------------------------------
     const float c = a.scale * 1.44269504088896340736f;
@@ -324,6 +387,18 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
   if (warp == kIssueThread / 32) tmem_dealloc(tb, kCols);
 }
 
+bool encode(CUtensorMap* m, const void* base, long long rows, int heads, int d, int box_rows) {
+  const EncodeTiledFn fn = tma_encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * heads * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+  const cuuint32_t each[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, each,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   static std::mutex mu;
@@ -341,7 +416,15 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     }
   }
   const int tiles = (a.T * (a.H / a.KV) + kM - 1) / kM;
-  k_attn_tiles<D><<<dim3((unsigned)(a.nseq * a.nsplit), tiles * a.KV), kBlock, Shape<D>::smem, s>>>(a);
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  int box = kTokens;
+  while (a.page_tokens % box != 0) box /= 2;
+  const long long rows = (long long)a.npages * a.page_tokens;
+  if (box < 8 || rows < box || rows > 0x7fffffff || !encode(&maps.k, a.k_pages, rows, a.KV, D, box) ||
+      !encode(&maps.v, a.v_pages, rows, a.KV, D, box))
+    box = 0;
+  k_attn_tiles<D><<<dim3((unsigned)(a.nseq * a.nsplit), tiles * a.KV), kBlock, Shape<D>::smem, s>>>(a, maps, box);
   return cudaGetLastError();
 }
 

@@ -120,6 +120,9 @@ ers::AttnArgs attn_args(const ers_attn_dims* d, const ers_attn_cache* c, int32_t
     a.slot_pages = c->slot_pages;
     a.npages = c->npages;
     a.page_tokens = c->page_tokens;
+    // division by multiplication (Granlund and Montgomery, 1994): 2^shift >= page_tokens, magic = 2^32 (2^shift / page_tokens - 1) + 1
+    while ((1ll << a.page_shift) < a.page_tokens) ++a.page_shift;
+    a.page_magic = (uint32_t)((((1ull << a.page_shift) - (uint64_t)a.page_tokens) << 32) / (uint64_t)a.page_tokens + 1);
   }
   a.slot = slot;
   a.k = k;

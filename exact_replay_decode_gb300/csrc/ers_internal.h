@@ -280,6 +280,8 @@ struct AttnArgs {
   const int32_t* refs;      // [npages]
   int32_t* pos;             // [nslots]
   int nslots, slot_pages, npages, page_tokens;
+  uint32_t page_magic;      // at / page_tokens is (umulhi(page_magic, at) + at) >> page_shift, at < 2^31
+  int page_shift;
   const int32_t* slot;
   float* part;              // nsplit > 1: [nseq, T, H, nsplit] (max, sum), then [nseq, T, H, nsplit, D] outputs
   const int32_t* cu;        // append: [nseq + 1]
