@@ -6,6 +6,9 @@
 
 namespace ers {
 
+// Of `all` parts of rows, the workspace holds a maximum and a sum each, then, from this float on, their outputs (16-byte aligned).
+__host__ __device__ __forceinline__ size_t part_outputs(size_t all) { return (2 * all + 3) & ~size_t(3); }
+
 struct AttnSeq {
   const int32_t* pages;   // the slot's row of the table
   int slot, pos;          // tokens of the past

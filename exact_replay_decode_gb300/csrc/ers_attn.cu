@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_attn_rows(const __grid_constant
       const size_t at = out_row(r) * a.nsplit + split, all = (size_t)a.nseq * a.T * a.H * a.nsplit;
       if (lane == 0) reinterpret_cast<float2*>(a.part)[at] = make_float2(m[x], l[x]);
 #pragma unroll
-      for (int c = 0; c < C; ++c) a.part[2 * all + at * D + lane + 32 * c] = o[x][c];
+      for (int c = 0; c < C; ++c) a.part[part_outputs(all) + at * D + lane + 32 * c] = o[x][c];
     }
   }
 }
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ 
   const int lane = threadIdx.x % 32;
   if (row >= rows) return;
   const float2* ml = reinterpret_cast<const float2*>(a.part) + row * a.nsplit;
-  const float* part = a.part + 2 * rows * a.nsplit + row * a.nsplit * D;
+  const float* part = a.part + part_outputs(rows * a.nsplit) + row * a.nsplit * D;
   float m = -INFINITY;
   bool failed = false;
   for (int s = lane; s < a.nsplit; s += 32) {
@@ -172,13 +172,17 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ 
   for (int off = 16; off >= 1; off /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
   if (__any_sync(kFull, failed)) return;       // reported; nothing is written
   float l = 0.f, o[C] = {};
+#pragma unroll 8
   for (int s = 0; s < a.nsplit; ++s) {
     const float2 v = ml[s];
-    if (v.y == 0.f) continue;                  // saw nothing
-    const float f = expf(v.x - m);
+    const bool saw = v.y != 0.f;               // (one that saw nothing may have left its outputs unwritten)
+    const float f = saw ? expf(v.x - m) : 0.f;
     l = fmaf(v.y, f, l);
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = fmaf(part[(size_t)s * D + lane + 32 * c], f, o[c]);
+    for (int c = 0; c < C; ++c) {
+      const float x = part[(size_t)s * D + lane + 32 * c];
+      o[c] = fmaf(saw ? x : 0.f, f, o[c]);
+    }
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) ((T*)a.o)[row * D + lane + 32 * c] = from_f<T>(l == 0.f ? 0.f : o[c] / l);
@@ -295,20 +299,32 @@ __global__ void __launch_bounds__(kThreads) k_attn_commit(const __grid_constant_
 
 }  // namespace
 
+// Parts of a past: what takes the least time by a model in tiles of 64 tokens, each CTA some 4 beside its own, of as many CTAs
+// as run at once (two a SM on the tensor cores, four of the fp32 kernel).  By 1, 2, 4, 8, 16 and 32 parts, us (without the model's
+// finer ones): 1 x 32768 tokens 859, 435, 230, 123, 72, 53; 8 x 8192 228, 123, 78, 87, 101, 126; 16 x 4096, 64 drafts
+// 142, 176, 207, 263; 64 x 4096 261, 289, 335, 420 (before later steps).
 void attn_plan(AttnArgs* a, int max_len) {
-  const int each = a->io == ERS_DTYPE_BF16 ? 128 : kRows, tiles = (a->T * (a->H / a->KV) + each - 1) / each;
-  const long long units = (long long)a->nseq * a->KV * tiles;
-  const long long blocks = (max_len + 255) / 256;
-  long long n = 608 / (units < 1 ? 1 : units);
-  n = n < 1 ? 1 : n > blocks ? (blocks < 1 ? 1 : blocks) : n;
-  a->per = (int)((blocks + n - 1) / n * 256);
-  if (a->per < 256) a->per = 256;
-  a->nsplit = (int)((max_len + (long long)a->per - 1) / a->per);
-  if (a->nsplit < 1) a->nsplit = 1;
+  const bool tiles_of = a->io == ERS_DTYPE_BF16;
+  const int each = tiles_of ? 128 : kRows, slots = tiles_of ? 304 : 608, rows = a->T * (a->H / a->KV);
+  const long long units = (long long)a->nseq * a->KV * ((rows + each - 1) / each), tokens = max_len;
+  const int blocks = (int)((tokens + 63) / 64);
+  int per = blocks < 1 ? 1 : blocks;
+  long long least = 0;
+  for (int n = 1; n <= 64 && n <= blocks; ++n) {
+    const int p = (blocks + n - 1) / n;
+    const long long parts = (blocks + p - 1) / p, cost = (units * parts + slots - 1) / slots * (p + 4);
+    if (n == 1 || cost < least) {
+      least = cost;
+      per = p;
+    }
+  }
+  a->per = (int)(per > 0x1000000 ? 0x40000000 : per * 64);
+  a->nsplit = blocks < 1 ? 1 : (blocks + per - 1) / per;
 }
 
 size_t attn_workspace(const AttnArgs& a) {
-  return a.nsplit == 1 ? 0 : align256((size_t)a.nseq * a.T * a.H * a.nsplit * (a.D + 2) * sizeof(float));
+  const size_t all = (size_t)a.nseq * a.T * a.H * a.nsplit;
+  return a.nsplit == 1 ? 0 : align256((part_outputs(all) + all * a.D) * sizeof(float));
 }
 
 cudaError_t attn_verify(const AttnArgs& a, cudaStream_t s) {

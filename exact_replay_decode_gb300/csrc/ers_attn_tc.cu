@@ -35,7 +35,7 @@ constexpr uint32_t kColS = 0, kColO = 128, kCols = 256;   // two tiles' scores, 
 constexpr float kRise = 8.f;
 
 struct Hdr {
-  uint64_t full[kStages], empty[kStages], s_ready[2], p_ready, o_done;
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], s_ready[2], p_ready, o_done;
   uint64_t bad;                      // drafts whose values are not finite
   int32_t parent[kMaxDrafts];
   uint32_t tmem;
@@ -104,50 +104,98 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
   const auto out_row = [&](int r) { return ((size_t)i * a.T + r / rep) * a.H + kv * rep + r % rep; };
   AttnSeq s;
   int32_t err = attn_seq(a, i, &s);
+  uint4 q[D / 8];
+  if (tid < kM) {
+    const bf16* from = (const bf16*)a.q + (row < nrows ? out_row(row) * D : 0);
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x) q[x] = row < nrows ? *reinterpret_cast<const uint4*>(from + 8 * x) : make_uint4(0, 0, 0, 0);
+  }
   if (a.parent != nullptr && tid < a.T) hd.parent[tid] = a.parent[(size_t)i * a.T + tid];
-  if (tid == 0) hd.bad = 0;
+  const bool last = split == a.nsplit - 1;
+  const long long begin = (long long)split * a.per;
+  const int end = err != ERS_OK ? 0 : last ? s.pos : (int)min((long long)s.pos, begin + a.per);
+  const int past = begin < end ? (int)((end - begin + kTokens - 1) / kTokens) : 0, tiles = past + (last ? 1 : 0);
+  const int whole = box > 0 && begin < end ? (int)((end - begin) / kTokens) : 0;   // tiles that come by TMA
+  // ---- TMA: one thread, the first tiles while the others set up.  Pages are looked up a tile ahead, all at once: one after the
+  // other they took longer than the copies.
+  constexpr int kBoxes = kTokens / 8;
+  const int boxes = box > 0 ? kTokens / box : 0;
+  int page[kBoxes];
+  bool missing = false;
+  const auto look_up = [&](int n) {
+#pragma unroll
+    for (int x = 0; x < kBoxes; ++x) {
+      const int at = (int)begin + n * kTokens + x * box;
+      page[x] = n < whole && x < boxes ? s.pages[page_of(a, at)] : -1;
+    }
+  };
+  const auto load = [&](int n, uint8_t* to, const CUtensorMap* map, uint64_t* full) {
+    if (dead(hd)) return;
+    uint32_t count = 0;
+#pragma unroll
+    for (int x = 0; x < kBoxes; ++x) count += page[x] >= 0 && page[x] < a.npages;
+    missing |= count < (uint32_t)boxes;
+    mbar_arrive_expect_tx(full, count * box * D * 2);
+#pragma unroll
+    for (int x = 0; x < kBoxes; ++x) {
+      if (page[x] < 0 || page[x] >= a.npages) continue;
+      const int at = (int)begin + n * kTokens + x * box, at_row = page[x] * a.page_tokens + (at - page_of(a, at) * a.page_tokens);
+#pragma unroll
+      for (int d = 0; d < D; d += 64) tma_load_3d(to + d * kTokens * 2 + x * box * 128, map, d, kv, at_row, full);
+    }
+  };
+  const auto load_tile = [&](int n) {
+    const int b = n % kStages;
+    uint8_t* kt = stages + b * 2 * Sh::tile;
+    if (n >= kStages) wait(hd, &hd.k_empty[b], n / kStages - 1, a.status);   // K's place is free long before V's
+    load(n, kt, &maps.k, &hd.k_full[b]);
+    if (n >= kStages) wait(hd, &hd.v_empty[b], n / kStages - 1, a.status);
+    load(n, kt + Sh::tile, &maps.v, &hd.v_full[b]);
+    look_up(n + 1);
+  };
+  if (tid == kLoadThread) {
+    for (int b = 0; b < kStages; ++b) {
+      mbar_init(&hd.k_full[b], 1);
+      mbar_init(&hd.v_full[b], 1);
+      mbar_init(&hd.k_empty[b], 1);
+      mbar_init(&hd.v_empty[b], 1);
+      mbar_init(&hd.s_ready[b], 1);
+    }
+    mbar_init(&hd.p_ready, min(kM, (nrows - row0 + 31) / 32 * 32));   // of the warps that have rows
+    mbar_init(&hd.o_done, 1);
+    fence_mbar_init();
+    hd.dead = 0;
+    hd.bad = 0;
+    look_up(0);
+    for (int n = 0; n < kStages && n < whole; ++n) load_tile(n);
+  }
+  if (warp == kIssueThread / 32) tmem_alloc(&hd.tmem, kCols);
+  if (tid < kM) {
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x) *reinterpret_cast<uint4*>(base + sw128(kM, tid, 8 * x)) = q[x];
+    fence_async_smem();
+  }
   __syncthreads();
   const int32_t* parent = a.parent != nullptr ? hd.parent : nullptr;
   bool wrong = false;
   if (tid < a.T) path_of(parent, tid, &wrong);
-  if (__syncthreads_or(wrong) && err == ERS_OK) err = ERS_EINVAL;
-  if (err != ERS_OK) {
-    if (tid == 0) report(a.status, err);
-    if (a.nsplit > 1 && tid < kM && row < nrows)
-      reinterpret_cast<float2*>(a.part)[out_row(row) * a.nsplit + split] = make_float2(0.f, -1.f);
-    return;
-  }
-  const bool last = split == a.nsplit - 1;
-  const long long begin = (long long)split * a.per;
-  const int end = last ? s.pos : (int)min((long long)s.pos, begin + a.per);
-  const int past = begin < end ? (int)((end - begin + kTokens - 1) / kTokens) : 0, tiles = past + (last ? 1 : 0);
-  if (tiles == 0) {                            // nothing of the past is this CTA's
-    if (tid < kM && row < nrows) reinterpret_cast<float2*>(a.part)[out_row(row) * a.nsplit + split] = make_float2(0.f, 0.f);
-    return;
-  }
-  if (warp == kIssueThread / 32) tmem_alloc(&hd.tmem, kCols);
-  if (tid == kLoadThread) {
-    for (int b = 0; b < kStages; ++b) {
-      mbar_init(&hd.full[b], kLoaders);
-      mbar_init(&hd.empty[b], 1);
-      mbar_init(&hd.s_ready[b], 1);
-    }
-    mbar_init(&hd.p_ready, kM);
-    mbar_init(&hd.o_done, 1);
-    fence_mbar_init();
-    hd.dead = 0;
-  }
-  if (tid < kM) {
-    const bf16* q = (const bf16*)a.q + (row < nrows ? out_row(row) * D : 0);
-#pragma unroll
-    for (int x = 0; x < D; x += 8)
-      *reinterpret_cast<uint4*>(base + sw128(kM, tid, x)) = row < nrows ? *reinterpret_cast<const uint4*>(q + x) : make_uint4(0, 0, 0, 0);
-    fence_async_smem();
-  }
   before_sync();
-  __syncthreads();
+  const bool bad_tree = __syncthreads_or(wrong);
   after_sync();
   const uint32_t tb = __shfl_sync(kFull, hd.tmem, 0);
+  if (bad_tree || err != ERS_OK || tiles == 0) {   // an error, or nothing of the past is this CTA's
+    if (tid == 0 && (bad_tree || err != ERS_OK)) report(a.status, err != ERS_OK ? err : ERS_EINVAL);
+    if (a.nsplit > 1 && tid < kM && row < nrows)
+      reinterpret_cast<float2*>(a.part)[out_row(row) * a.nsplit + split] = make_float2(0.f, bad_tree || err != ERS_OK ? -1.f : 0.f);
+    if (tid == kLoadThread)                    // no copy may be left in flight
+      for (int n = 0; n < kStages && n < whole; ++n) {
+        wait(hd, &hd.k_full[n], 0, a.status);
+        wait(hd, &hd.v_full[n], 0, a.status);
+      }
+    __syncthreads();
+    if (warp == kIssueThread / 32) tmem_dealloc(tb, kCols);
+    return;
+  }
 
   if (tid >= kIssueThread) {
     // ---- the issuing warp -------------------------------------------------------------------------------
@@ -155,7 +203,7 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
     const bool leader = elected();
     const auto scores = [&](int n) {
       const int b = n % kStages;
-      if (!wait(hd, &hd.full[b], n / kStages, a.status)) return false;
+      if (!wait(hd, &hd.k_full[b], n / kStages, a.status)) return false;
       after_sync();
       fence_async_smem();
       const uint32_t kt = smem_u32(stages + b * 2 * Sh::tile), qt = smem_u32(base);
@@ -164,96 +212,78 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
         if (leader)
           mma(tb + kColS + (n & 1) * kTokens, sdesc(qt + (k >> 2) * kM * 128 + (k & 3) * 32, 16, 1024),
               sdesc(kt + (k >> 2) * kTokens * 128 + (k & 3) * 32, 16, 1024), id_s, k > 0);
-      if (leader) commit(&hd.s_ready[n & 1]);
+      if (leader) {
+        commit(&hd.s_ready[n & 1]);
+        commit(&hd.k_empty[b]);
+      }
       return true;
     };
     bool ok = scores(0);
 #pragma unroll 1
     for (int n = 0; ok && n < tiles; ++n) {
       bool ahead = n + 1 < tiles;
-      if (ahead && !__all_sync(kFull, mbar_test(&hd.full[(n + 1) % kStages], (n + 1) / kStages & 1))) ahead = false;
+      if (ahead && !__all_sync(kFull, mbar_test(&hd.k_full[(n + 1) % kStages], (n + 1) / kStages & 1))) ahead = false;
       if (ahead && !scores(n + 1)) break;
-      if (!wait(hd, &hd.p_ready, n, a.status)) break;
-      after_sync();
       const int b = n % kStages;
+      if (!wait(hd, &hd.v_full[b], n / kStages, a.status) || !wait(hd, &hd.p_ready, n, a.status)) break;
+      after_sync();
       const uint64_t vd = sdesc(smem_u32(stages + b * 2 * Sh::tile + Sh::tile), kTokens * 128, 1024);
 #pragma unroll
       for (int k = 0; k < kTokens / 16; ++k)
         if (leader) mma_ts(tb + kColO, tb + kColS + (n & 1) * kTokens + 8 * k, vd + k * (16 * 128 / 16), id_o, n > 0 || k > 0);
       if (leader) {
-        commit(&hd.empty[b]);
+        commit(&hd.v_empty[b]);
         commit(&hd.o_done);
       }
       if (!ahead && n + 1 < tiles && !scores(n + 1)) break;
     }
   } else if (tid >= kLoadThread) {
-    // ---- the loading warps: a tile's rows by 8 (D 64) or 16 neighbouring threads --------------------------
-    constexpr int kPer = D / 8, kStep = kLoaders / kPer;
-    constexpr int kEach = kTokens / kStep;     // a thread's rows; at least the 8 boxes that a tile may be of
-    static_assert(kEach >= 8, "pages of all boxes");
-    const int t = tid - kLoadThread, c = t % kPer * 8, r0 = t / kPer;
-    // Pages are looked up a tile ahead, all at once: one after the other they took longer than the copies.
-    const int boxes = box > 0 ? kTokens / box : 0, whole = box > 0 && begin < end ? (int)((end - begin) / kTokens) : 0;
-    int page[kEach];
-    bool missing = false;
-    const auto look_up = [&](int n) {
-#pragma unroll
-      for (int x = 0; x < kEach; ++x) {
-        const int at = (int)begin + n * kTokens + (n < whole ? x * box : r0 + x * kStep);
-        page[x] = n < past && at < end && (n >= whole || x < boxes) ? s.pages[page_of(a, at)] : -1;
-      }
-    };
-    look_up(0);
-    bool pending = false;                      // this thread's copies of the tile before
+    // ---- the loading warps ------------------------------------------------------------------------------
+    const int t = tid - kLoadThread;
+    if (t == 0)                                // (one thread polls: warps that do take issue slots from the rows')
+      for (int n = kStages; n < whole; ++n) load_tile(n);
+    // What is left by all of them, a tile's rows by 8 (D 64) or 16 neighbouring threads.
+    constexpr int kPer = D / 8, kStep = kLoaders / kPer, kEach = kTokens / kStep;
+    const int c = t % kPer * 8, r0 = t / kPer;
+    bool pending = false;                      // copies of the tile before
     const auto arrive = [&](int n) {
       if (!pending) return;
       copies_wait();
       fence_async_smem();
-      mbar_arrive(&hd.full[n % kStages]);
-      pending = false;
+      named_sync(1, kLoaders);
+      if (t == 0) {
+        mbar_arrive(&hd.k_full[n % kStages]);
+        mbar_arrive(&hd.v_full[n % kStages]);
+      }
     };
-    for (int n = 0; n < tiles; ++n) {
+    for (int n = whole; n < tiles; ++n) {
       arrive(n - 1);                           // told before any wait for its stage's turn
       const int b = n % kStages;
-      if (n >= kStages) wait(hd, &hd.empty[b], n / kStages - 1, a.status);
-      uint8_t *kt = stages + b * 2 * Sh::tile, *vt = kt + Sh::tile;
-      if (n < whole) {
-        if (t == 0 && !dead(hd)) {
-          uint32_t count = 0;
-#pragma unroll
-          for (int x = 0; x < kEach; ++x) count += page[x] >= 0 && page[x] < a.npages;
-          missing |= count < (uint32_t)boxes;
-          mbar_arrive_expect_tx(&hd.full[b], count * box * D * 4);
-#pragma unroll
-          for (int x = 0; x < kEach; ++x) {
-            if (page[x] < 0 || page[x] >= a.npages) continue;
-            const int at = (int)begin + n * kTokens + x * box, row = page[x] * a.page_tokens + (at - page_of(a, at) * a.page_tokens);
-#pragma unroll
-            for (int d = 0; d < D; d += 64) {
-              tma_load_3d(kt + d * kTokens * 2 + x * box * 128, &maps.k, d, kv, row, &hd.full[b]);
-              tma_load_3d(vt + d * kTokens * 2 + x * box * 128, &maps.v, d, kv, row, &hd.full[b]);
-            }
-          }
-        } else {
-          mbar_arrive(&hd.full[b]);
-        }
-        look_up(n + 1);
-        continue;
+      if (t == 0 && n >= kStages) {
+        wait(hd, &hd.k_empty[b], n / kStages - 1, a.status);
+        wait(hd, &hd.v_empty[b], n / kStages - 1, a.status);
       }
+      named_sync(1, kLoaders);
+      uint8_t *kt = stages + b * 2 * Sh::tile, *vt = kt + Sh::tile;
       pending = true;
       if (dead(hd)) continue;
       if (n < past) {
+        int at_page[kEach];
+#pragma unroll
+        for (int x = 0; x < kEach; ++x) {
+          const int at = (int)begin + n * kTokens + r0 + x * kStep;
+          at_page[x] = at < end ? s.pages[page_of(a, at)] : -1;
+        }
 #pragma unroll
         for (int x = 0; x < kEach; ++x) {
           const int r = r0 + x * kStep, at = (int)begin + n * kTokens + r;
-          const bool there = page[x] >= 0 && page[x] < a.npages;
+          const bool there = at_page[x] >= 0 && at_page[x] < a.npages;
           missing |= !there && at < end;
-          const size_t row = there ? (size_t)page[x] * a.page_tokens + (at - page_of(a, at) * a.page_tokens) : 0;
-          const size_t from = (row * a.KV + kv) * D + c;
+          const size_t at_row = there ? (size_t)at_page[x] * a.page_tokens + (at - page_of(a, at) * a.page_tokens) : 0;
+          const size_t from = (at_row * a.KV + kv) * D + c;
           copy16(kt + sw128(kTokens, r, c), (const bf16*)a.k_pages + from, there);
           copy16(vt + sw128(kTokens, r, c), (const bf16*)a.v_pages + from, there);
         }
-        look_up(n + 1);
         continue;
       }
       // Drafts: a value that is not finite would reach rows that do not see it as 0 x infinity, so it is left out, and
@@ -275,8 +305,8 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
     }
     arrive(tiles - 1);
     if (missing) report(a.status, ERS_ESLOT);
-  } else {
-    // ---- the rows -------------------------------------------------------------------------------------------
+  } else if (row0 + (tid & ~31) < nrows) {
+    // ---- the rows (a warp without any does nothing: what its lanes of P and O hold is read by no one) -------------------------------------------------------------------------------------------
     const float c = a.scale * 1.44269504088896340736f;
     bool unused = false;
     const uint64_t path = row < nrows ? path_of(parent, row / rep, &unused) : 0;
@@ -298,34 +328,30 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
         const int count = end - ((int)begin + n * kTokens);
         seen = path == 0 ? 0 : count >= kTokens ? ~0ull : (1ull << count) - 1;
       }
-      float top = -INFINITY;
-      if (__all_sync(kFull, seen == ~0ull)) {
+      const bool whole = __all_sync(kFull, seen == ~0ull);
+      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 0; x < 64; ++x) {
-          const float y = __uint_as_float(u[x / 32][x % 32]) * c;
-          u[x / 32][x % 32] = __float_as_uint(y);
-          top = fmaxf(top, y);
-        }
-      } else {
+      for (int x = 0; x < 64; ++x) u[x / 32][x % 32] = __float_as_uint(__uint_as_float(u[x / 32][x % 32]) * c);
+      if (!whole) {
 #pragma unroll
-        for (int x = 0; x < 64; ++x) {
-          const float y = seen >> x & 1u ? __uint_as_float(u[x / 32][x % 32]) * c : -INFINITY;
-          u[x / 32][x % 32] = __float_as_uint(y);
-          top = fmaxf(top, y);
-        }
+        for (int x = 0; x < 64; ++x) u[x / 32][x % 32] = (uint32_t)(seen >> (x & 32)) >> (x & 31) & 1u ? u[x / 32][x % 32] : 0xff800000u;
       }
+#pragma unroll
+      for (int x = 0; x < 64; ++x) tops[x % 4] = fmaxf(tops[x % 4], __uint_as_float(u[x / 32][x % 32]));
+      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
       // (a row that has seen nothing rises from -inf; one that still sees nothing does not)
       const bool rise = top > m + kRise || (m == -INFINITY && top > m);
       const float next = rise ? top : m, factor = rise ? exp2_of(m - next) : 1.f;   // from -inf: 0
       const float down = next == -INFINITY ? 0.f : next;
       uint32_t p[32];
-      float sum = 0.f;
+      float sums[4] = {};
 #pragma unroll
       for (int x = 0; x < 32; ++x) {
         p[x] = pack_bf16x2(exp2_of(__uint_as_float(u[x / 16][x % 16 * 2]) - down), exp2_of(__uint_as_float(u[x / 16][x % 16 * 2 + 1]) - down));
-        sum += __uint_as_float(p[x] << 16) + __uint_as_float(p[x] & 0xffff0000u);
+        sums[x % 2 * 2] += __uint_as_float(p[x] << 16);
+        sums[x % 2 * 2 + 1] += __uint_as_float(p[x] & 0xffff0000u);
       }
-      l = fmaf(l, factor, sum);
+      l = fmaf(l, factor, (sums[0] + sums[1]) + (sums[2] + sums[3]));
       m = next;
       if (n > 0) {
         wait(hd, &hd.o_done, n - 1, a.status);
@@ -363,7 +389,7 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
       arrived(o);
       if (row >= nrows) continue;
       if (a.nsplit > 1) {
-        float* to = a.part + 2 * all + part * D + x;
+        float* to = a.part + part_outputs(all) + part * D + x;
 #pragma unroll
         for (int y = 0; y < 32; y += 4) *reinterpret_cast<uint4*>(to + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
       } else {

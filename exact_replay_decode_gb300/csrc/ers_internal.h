@@ -283,7 +283,7 @@ struct AttnArgs {
   uint32_t page_magic;      // at / page_tokens is (umulhi(page_magic, at) + at) >> page_shift, at < 2^31
   int page_shift;
   const int32_t* slot;
-  float* part;              // nsplit > 1: [nseq, T, H, nsplit] (max, sum), then [nseq, T, H, nsplit, D] outputs
+  float* part;              // nsplit > 1: [nseq, T, H, nsplit] (max, sum), then (part_outputs) [nseq, T, H, nsplit, D]
   const int32_t* cu;        // append: [nseq + 1]
   long long ntokens;
   const int32_t* path;      // commit: [nseq, T] or null: the first drafts
