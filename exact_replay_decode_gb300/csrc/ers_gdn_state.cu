@@ -52,7 +52,7 @@ __device__ __forceinline__ void step_row(float4 (&s)[N], const float4 (&k)[N], D
 // ---- one token per sequence ---------------------------------------------------------------------------
 // Each state is read and written once, 128 KB a head of 128 x 128: bandwidth.  A warp takes kSide * sets rows, all of their
 // loads under way before the first is used.  The output is taken from the old state, a S q + u (k . q), so that its
-// exchanges run beside those of S k.
+// exchanges run beside those of S k.  256 sequences x 64 heads of 128 x 128: 319 us, the measured bandwidth.
 constexpr int kDecodeRows = kThreads / 32 * kSide;   // rows of a CTA for each set
 
 template <typename T, int DK, int sets>
@@ -95,19 +95,52 @@ __global__ void __launch_bounds__(kThreads) k_gdn_decode(const __grid_constant__
   }
 }
 
-// ---- prompts, token by token ----------------------------------------------------------------------------
-// A CTA keeps kStepRows * rows state rows in registers over the whole sequence; tokens come through shared memory, kTok at a
-// time, the next ones under way.  The chain through a token is the product with k, its three exchanges and the update.
-constexpr int kStepThreads = 128, kTok = 32;
+// ---- prompts, eight tokens at a time ----------------------------------------------------------------------
+// fp32 prompts, and short bf16 ones.  A CTA keeps its state rows in registers over the whole sequence; tokens come through shared
+// memory, kTok at a time, the next ones under way.  Of a batch of eight tokens every product with the state is one with the
+// state before it, so that their exchanges across lanes run side by side, and the residuals follow from products of keys:
+//   y_t = S k_t, z_t = S q_t;   u_t = beta_t (v_t - e^(G_t) y_t) - sum_(s<t) beta_t e^(G_t - G_s) (k_s.k_t) u_s
+//   o_t = scale (e^(G_t) z_t + sum_(s<=t) e^(G_t - G_s) (k_s.q_t) u_s),   S <- e^(G_7) S + sum_t e^(G_7 - G_t) u_t k_t^T
+// (token by token, with an exchange in the chain of each, 1025 tokens x 16 heads took 400 us in place of 273).  G_t - G_s is summed from the
+// gates between: no cancellation.  What a token holds that is not finite reaches nothing before it.
+constexpr int kStepThreads = 128, kTok = 32, kBatch = 8;
 constexpr int kStepRows = kStepThreads / 32 * kSide;
 
 template <typename T, int DK, int R>
 struct StepTiles {
-  T q[2][kTok][DK];
-  T k[2][kTok][DK];
+  static constexpr int LD = DK + 16 / sizeof(T);            // rows of tokens start in other banks
+  T q[2][kTok][LD];
+  T k[2][kTok][LD];
   T v[2][kTok][R];
   float g[2][kTok], beta[2][kTok];
+  alignas(16) float kk[kTok][kBatch];                       // beta_t e^(G_t - G_s) k_s.k_t, s < t
+  alignas(16) float qk[kTok][kBatch];                       // e^(G_t - G_s) k_s.q_t, s <= t
+  float since[kTok], left[kTok];                            // e^(G_t), e^(G_7 - G_t)
+  Decay whole[kTok / kBatch];                               // e^(G_7)
 };
+
+// Adds up eight values across the eight lanes of a row: lane j gets the total of value j.
+__device__ __forceinline__ float totals(float (&v)[kBatch], int j) {
+#pragma unroll
+  for (int n = 4; n >= 1; n /= 2) {
+    const bool upper = (j & n) != 0;
+#pragma unroll
+    for (int r = 0; r < n; ++r) {
+      const float give = upper ? v[r] : v[r + n], keep = upper ? v[r + n] : v[r];
+      v[r] = keep + __shfl_xor_sync(kFull, give, n);
+    }
+  }
+  return v[0];
+}
+__device__ __forceinline__ void axpy(float4& a, float f, float4 x) {
+  a.x = fmaf(f, x.x, a.x);
+  a.y = fmaf(f, x.y, a.y);
+  a.z = fmaf(f, x.z, a.z);
+  a.w = fmaf(f, x.w, a.w);
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
 
 template <typename T, int DK, int rows>
 __global__ void __launch_bounds__(kStepThreads) k_gdn_steps(const __grid_constant__ DeltaArgs a) {
@@ -131,21 +164,28 @@ __global__ void __launch_bounds__(kStepThreads) k_gdn_steps(const __grid_constan
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
   const auto fetch = [&](int t0, int b) {
     constexpr int e = 16 / sizeof(T);                       // elements of a copy
-    const int n = min(kTok, s.len - t0);
-    for (int x = threadIdx.x; x < n * (DK / e); x += kStepThreads) {
+    const int n = min(kTok, s.len - t0), all = (n + kBatch - 1) / kBatch * kBatch;   // zeros in the rest of the last batch
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int x = threadIdx.x; x < all * (DK / e); x += kStepThreads) {
       const int t = x / (DK / e), c = x % (DK / e) * e;
-      const size_t at = ((size_t)(s.t0 + t0 + t) * a.G + g) * DK + c;
-      tc::cp_async16(&tiles.q[b][t][c], (const T*)a.q + at);
-      tc::cp_async16(&tiles.k[b][t][c], (const T*)a.k + at);
+      if (t < n) {
+        const size_t at = ((size_t)(s.t0 + t0 + t) * a.G + g) * DK + c;
+        tc::cp_async16(&tiles.q[b][t][c], (const T*)a.q + at);
+        tc::cp_async16(&tiles.k[b][t][c], (const T*)a.k + at);
+      } else {
+        *reinterpret_cast<uint4*>(&tiles.q[b][t][c]) = zero;
+        *reinterpret_cast<uint4*>(&tiles.k[b][t][c]) = zero;
+      }
     }
-    for (int x = threadIdx.x; x < n * (R / e); x += kStepThreads) {
+    for (int x = threadIdx.x; x < all * (R / e); x += kStepThreads) {
       const int t = x / (R / e), c = x % (R / e) * e;
-      tc::cp_async16(&tiles.v[b][t][c], (const T*)a.v + ((size_t)(s.t0 + t0 + t) * a.H + h) * a.dv + d0 + c);
+      if (t < n) tc::cp_async16(&tiles.v[b][t][c], (const T*)a.v + ((size_t)(s.t0 + t0 + t) * a.H + h) * a.dv + d0 + c);
+      else *reinterpret_cast<uint4*>(&tiles.v[b][t][c]) = zero;
     }
-    if (threadIdx.x < n) {
+    if (threadIdx.x < all) {
       const size_t at = (size_t)(s.t0 + t0 + threadIdx.x) * a.H + h;
-      tiles.g[b][threadIdx.x] = a.g[at];
-      tiles.beta[b][threadIdx.x] = a.beta[at];
+      tiles.g[b][threadIdx.x] = threadIdx.x < n ? a.g[at] : 0.f;
+      tiles.beta[b][threadIdx.x] = threadIdx.x < n ? a.beta[at] : 0.f;
     }
     static_assert(R % e == 0, "whole copies");
   };
@@ -155,23 +195,106 @@ __global__ void __launch_bounds__(kStepThreads) k_gdn_steps(const __grid_constan
     __syncthreads();                                        // this tile is there, the other one no longer read
     if (t0 + kTok < s.len) fetch(t0 + kTok, b ^ 1);
     const int n = min(kTok, s.len - t0);
-#pragma unroll 1
-    for (int t = 0; t < n; ++t) {
-      float4 k[N], q[N];
-#pragma unroll
-      for (int x = 0; x < N; ++x) {
-        k[x] = quad(&tiles.k[b][t][4 * (j + kRowLanes * x)]);
-        q[x] = quad(&tiles.q[b][t][4 * (j + kRowLanes * x)]);
+    // products of the tile's keys and queries: two lanes for each pair of a batch
+    for (int t8 = 0; t8 < n; t8 += kBatch) {
+      const int pair = threadIdx.x / 2, t = pair / kBatch, u = pair % kBatch, half = threadIdx.x % 2;
+      const float* gate = tiles.g[b] + t8;
+      float kk = 0.f, qk = 0.f;
+      if (u <= t) {
+#pragma unroll 4
+        for (int x = 4 * half; x < DK; x += 8) {
+          const float4 ku = quad(&tiles.k[b][t8 + u][x]);
+          kk = dot4(ku, quad(&tiles.k[b][t8 + t][x]), kk);
+          qk = dot4(ku, quad(&tiles.q[b][t8 + t][x]), qk);
+        }
       }
-      const Decay decay = decay_of(tiles.g[b][t]);
-      const float beta = tiles.beta[b][t], whole = decay.hi + decay.lo;
-      T* o = (T*)a.o + ((size_t)(s.t0 + t0 + t) * a.H + h) * a.dv + d0;
+      kk += __shfl_xor_sync(kFull, kk, 1);
+      qk += __shfl_xor_sync(kFull, qk, 1);
+      if (half == 0) {
+        float between = 0.f;
+        for (int x = u + 1; x <= t; ++x) between += gate[x];
+        const float f = u <= t ? expf(between) : 0.f;
+        tiles.kk[t8 + t][u] = u < t ? tiles.beta[b][t8 + t] * f * kk : 0.f;
+        tiles.qk[t8 + t][u] = u <= t ? f * qk : 0.f;
+      } else if (u == 0) {
+        float before = 0.f, after = 0.f;
+        for (int x = 0; x <= t; ++x) before += gate[x];
+        for (int x = t + 1; x < kBatch; ++x) after += gate[x];
+        tiles.since[t8 + t] = expf(before);
+        tiles.left[t8 + t] = expf(after);
+        if (t == kBatch - 1) tiles.whole[t8 / kBatch] = decay_of(before);
+      }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int t8 = 0; t8 < n; t8 += kBatch) {
+      float y[rows][kBatch] = {}, z[rows][kBatch] = {};
+#pragma unroll
+      for (int x = 0; x < N; ++x)
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) {
+          const float4 k = quad(&tiles.k[b][t8 + t][4 * (j + kRowLanes * x)]), q = quad(&tiles.q[b][t8 + t][4 * (j + kRowLanes * x)]);
+#pragma unroll
+          for (int r = 0; r < rows; ++r) {
+            y[r][t] = dot4(st[r][x], k, y[r][t]);
+            z[r][t] = dot4(st[r][x], q, z[r][t]);
+          }
+        }
+      float mine[rows];                                     // z of token j
 #pragma unroll
       for (int r = 0; r < rows; ++r) {
-        const float sk = row_sum(dot(st[r], k));
-        step_row(st[r], k, decay, beta * fmaf(-whole, sk, to_f(tiles.v[b][t][own + kSide * r])));
-        const float sq = row_sum(dot(st[r], q));
-        if (j == 0) o[own + kSide * r] = from_f<T>(a.scale * sq);
+        const float all = totals(y[r], j);
+        mine[r] = totals(z[r], j);
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) y[r][t] = __shfl_sync(kFull, all, (lane & ~(kRowLanes - 1)) | t);
+      }
+      float (&u)[rows][kBatch] = y;                         // the residuals, in place
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t) {
+        const float beta = tiles.beta[b][t8 + t], since = tiles.since[t8 + t];
+        const float4 c0 = quad(&tiles.kk[t8 + t][0]), c1 = quad(&tiles.kk[t8 + t][4]);
+        const float c[kBatch] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+        for (int r = 0; r < rows; ++r) {
+          float x = beta * fmaf(-since, y[r][t], to_f(tiles.v[b][t8 + t][own + kSide * r]));
+#pragma unroll
+          for (int e = 0; e < t; ++e) x = fmaf(-c[e], u[r][e], x);
+          u[r][t] = x;
+        }
+      }
+      {
+        const float4 c0 = quad(&tiles.qk[t8 + j][0]), c1 = quad(&tiles.qk[t8 + j][4]);
+        const float c[kBatch] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w}, since = tiles.since[t8 + j];
+        T* o = (T*)a.o + ((size_t)(s.t0 + t0 + t8 + j) * a.H + h) * a.dv + d0 + own;
+#pragma unroll
+        for (int r = 0; r < rows; ++r) {
+          float x = since * mine[r];
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e)
+            if (e <= j) x = fmaf(c[e], u[r][e], x);         // (what comes later may be anything)
+          if (t8 + j < n) o[kSide * r] = from_f<T>(a.scale * x);
+        }
+      }
+      const Decay whole = tiles.whole[t8 / kBatch];
+#pragma unroll
+      for (int r = 0; r < rows; ++r)
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) u[r][t] *= tiles.left[t8 + t];
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+#pragma unroll
+        for (int r = 0; r < rows; ++r) {
+          st[r][x].x = fmaf(whole.hi, st[r][x].x, whole.lo * st[r][x].x);
+          st[r][x].y = fmaf(whole.hi, st[r][x].y, whole.lo * st[r][x].y);
+          st[r][x].z = fmaf(whole.hi, st[r][x].z, whole.lo * st[r][x].z);
+          st[r][x].w = fmaf(whole.hi, st[r][x].w, whole.lo * st[r][x].w);
+        }
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) {
+          const float4 k = quad(&tiles.k[b][t8 + t][4 * (j + kRowLanes * x)]);
+#pragma unroll
+          for (int r = 0; r < rows; ++r) axpy(st[r][x], u[r][t], k);
+        }
       }
     }
   }
@@ -205,13 +328,19 @@ cudaError_t launch_steps(const DeltaArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Rows of a lane: one while a CTA of such has an SM for itself, two while two of those fit a SM, four beyond: k and q are read from
+// shared memory by every warp, which bounds many CTAs.  By one, two and four, us:
+//   fp32, 1024 x 16 heads 281, 305, 602; x 32 391, 305, 623; 4 x 1024 x 64 2687, 1725, 1409
+//   bf16, 16 x 16 6.3, 7.8, 13.0; 33 x 64 29.5, 19.1, 31.3; 4 x 33 x 32 56.3, 36.3, 32.2
 template <typename T, int DK>
 cudaError_t steps(const DeltaArgs& a, cudaStream_t s) {
-  return launch_steps<T, DK, 2>(a, s);
+  const long long ctas = (long long)a.nseq * a.H * (a.dv / kStepRows);
+  return ctas <= 152 ? launch_steps<T, DK, 1>(a, s) : ctas <= 608 ? launch_steps<T, DK, 2>(a, s) : launch_steps<T, DK, 4>(a, s);
 }
 
 template <typename T, int DK>
 cudaError_t decode(const DeltaArgs& a, cudaStream_t s) {
+  // a CTA per head where those fill the SMs, else one per 32 rows of its state
   const dim3 few(a.nseq, a.H, a.dv / kDecodeRows);
   if ((long long)a.nseq * a.H < 608) {
     k_gdn_decode<T, DK, 1><<<few, kThreads, 0, s>>>(a);
@@ -225,9 +354,11 @@ cudaError_t decode(const DeltaArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// bf16 prompts of more tokens than these go by chunks.
-constexpr int kFewTokens = 24;
-static bool by_chunks(const DeltaArgs& a) { return a.io == ERS_DTYPE_BF16 && a.max_len > kFewTokens; }
+// bf16 prompts of more tokens than these go by chunks, which take 15 us whatever they hold (32 heads: 16 tokens 8.2 us by the
+// recurrence, 33 15.1 and 14.9; 128 heads: 16 tokens 15.1 and 22.3, 33 32 and 22.7).
+static bool by_chunks(const DeltaArgs& a) {
+  return a.io == ERS_DTYPE_BF16 && a.max_len > ((long long)a.nseq * a.H <= 64 ? 32 : 24);
+}
 
 cudaError_t gdn_fwd(const DeltaArgs& a, cudaStream_t s) {
   if (by_chunks(a)) return gdn_tc(a, s);
