@@ -300,9 +300,11 @@ __global__ void __launch_bounds__(kThreads) k_attn_commit(const __grid_constant_
 }  // namespace
 
 // Parts of a past: what takes the least time by a model in tiles of 64 tokens, each CTA some 4 beside its own, of as many CTAs
-// as run at once (two a SM on the tensor cores, four of the fp32 kernel).  By 1, 2, 4, 8, 16 and 32 parts, us (without the model's
-// finer ones): 1 x 32768 tokens 859, 435, 230, 123, 72, 53; 8 x 8192 228, 123, 78, 87, 101, 126; 16 x 4096, 64 drafts
-// 142, 176, 207, 263; 64 x 4096 261, 289, 335, 420 (before later steps).
+// as run at once (two a SM on the tensor cores, four of the fp32 kernel), and a quarter for each part that a row is joined
+// of (bf16; a tile of the fp32 kernel takes much longer than that).  By 1, 2, 4, 8, 16, 32 and 64 parts, us:
+//   1 x 32768 tokens 593, 310, 163, 89, 54, 41, 54 (38: 40)     8 x 8192, 4 drafts 156, 89, 57, 67, 79, 98, 138
+//   1 x 1000 26, 20, 16, 15, 16 (6: 12.5)                       64 x 4096, 16 drafts 186, 220, 265, 339
+//   16 x 4096, 64 drafts 105, 148, 183, 237                     fp32, 4 x up to 1000, 7 drafts 129, 69, 40, 26, 21
 void attn_plan(AttnArgs* a, int max_len) {
   const bool tiles_of = a->io == ERS_DTYPE_BF16;
   const int each = tiles_of ? 128 : kRows, slots = tiles_of ? 304 : 608, rows = a->T * (a->H / a->KV);
@@ -312,7 +314,7 @@ void attn_plan(AttnArgs* a, int max_len) {
   long long least = 0;
   for (int n = 1; n <= 64 && n <= blocks; ++n) {
     const int p = (blocks + n - 1) / n;
-    const long long parts = (blocks + p - 1) / p, cost = (units * parts + slots - 1) / slots * (p + 4);
+    const long long parts = (blocks + p - 1) / p, cost = (units * parts + slots - 1) / slots * (p + 4) * 4 + (tiles_of && parts > 1 ? parts : 0);
     if (n == 1 || cost < least) {
       least = cost;
       per = p;

@@ -12,6 +12,12 @@
 // tiles of pages whose tokens are a multiple of 8 come by TMA, `box` tokens at a time; others, and the last one (zeros behind
 // the last token: a page may hold anything there), by 16-byte copies of both warps.  Two CTAs per SM (two stages of 32 KB each at D 128, 256 columns of tensor
 // memory) run beside each other: one loads while the other computes.
+//
+// What bounds it: a tile moves 32 KB (D 128), 0.74 us of an SM's share of the memory, and its exponentials take 512 cycles of each
+// scheduler.  64 trees of 16 drafts over 2269 to 4096 tokens x 8 heads: 184 us, 126 of them the bytes' (the 512 CTAs come in
+// waves of 304); one token over 32768 40 us in 37 parts (20 the bytes'; set-up, a part's first loads and the join are the rest);
+// 256 single tokens over 1024 212 us (160).  All loading threads polling in place of one cost 388 us in place of 184: they take
+// issue slots from the rows'.
 #include <string.h>
 
 #include <mutex>

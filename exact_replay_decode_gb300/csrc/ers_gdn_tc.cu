@@ -11,7 +11,14 @@
 //
 // Precision: q, k and v are exact operands.  T' is taken as three bf16 terms (24 bits); W, S, M, U and the decayed U as
 // two (16 bits and more: each is off by at most 2^-17, in the mean 2^-18.7; a third term of all of them would double the products of the
-// serial loop).  The state itself is fp32 in registers, one rounded multiply-add a chunk.
+// serial loop).  The state itself is fp32 in registers, one rounded multiply-add a chunk: final states are 3e-6 of their size
+// off, over 97 tokens as over 32768.
+//
+// What bounds it (2048 tokens x 32 heads of 128 x 128: 50 and 54 us).  k_gdn_inside: the dependent phases of a CTA, 21000 cycles
+// with two a SM (loads 7400, of two products of 128 x 128 x 64 and the scores' 4200, T 4500, the rest made and stored); barriers
+// are most of its stalls.  k_gdn_through: the chain of a chunk, 2900 cycles of 32 state rows (4700 of 64): the state into terms 300,
+// W S^T 1300, U into terms 550, K^T U' and the state's step 760.  Where all parts of 32 rows have an SM they are taken
+// (2048 x 32 heads 81 to 53 us); more CTAs than SMs would do the same operands' work twice.
 #include <mutex>
 #include <type_traits>
 
@@ -181,20 +188,21 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant__ DeltaArgs a) {
   extern __shared__ __align__(1024) uint8_t gdn_smem[];
   InsideSmem<DK, DV>& sm = *reinterpret_cast<InsideSmem<DK, DV>*>(gdn_smem);
-  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0), lane = tid % 32, h = blockIdx.y, rep = a.H / a.G, g = h / rep;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0), lane = tid % 32, rep = a.H / a.G;
+  const int number = blockIdx.x / a.H, h = blockIdx.x % a.H, g = h / rep;   // a chunk's heads side by side: their inputs share sectors
   if (!ascending(a) || (smem_u32(gdn_smem) & 1023u) != 0) return;   // (the next launch reports it)
   int i = 0;
   for (int hi = a.nseq - 1; i < hi;) {         // the last sequence whose chunks start at or before this one
     const int mid = (i + hi + 1) / 2;
-    if ((long long)(a.cu[mid] / kC) + mid <= blockIdx.x) i = mid;
+    if ((long long)(a.cu[mid] / kC) + mid <= number) i = mid;
     else hi = mid - 1;
   }
   const int s0 = a.cu[i], len = a.cu[i + 1] - s0;
-  const long long c0 = ((long long)blockIdx.x - (s0 / kC + i)) * kC;
+  const long long c0 = ((long long)number - (s0 / kC + i)) * kC;
   if (c0 >= len) return;
   const int t0 = s0 + (int)c0, n = min(kC, len - (int)c0);
   const Layout lay(a.H, a.G, DK, DV);
-  uint8_t* chunk = static_cast<uint8_t*>(a.ws) + blockIdx.x * lay.chunk;
+  uint8_t* chunk = static_cast<uint8_t*>(a.ws) + number * lay.chunk;
   uint8_t *mine = chunk + (size_t)h * lay.head, *shared = chunk + (size_t)a.H * lay.head + (size_t)g * lay.group;
 
   // Tiles, zeros behind the last token and in place of what is not finite; all of a thread's loads under way at once.
@@ -755,9 +763,10 @@ cudaError_t launch(const DeltaArgs& a, cudaStream_t s) {
   static bool done[64] = {};
   cudaError_t e = allow(k_gdn_inside<DK, DV>, sizeof(InsideSmem<DK, DV>), done, mu);
   if (e != cudaSuccess) return e;
-  k_gdn_inside<DK, DV><<<dim3((unsigned)chunk_numbers(a.ntokens, a.nseq), a.H), kInside, sizeof(InsideSmem<DK, DV>), s>>>(a);
+  k_gdn_inside<DK, DV><<<(unsigned)(chunk_numbers(a.ntokens, a.nseq) * a.H), kInside, sizeof(InsideSmem<DK, DV>), s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // 32 rows a CTA while every one of those has an SM for itself (2048 x 32 heads: 53 us, by 64 rows 81)
   return (long long)a.nseq * a.H * (DV / 32) <= 152 ? launch_through<DK, 32>(a, s) : launch_through<DK, 64>(a, s);
 }
 

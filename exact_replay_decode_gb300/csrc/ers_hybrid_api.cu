@@ -72,8 +72,10 @@ void set_cache(ers::DeltaArgs* a, const ers_linattn_cache* c, const int32_t* slo
   a->read_page = read_page;
 }
 
-ers_status check_lengths(int64_t ntokens, int32_t max_seqlen) {
-  return ntokens < 0 || ntokens > 0x7fffffff || max_seqlen < 0 ? ERS_EINVAL : ERS_OK;
+// (a launch has a CTA for every head of every 64 tokens)
+ers_status check_lengths(const ers_linattn_dims* d, int32_t nseq, int64_t ntokens, int32_t max_seqlen) {
+  if (ntokens < 0 || ntokens > 0x7fffffff || max_seqlen < 0) return ERS_EINVAL;
+  return (ntokens / 64 + nseq) * d->nheads > 0x7fffffff ? ERS_EINVAL : ERS_OK;
 }
 
 ers_status set_workspace(ers::DeltaArgs* a, void* workspace, size_t bytes) {
@@ -140,7 +142,7 @@ bool drafts_ok(const ers_attn_dims* d, int32_t nseq, int32_t T) {
 extern "C" {
 
 size_t ers_gdn_fwd_workspace_size(const ers_linattn_dims* dims, int32_t nseq, int64_t ntokens, int32_t max_seqlen) {
-  if (check_delta(dims, nseq) != ERS_OK || check_lengths(ntokens, max_seqlen) != ERS_OK || nseq == 0) return 0;
+  if (check_delta(dims, nseq) != ERS_OK || check_lengths(dims, nseq, ntokens, max_seqlen) != ERS_OK || nseq == 0) return 0;
   return ers::gdn_fwd_workspace(delta_args(dims, nseq, ntokens, max_seqlen));
 }
 
@@ -149,7 +151,7 @@ ers_status ers_gdn_fwd(const ers_linattn_dims* dims, int32_t nseq, int64_t ntoke
                        const float* beta, const float* init_state, void* o, float* final_state, void* workspace,
                        size_t workspace_bytes, ers_stream_t stream, int32_t* dev_status) {
   ERS_TRY(check_delta(dims, nseq));
-  ERS_TRY(check_lengths(ntokens, max_seqlen));
+  ERS_TRY(check_lengths(dims, nseq, ntokens, max_seqlen));
   if (nseq == 0) return ERS_OK;
   ers::DeltaArgs a = delta_args(dims, nseq, ntokens, max_seqlen);
   set_tokens(&a, q, k, v, g, beta, o, dev_status);
@@ -169,7 +171,7 @@ ers_status ers_gdn_prefill(const ers_linattn_dims* dims, const ers_linattn_cache
                            const void* q, const void* k, const void* v, const float* g, const float* beta, void* o,
                            void* workspace, size_t workspace_bytes, ers_stream_t stream, int32_t* dev_status) {
   ERS_TRY(check_delta(dims, nseq));
-  ERS_TRY(check_lengths(ntokens, max_seqlen));
+  ERS_TRY(check_lengths(dims, nseq, ntokens, max_seqlen));
   ERS_TRY(check_state_cache(cache, nseq, slot, read_page));
   if (nseq == 0) return ERS_OK;
   ers::DeltaArgs a = delta_args(dims, nseq, ntokens, max_seqlen);

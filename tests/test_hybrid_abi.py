@@ -38,6 +38,7 @@ def test_gdn_refusals(lib):
         assert _fwd(lib, _dims(**bad)) == code, bad
     assert _fwd(lib, nseq=-1) == 1 and _fwd(lib, ntokens=-1) == 1 and _fwd(lib, max_len=-1) == 1
     assert _fwd(lib, ntokens=1 << 31) == 1 and _fwd(lib, nseq=1 << 28) == 1
+    assert _fwd(lib, _dims(nheads=128), ntokens=0x7fffffff) == 1
     for kw in (dict(q=None), dict(cu=None), dict(final=None), dict(g=None)):
         assert _fwd(lib, nseq=1, **kw) == 1, kw
     for kw in (dict(q=OFF), dict(cu=OFF), dict(final=OFF), dict(init=OFF), dict(g=OFF), dict(status=OFF), dict(ws=OFF)):
