@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) k_gdn_decode(const __grid_constant__
 // state before it, so that their exchanges across lanes run side by side, and the residuals follow from products of keys:
 //   y_t = S k_t, z_t = S q_t;   u_t = beta_t (v_t - e^(G_t) y_t) - sum_(s<t) beta_t e^(G_t - G_s) (k_s.k_t) u_s
 //   o_t = scale (e^(G_t) z_t + sum_(s<=t) e^(G_t - G_s) (k_s.q_t) u_s),   S <- e^(G_7) S + sum_t e^(G_7 - G_t) u_t k_t^T
-// (token by token, with an exchange in the chain of each, 1025 tokens x 16 heads took 400 us in place of 273).  G_t - G_s is summed from the
+// (token by token, with an exchange in the chain of each, 1025 tokens x 16 heads took 400 us in place of 242).  G_t - G_s is summed from the
 // gates between: no cancellation.  What a token holds that is not finite reaches nothing before it.
 constexpr int kStepThreads = 128, kTok = 32, kBatch = 8;
 constexpr int kStepRows = kStepThreads / 32 * kSide;
@@ -112,7 +112,8 @@ struct StepTiles {
   T q[2][kTok][LD];
   T k[2][kTok][LD];
   T v[2][kTok][R];
-  float g[2][kTok], beta[2][kTok];
+  alignas(16) float g[2][kTok];
+  float beta[2][kTok];
   alignas(16) float kk[kTok][kBatch];                       // beta_t e^(G_t - G_s) k_s.k_t, s < t
   alignas(16) float qk[kTok][kBatch];                       // e^(G_t - G_s) k_s.q_t, s <= t
   float since[kTok], left[kTok];                            // e^(G_t), e^(G_7 - G_t)
@@ -195,34 +196,43 @@ __global__ void __launch_bounds__(kStepThreads) k_gdn_steps(const __grid_constan
     __syncthreads();                                        // this tile is there, the other one no longer read
     if (t0 + kTok < s.len) fetch(t0 + kTok, b ^ 1);
     const int n = min(kTok, s.len - t0);
-    // products of the tile's keys and queries: two lanes for each pair of a batch
-    for (int t8 = 0; t8 < n; t8 += kBatch) {
-      const int pair = threadIdx.x / 2, t = pair / kBatch, u = pair % kBatch, half = threadIdx.x % 2;
-      const float* gate = tiles.g[b] + t8;
-      float kk = 0.f, qk = 0.f;
-      if (u <= t) {
-#pragma unroll 4
-        for (int x = 4 * half; x < DK; x += 8) {
-          const float4 ku = quad(&tiles.k[b][t8 + u][x]);
-          kk = dot4(ku, quad(&tiles.k[b][t8 + t][x]), kk);
-          qk = dot4(ku, quad(&tiles.q[b][t8 + t][x]), qk);
+    // products of the tile's keys and queries: two lanes for each pair of a batch, the batches' side by side
+    const int pair = threadIdx.x / 2, t = pair / kBatch, u = pair % kBatch, half = threadIdx.x % 2;
+    float kk[kTok / kBatch] = {}, qk[kTok / kBatch] = {};
+    if (u <= t) {
+#pragma unroll 2
+      for (int x = 4 * half; x < DK; x += 8)
+#pragma unroll
+        for (int m = 0; m < kTok / kBatch; ++m) {
+          if (m * kBatch >= n) break;
+          const float4 ku = quad(&tiles.k[b][m * kBatch + u][x]);
+          kk[m] = dot4(ku, quad(&tiles.k[b][m * kBatch + t][x]), kk[m]);
+          qk[m] = dot4(ku, quad(&tiles.q[b][m * kBatch + t][x]), qk[m]);
         }
-      }
-      kk += __shfl_xor_sync(kFull, kk, 1);
-      qk += __shfl_xor_sync(kFull, qk, 1);
+    }
+#pragma unroll
+    for (int m = 0; m < kTok / kBatch; ++m) {
+      if (m * kBatch >= n) break;
+      kk[m] += __shfl_xor_sync(kFull, kk[m], 1);
+      qk[m] += __shfl_xor_sync(kFull, qk[m], 1);
+      const float4 g0 = quad(&tiles.g[b][m * kBatch]), g1 = quad(&tiles.g[b][m * kBatch + 4]);
+      const float gate[kBatch] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+      const auto sum = [&](int from, int to) {              // of gates, no others in between
+        float v = 0.f;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x)
+          if (x >= from && x <= to) v += gate[x];
+        return v;
+      };
       if (half == 0) {
-        float between = 0.f;
-        for (int x = u + 1; x <= t; ++x) between += gate[x];
-        const float f = u <= t ? expf(between) : 0.f;
-        tiles.kk[t8 + t][u] = u < t ? tiles.beta[b][t8 + t] * f * kk : 0.f;
-        tiles.qk[t8 + t][u] = u <= t ? f * qk : 0.f;
+        const float f = u <= t ? expf(sum(u + 1, t)) : 0.f;
+        tiles.kk[m * kBatch + t][u] = u < t ? tiles.beta[b][m * kBatch + t] * f * kk[m] : 0.f;
+        tiles.qk[m * kBatch + t][u] = u <= t ? f * qk[m] : 0.f;
       } else if (u == 0) {
-        float before = 0.f, after = 0.f;
-        for (int x = 0; x <= t; ++x) before += gate[x];
-        for (int x = t + 1; x < kBatch; ++x) after += gate[x];
-        tiles.since[t8 + t] = expf(before);
-        tiles.left[t8 + t] = expf(after);
-        if (t == kBatch - 1) tiles.whole[t8 / kBatch] = decay_of(before);
+        const float before = sum(0, t);
+        tiles.since[m * kBatch + t] = expf(before);
+        tiles.left[m * kBatch + t] = expf(sum(t + 1, kBatch - 1));
+        if (t == kBatch - 1) tiles.whole[m] = decay_of(before);
       }
     }
     __syncthreads();
@@ -330,11 +340,13 @@ cudaError_t launch_steps(const DeltaArgs& a, cudaStream_t s) {
 
 // Rows of a lane: one while a CTA of such has an SM for itself, two while two of those fit a SM, four beyond: k and q are read from
 // shared memory by every warp, which bounds many CTAs.  By one, two and four, us:
-//   fp32, 1024 x 16 heads 281, 305, 602; x 32 391, 305, 623; 4 x 1024 x 64 2687, 1725, 1409
-//   bf16, 16 x 16 6.3, 7.8, 13.0; 33 x 64 29.5, 19.1, 31.3; 4 x 33 x 32 56.3, 36.3, 32.2
+//   fp32, 1024 x 16 heads 254, 287, 571; x 32 352, 290, 623; 4 x 1024 x 64 2448, 1618, 1397; 300 and 1025 x 16 242, 261, 279
+//   bf16, 16 x 16 6.2, 7.9, 12.8; 33 x 64 28.2, 18.6, 30.4; 4 x 33 x 32 54.3, 35.7, 31.4
 template <typename T, int DK>
 cudaError_t steps(const DeltaArgs& a, cudaStream_t s) {
-  const long long ctas = (long long)a.nseq * a.H * (a.dv / kStepRows);
+  // (of the lengths only the longest and the sum are known: as many sequences as the sum has longest ones count)
+  const long long full = min(max((a.ntokens + a.max_len / 2) / max(a.max_len, 1), 1LL), (long long)a.nseq);
+  const long long ctas = full * a.H * (a.dv / kStepRows);
   return ctas <= 152 ? launch_steps<T, DK, 1>(a, s) : ctas <= 608 ? launch_steps<T, DK, 2>(a, s) : launch_steps<T, DK, 4>(a, s);
 }
 
@@ -354,8 +366,8 @@ cudaError_t decode(const DeltaArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// bf16 prompts of more tokens than these go by chunks, which take 15 us whatever they hold (32 heads: 16 tokens 8.2 us by the
-// recurrence, 33 15.1 and 14.9; 128 heads: 16 tokens 15.1 and 22.3, 33 32 and 22.7).
+// bf16 prompts of more tokens than these go by chunks, which take 15 us whatever they hold (32 heads: 24 tokens 10.2 us by the
+// recurrence, 33 15.0 and 15.0; 128 heads: 24 tokens 20.1 and 23.0, 33 31.4 and 23.2).
 static bool by_chunks(const DeltaArgs& a) {
   return a.io == ERS_DTYPE_BF16 && a.max_len > ((long long)a.nseq * a.H <= 64 ? 32 : 24);
 }

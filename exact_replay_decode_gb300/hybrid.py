@@ -107,7 +107,8 @@ class AttnCache:
     of slot_pages pages per slot (pages: a PagePool of both), and the tokens in use pos [nslots] int32.
 
     npages None: nslots * slot_pages, slot s starting out with its share of them.  Otherwise every page starts out free, and
-    pages_own(cache.pages, slots) hands them out.  k, v: tensors to use as the pages (they stay the cache's)."""
+    pages_own(cache.pages, slots) hands them out.  k, v: tensors to use as the pages (they stay the cache's).  The page calls
+    do not touch pos: after pages_fork(src, dst) the caller sets pos[dst] = pos[src], after pages_free pos[slot] = 0."""
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)

@@ -594,7 +594,7 @@ ERS_API ers_status ers_gdn_decode(const ers_linattn_dims* dims, const ers_linatt
  * Device errors: ERS_ESLOT (slot, or a page outside [0, npages): a verify's outputs are then undefined), ERS_EALIGN (pos
  *   outside the table), ERS_EINVAL (a parent that is neither an earlier place in use nor -1 or -2; a shared page or a
  *   slot listed twice; cu_seqlens not ascending within [0, ntokens]: nothing is appended at all), ERS_EOVERFLOW (no room in
- *   the table), ERS_ECOMMIT (accepted outside [0, T], a path outside [0, T)). */
+ *   the table), ERS_ECOMMIT (accepted outside [0, T], a path outside [0, T)), ERS_ETIMEOUT (a verify's outputs are undefined). */
 typedef struct ers_attn_dims {
   int32_t nheads;
   int32_t kv_heads;
