@@ -393,3 +393,63 @@ def test_captured_steps(io):
         graph.replay()
         torch.cuda.synchronize()
         assert cache.pos.tolist() == [902 + 2 * step, 44 + 4 * step]
+
+
+def test_pools_beyond_32_bits():
+    """Pages whose rows start beyond 2^31 elements and 2^32 bytes of the pool: read, written and committed to."""
+    ers = _ers()
+    KV, D, page, npages = 4, 128, 64, 70000                # 2.3e9 elements each
+    k, v = (torch.empty(npages, page, KV, D, dtype=BF16, device="cuda") for _ in range(2))
+    cache = ers.AttnCache(2, KV, D, page_tokens=page, slot_pages=4, npages=npages, k=k, v=v)
+    cache.pages.table.copy_(torch.tensor([[npages - 1, 3, 66000, npages - 2], [1, 69000, 2, 68000]], dtype=torch.int32))
+    cache.pages.refs[cache.pages.table.flatten().long()] = 1
+    rows = [torch.randn(300, KV, D, device="cuda", generator=_gen(s)).to(BF16) for s in (7, 8)]
+    ers.attn_append(cache, *rows, torch.tensor([0, 180, 300], dtype=torch.int32, device="cuda"))
+    assert torch.equal(cache.k[npages - 1], rows[0][:64]) and torch.equal(cache.v[69000][:56], rows[1][244:])
+    q, dk, dv = _drafts(27, 2, 3, 8, KV, D, BF16)
+    _check(ers.attn_verify(cache, q, dk, dv), cache, q, dk, dv)
+    ers.attn_commit(cache, dk, dv, torch.tensor([3, 2], dtype=torch.int32, device="cuda"))
+    assert torch.equal(cache.k[66000][52:55], dk[0]) and torch.equal(cache.v[69000][56:58], dv[1, :2])
+    _check(ers.attn_verify(cache, q, dk, dv, max_len=183), cache, q, dk, dv)
+
+
+@IO
+def test_on_another_stream(io):
+    """stream=: every allocation, launch and status of the calls belongs to that stream."""
+    ers = _ers()
+    cache = _cache(28, [700, 20], 2, 128, 64, io, room=8)
+    q, k, v = _drafts(29, 2, 4, 8, 2, 128, io)
+    accepted = torch.tensor([4, 1], dtype=torch.int32, device="cuda")
+    good = ers.attn_verify(cache, q, k, v, max_len=700)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o = ers.attn_verify(cache, q, k, v, max_len=700, stream=side)
+    ers.attn_commit(cache, k, v, accepted, stream=side)
+    after = ers.attn_verify(cache, q, k, v, max_len=700, stream=side, check=False)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(o, good) and cache.pos.tolist() == [704, 21]
+    _check(after, cache, q, k, v)
+
+
+@IO
+def test_a_fork_reads_its_parents_pages(io):
+    """Slots that share a prompt's pages attend to them; a row may only be added once the page is the slot's own."""
+    ers = _ers()
+    cache = ers.AttnCache(3, 2, 64, page_tokens=16, slot_pages=3, npages=7, io_dtype=io)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ers.pages_own(cache.pages, torch.tensor([0], **i32))
+    rows = [torch.randn(20, 2, 64, device="cuda", generator=_gen(s)).to(io) for s in (9, 10)]
+    ers.attn_append(cache, *rows, slot=torch.tensor([0], **i32))
+    ers.pages_fork(cache.pages, torch.tensor([0], **i32), torch.tensor([2], **i32))
+    cache.pos[2] = cache.pos[0]
+    q, k, v = _drafts(30, 2, 2, 4, 2, 64, io)
+    slot = torch.tensor([0, 2], **i32)
+    _check(ers.attn_verify(cache, q, k, v, slot=slot), cache, q, k, v, slots=[0, 2])
+    one = torch.ones(2, **i32)
+    with pytest.raises(ers.ErsError, match="ERS_EINVAL"):
+        ers.attn_commit(cache, k, v, one, slot=slot)
+    assert cache.pos.tolist() == [20, 0, 20]
+    ers.pages_own(cache.pages, torch.tensor([2], **i32))
+    ers.attn_commit(cache, k, v, one, slot=slot)
+    assert cache.pos.tolist() == [21, 0, 21]
+    _check(ers.attn_verify(cache, q, k, v, slot=slot), cache, q, k, v, slots=[0, 2])

@@ -289,3 +289,42 @@ def test_captured_and_on_other_streams(io):
            for a, b in zip(*sets)]
     _, states, _, off = _rule(*six, [6] * 300, c=(128 + 16) * 2.0 ** -24)
     assert ((cache.state.double() - states).norm(dim=-1) <= off).all()
+
+
+@pytest.mark.parametrize("io", [BF16, F32], ids=["bf16", "f32"])
+def test_states_beyond_32_bits(io):
+    """A pool of 2.2e9 floats: its last pages are read and written, by prompts and by tokens."""
+    ers = _ers()
+    H, npages = 32, 4200
+    cache = ers.LinAttnCache(2, H, 16, npages=npages, io_dtype=io, state=torch.empty(npages, H, 128, 128, device="cuda"))
+    cache.pages.table.copy_(torch.tensor([[npages - 1], [5]], dtype=torch.int32))
+    read = torch.tensor([-1, npages - 2], dtype=torch.int32, device="cuda")
+    cache.state[npages - 2] = torch.randn(H, 128, 128, device="cuda", generator=_gen(17)) * 0.3
+    init = torch.stack([torch.zeros_like(cache.state[0]), cache.state[npages - 2]])
+    args = _inputs(18, 72, H, 16, 128, 128, io)
+    prompt, token = [x[:70].contiguous() for x in args], [x[70:].contiguous() for x in args]
+    lens = [40, 30]
+    o = ers.gdn_prefill(cache, *prompt, _cu(lens), read_page=read)
+    o2 = ers.gdn_decode(cache, *token)
+    seq = [torch.cat([x[:40], x[70:71], x[40:70], x[71:]]) for x in args]
+    _check(torch.cat([o[:40], o2[:1], o[40:], o2[1:]]), cache.state[[npages - 1, 5]], seq, [41, 31], init, chunks=io == BF16)
+
+
+def test_more_sequences_than_tokens():
+    """Empty sequences around a few tokens, by chunks and by the recurrence."""
+    for n in (3, 40):
+        lens = [0] * 50 + [n] + [0] * 50 + [1, 0]
+        args = _inputs(19, n + 1, 4, 2, 64, 64, BF16)
+        init = torch.randn(len(lens), 4, 64, 64, device="cuda", generator=_gen(20))
+        o, fin = _ers().gdn_fwd(*args, _cu(lens), init_state=init, max_seqlen=n)
+        _check(o, fin, args, lens, init)
+        still = [i for i, m in enumerate(lens) if m == 0]
+        assert torch.equal(fin[still], init[still])
+
+
+@pytest.mark.parametrize("hint", [1, 10 ** 9])
+def test_max_seqlen_never_changes_what_is_computed(hint):
+    lens = [100, 3, 64]
+    args = _inputs(21, 167, 4, 2, 128, 128, BF16)
+    o, fin = _ers().gdn_fwd(*args, _cu(lens), max_seqlen=hint)
+    _check(o, fin, args, lens)
