@@ -14,9 +14,9 @@
 // memory) run beside each other: one loads while the other computes.
 //
 // What bounds it: a tile moves 32 KB (D 128), 0.74 us of an SM's share of the memory, and its exponentials take 512 cycles of each
-// scheduler.  64 trees of 16 drafts over 2269 to 4096 tokens x 8 heads: 184 us, 126 of them the bytes' (the 512 CTAs come in
-// waves of 304); one token over 32768 40 us in 37 parts (20 the bytes'; set-up, a part's first loads and the join are the rest);
-// 256 single tokens over 1024 212 us (160).  All loading threads polling in place of one cost 388 us in place of 184: they take
+// scheduler.  64 trees of 16 drafts over 2269 to 4096 tokens x 8 heads: 171 us, 126 of them the bytes' (the 512 CTAs come in
+// waves of 304; with a head's sequences side by side in place of a sequence's heads 185); one token over 32768 39 us in 37 parts (20 the bytes'; set-up, a part's first loads and the join are the rest);
+// 256 single tokens over 1024 214 us (160).  All loading threads polling in place of one cost 388 us in place of 185: they take
 // issue slots from the rows'.
 #include <string.h>
 
@@ -104,7 +104,9 @@ __global__ void __launch_bounds__(kBlock, 2) k_attn_tiles(const __grid_constant_
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(attn_smem) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = base + Sh::qtile;          // K, V, K, V
   Hdr& hd = *reinterpret_cast<Hdr*>(stages + kStages * 2 * Sh::tile);
-  const int split = blockIdx.x % a.nsplit, i = blockIdx.x / a.nsplit, kv = blockIdx.y % a.KV, row0 = blockIdx.y / a.KV * kM;
+  // the heads of a sequence's tokens side by side: their rows lie beside each other
+  const int heads = (a.T * (a.H / a.KV) + kM - 1) / kM * a.KV, head = blockIdx.x % heads, run = blockIdx.x / heads;
+  const int split = run % a.nsplit, i = run / a.nsplit, kv = head % a.KV, row0 = head / a.KV * kM;
   const int rep = a.H / a.KV, nrows = a.T * rep, tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0);
   const int row = row0 + tid;                  // of the threads that own rows
   const auto out_row = [&](int r) { return ((size_t)i * a.T + r / rep) * a.H + kv * rep + r % rep; };
@@ -456,7 +458,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   if (box < 8 || rows < box || rows > 0x7fffffff || !encode(&maps.k, a.k_pages, rows, a.KV, D, box) ||
       !encode(&maps.v, a.v_pages, rows, a.KV, D, box))
     box = 0;
-  k_attn_tiles<D><<<dim3((unsigned)(a.nseq * a.nsplit), tiles * a.KV), kBlock, Shape<D>::smem, s>>>(a, maps, box);
+  k_attn_tiles<D><<<(unsigned)((long long)a.nseq * a.nsplit * tiles * a.KV), kBlock, Shape<D>::smem, s>>>(a, maps, box);
   return cudaGetLastError();
 }
 
