@@ -189,12 +189,15 @@ __device__ __forceinline__ void publish() {
   after_sync();
 }
 
-// named barrier among `count` threads (id 1..15), and its AND-reduction form
+// named barrier among `count` threads (id 1..15), and its AND-reduction form.  Both are for whole warps, and for converged ones:
+// the lanes meet first, for some may come from a section of their own.
 __device__ __forceinline__ void named_sync(uint32_t id, uint32_t count) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 __device__ __forceinline__ bool named_sync_and(uint32_t id, uint32_t count, bool v) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
@@ -206,12 +209,14 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// warp-wide
+// warp-wide, by converged lanes as well
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols));
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
 }
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols));
 }
 
