@@ -33,11 +33,14 @@ def test_lanes_meet_before_barriers_and_tensor_memory_changes_hands(name):
     assert 0 <= body.find("__syncwarp();") < body.index("asm volatile")
 
 
-def test_attention_issues_by_one_lane_without_votes():
-    body = _body(_source("ers_attn_tc.cu"), "if (tid >= kIssueThread)")
-    loop = _body(body, "if (elected())")
-    assert "break" in loop and "mma_ts(" in loop
-    assert not re.search(r"__\w+_sync\(", body)
+def test_attentions_issuing_warp_goes_on_or_leaves_as_one():
+    """Its lanes vote on whether the next tile is there, so none may have left on its own: a wait's end is voted on as well."""
+    text = _source("ers_attn_tc.cu")
+    start = text.index("if (tid >= kIssueThread)")
+    body = text[start:text.index("else if (tid >= kLoadThread)", start)]
+    assert "__all_sync(kFull, mbar_test(" in body and "break;" in body
+    for m in re.finditer(r"\bwait\(", body):
+        assert body[:m.start()].endswith("__all_sync(kFull, ")
 
 
 def test_attention_outputs_meet_before_every_load():
