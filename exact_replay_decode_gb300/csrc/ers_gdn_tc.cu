@@ -11,8 +11,9 @@
 //
 // Precision: q, k and v are exact operands.  T' is taken as three bf16 terms (24 bits); W, S, M, U and the decayed U as
 // two (16 bits and more: each is off by at most 2^-17, in the mean 2^-18.7; a third term of all of them would double the products of the
-// serial loop).  The state itself is fp32 in registers, one rounded multiply-add a chunk: final states are 3e-6 of their size
-// off, over 97 tokens as over 32768.
+// serial loop).  The state itself is fp32 in registers, one rounded multiply-add a chunk by a factor of two floats (of one, whose
+// rounding is the same each time where the gate is, a state over 32768 tokens was 4e-5 off): final states are 3e-6 of their size
+// off, over 97 tokens as over 32768, and what they hold from n tokens ago sqrt(n / 64) 2^-24 more.
 //
 // What bounds it (2048 tokens x 32 heads of 128 x 128: 50 and 54 us).  k_gdn_inside: the dependent phases of a CTA, 21000 cycles
 // with two a SM (loads 7400, of two products of 128 x 128 x 64 and the scores' 4200, T 4500, the rest made and stored); barriers
@@ -42,9 +43,9 @@ constexpr float kLeast = -200.f;             // a lower log-gate is e^-200 = 0 i
 struct Factors {
   float since[kC];                           // e^(G_i)
   float left[kC];                            // e^(G_C - G_i)
-  float whole;                               // e^(G_C)
+  Decay whole;                               // e^(G_C): as two floats, for the state meets it once a chunk
   int bad;                                   // the first token with something that is not finite (kC: none)
-  float pad[126];
+  float pad[125];
 };
 static_assert(sizeof(Factors) == 1024, "whole copies");
 
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
       f.left[t] = exp2f(df_diff(all, s));
     }
     if (lane == 0) {
-      f.whole = exp2f(all.hi + all.lo);
+      f.whole = decay_of((all.hi + all.lo) * 0.69314718055994530942f);
       f.bad = sm.bad;
     }
   }
@@ -671,7 +672,8 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       }
       wait(hd, &hd.full[c & 1], c >> 1, a.status);
       const Factors& f = *reinterpret_cast<const Factors*>(gdn_smem + (c & 1) * St::size + St::f);
-      const float whole = f.whole, left = f.left[row];
+      const Decay whole = f.whole;
+      const float left = f.left[row];
       since = f.since[row];
       bad = f.bad;
       mbar_arrive(&hd.empty[c & 1]);
@@ -714,7 +716,7 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
       float v[X];
       tmem_sums<P>(quarter + Col::three + x0, v);
 #pragma unroll
-      for (int j = 0; j < X; ++j) s[j] = fmaf(whole, s[j], v[j]);
+      for (int j = 0; j < X; ++j) s[j] = whole.step(s[j], v[j]);
       before_sync();
     }
     if (chunks > 0 && !makes_u) outputs(chunks - 1);
