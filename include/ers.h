@@ -543,11 +543,15 @@ ERS_API ers_status ers_linattn_decode(const ers_linattn_dims* dims, const float*
  * ers_gdn_fwd: prompts from init_state [nseq, H, dv, dk] (NULL: zeros) to final_state (may be init_state itself).
  * ers_gdn_prefill / ers_gdn_decode: states in the pages of a pool, prompts or one token per sequence.
  * A NaN or infinity in a token may reach all of that head's outputs from that token on and its final state, and no others.
+ * Sums of finite tokens beyond 3e38 are infinite.  By the recurrence they reach the outputs of their state row from that token on and
+ *   the row's final state.  By chunks (below) also those of the row, or where products of keys overflow of the head, from the start of
+ *   the token's chunk on (chunks count from the sequence's first token); earlier chunks, other rows, heads and sequences keep theirs.
  * Precision: states are fp32.  fp32 prompts, single tokens and bf16 prompts of up to 24 (32 of few heads) tokens round each step to
  *   nearest (final states are within 2e-7 of their size of the rule's).  Longer bf16 prompts are formed in chunks of 64 tokens from
  *   operands of 16 bits and more: final states are 3e-6 of their size off, and the outputs' own rounding to 8 bits hides it.
  *   A state is rounded to nearest once every 64 tokens (fp32 prompts: 8): what it holds from n tokens ago is off by no more than
- *   sqrt(n / 64) 2^-24 of itself beside that (1.3e-6 at 32768; fp32 prompts sqrt(n / 8) 2^-24).  Values under 2^-110 of such operands have fewer bits; sums beyond 3e38 overflow.
+ *   sqrt(n / 64) 2^-24 of itself beside that (1.3e-6 at 32768; fp32 prompts sqrt(n / 8) 2^-24).  Values
+ *   under 2^-110 of the chunks' operands have fewer bits.
  *   How a prompt is split (nseq, max_seqlen) changes the order of sums; a log-gate under -200 counts as -200 there (0 in fp32 as well).
  * ntokens / 64 + nseq times nheads is at most 2^31 - 1 (ERS_EINVAL).
  * Device errors: ERS_ESLOT as for linear attention, and ERS_EINVAL (cu_seqlens not ascending within [0, ntokens]: of the recurrence,
