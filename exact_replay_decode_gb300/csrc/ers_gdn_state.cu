@@ -151,8 +151,12 @@ __global__ void __launch_bounds__(kStepThreads) k_gdn_steps(const __grid_constan
   Tiles& tiles = *reinterpret_cast<Tiles*>(smem);
   const int parts = a.dv / R, part = blockIdx.x % parts, unit = blockIdx.x / parts;   // a sequence's CTAs side by side
   const int i = unit / a.H, h = unit % a.H, g = h / (a.H / a.G);
+  // Beside the chunks of a call's longer sequences the grid may run while theirs does; it ends no sooner.
+  const auto done = [&] {
+    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   DeltaSeq s;
-  if (!delta_seq(a, i, h, &s)) return;
+  if (!delta_seq(a, i, h, &s)) return done();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, j = lane % kRowLanes;
   const int own = warp * kSide * rows + lane / kRowLanes;   // this lane's rows of the CTA: own + kSide * r
   const int d0 = part * R;
@@ -313,10 +317,12 @@ __global__ void __launch_bounds__(kStepThreads) k_gdn_steps(const __grid_constan
 #pragma unroll
     for (int x = 0; x < N; ++x)
       *reinterpret_cast<float4*>(s.out + (size_t)(d0 + own + kSide * r) * DK + 4 * (j + kRowLanes * x)) = st[r][x];
+  done();
 }
 
+// beside: as a programmatic dependent of the stream's last launch
 template <typename T, int DK, int rows>
-cudaError_t launch_steps(const DeltaArgs& a, cudaStream_t s) {
+cudaError_t launch_steps(const DeltaArgs& a, bool beside, cudaStream_t s) {
   constexpr int R = kStepRows * rows;
   using Tiles = StepTiles<T, DK, R>;
   const auto kernel = k_gdn_steps<T, DK, rows>;
@@ -334,8 +340,17 @@ cudaError_t launch_steps(const DeltaArgs& a, cudaStream_t s) {
       done[dev] = true;
     }
   }
-  kernel<<<dim3((unsigned)((long long)a.nseq * a.H * (a.dv / R))), kStepThreads, sizeof(Tiles), s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)a.nseq * a.H * (a.dv / R)));
+  cfg.blockDim = dim3(kStepThreads);
+  cfg.dynamicSmemBytes = sizeof(Tiles);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 // Rows of a lane: one while a CTA of such has an SM for itself, two while two of those fit a SM, four beyond: k and q are read from
@@ -343,11 +358,16 @@ cudaError_t launch_steps(const DeltaArgs& a, cudaStream_t s) {
 //   fp32, 1024 x 16 heads 254, 287, 571; x 32 352, 290, 623; 4 x 1024 x 64 2448, 1618, 1397; 300 and 1025 x 16 242, 261, 279
 //   bf16, 16 x 16 6.2, 7.9, 12.8; 33 x 64 28.2, 18.6, 30.4; 4 x 33 x 32 54.3, 35.7, 31.4
 template <typename T, int DK>
-cudaError_t steps(const DeltaArgs& a, cudaStream_t s) {
-  // (of the lengths only the longest and the sum are known: as many sequences as the sum has longest ones count)
-  const long long full = min(max((a.ntokens + a.max_len / 2) / max(a.max_len, 1), 1LL), (long long)a.nseq);
+cudaError_t steps(const DeltaArgs& a, bool beside, cudaStream_t s) {
+  // (of the lengths only the longest and the sum are known: as many sequences as the sum has longest ones count, or the others where
+  // the longer ones go by chunks)
+  const long long longest = max(a.max_len, 1), n = a.len1 == 0x7fffffff ? (a.ntokens + longest / 2) / longest
+                                                                       : a.nseq - (a.ntokens + longest - 1) / longest;
+  const long long full = min(max(n, 1LL), (long long)a.nseq);
   const long long ctas = full * a.H * (a.dv / kStepRows);
-  return ctas <= 152 ? launch_steps<T, DK, 1>(a, s) : ctas <= 608 ? launch_steps<T, DK, 2>(a, s) : launch_steps<T, DK, 4>(a, s);
+  return ctas <= 152   ? launch_steps<T, DK, 1>(a, beside, s)
+         : ctas <= 608 ? launch_steps<T, DK, 2>(a, beside, s)
+                       : launch_steps<T, DK, 4>(a, beside, s);
 }
 
 template <typename T, int DK>
@@ -366,16 +386,36 @@ cudaError_t decode(const DeltaArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// bf16 prompts of more tokens than these go by chunks, which take 15 us whatever they hold (32 heads: 24 tokens 10.2 us by the
-// recurrence, 33 15.0 and 15.0; 128 heads: 24 tokens 20.1 and 23.0, 33 31.4 and 23.2).
-static bool by_chunks(const DeltaArgs& a) {
-  return a.io == ERS_DTYPE_BF16 && a.max_len > ((long long)a.nseq * a.H <= 64 ? 32 : 24);
+// bf16 sequences of more tokens than these go by chunks, which take 15 us whatever they hold (32 heads: 24 tokens 10.2 us by the
+// recurrence, 33 15.0 and 15.0; 128 heads: 24 tokens 20.1 and 23.0, 33 31.4 and 23.2).  A sequence's own length decides, on the
+// device, so that neither its neighbours nor a loose max_len take bits from a short one; where that leaves no short ones (the longest
+// length times the sequences is all tokens), one launch is spared.  With all of a call by chunks 2048 tokens and 256 single ones x 64
+// heads took 2084 us and 1.5 GB in place of 1185 and 0.7, 97 and 15 single ones x 32 73 us (45); 2048, 777, 513 and 1 x 64 270 (274),
+// 2048 and 63 of 20 x 32 334 (396).
+static int few_tokens(const DeltaArgs& a) { return (long long)a.nseq * a.H <= 64 ? 32 : 24; }
+
+// The sequences that go by chunks, as a call of their own; false: there are none.
+static bool by_chunks(const DeltaArgs& a, DeltaArgs* many) {
+  if (a.io != ERS_DTYPE_BF16 || a.max_len <= few_tokens(a)) return false;
+  *many = a;
+  many->len0 = (long long)a.nseq * a.max_len <= a.ntokens ? 0 : few_tokens(a) + 1;
+  many->most = many->len0 == 0 || a.ntokens / many->len0 > a.nseq ? a.nseq : (int)(a.ntokens / many->len0);
+  return true;
 }
 
+static cudaError_t by_steps(const DeltaArgs& a, bool beside, cudaStream_t s) {
+  if (a.io == ERS_DTYPE_BF16)
+    return a.dk == 64 ? steps<__nv_bfloat16, 64>(a, beside, s) : steps<__nv_bfloat16, 128>(a, beside, s);
+  return a.dk == 64 ? steps<float, 64>(a, beside, s) : steps<float, 128>(a, beside, s);
+}
+cudaError_t gdn_steps_beside(const DeltaArgs& a, cudaStream_t s) { return by_steps(a, true, s); }
+
 cudaError_t gdn_fwd(const DeltaArgs& a, cudaStream_t s) {
-  if (by_chunks(a)) return gdn_tc(a, s);
-  if (a.io == ERS_DTYPE_BF16) return a.dk == 64 ? steps<__nv_bfloat16, 64>(a, s) : steps<__nv_bfloat16, 128>(a, s);
-  return a.dk == 64 ? steps<float, 64>(a, s) : steps<float, 128>(a, s);
+  DeltaArgs many;
+  if (!by_chunks(a, &many)) return by_steps(a, false, s);
+  DeltaArgs few = a;
+  few.len1 = many.len0 - 1;
+  return gdn_tc(many, many.len0 > 0 ? &few : nullptr, s);
 }
 
 cudaError_t gdn_decode(const DeltaArgs& a, cudaStream_t s) {
@@ -383,6 +423,9 @@ cudaError_t gdn_decode(const DeltaArgs& a, cudaStream_t s) {
   return a.dk == 64 ? decode<float, 64>(a, s) : decode<float, 128>(a, s);
 }
 
-size_t gdn_fwd_workspace(const DeltaArgs& a) { return by_chunks(a) ? gdn_tc_workspace(a) : 0; }
+size_t gdn_fwd_workspace(const DeltaArgs& a) {
+  DeltaArgs many;
+  return by_chunks(a, &many) ? gdn_tc_workspace(many) : 0;
+}
 
 }  // namespace ers

@@ -69,8 +69,13 @@ struct Layout {
   }
 };
 
-// Sequence i's chunks are numbers t0 / kC + i on: as many as there can be lie between those of two neighbours.
-__host__ __device__ __forceinline__ long long chunk_numbers(long long ntokens, int nseq) { return ntokens / kC + nseq; }
+// The chunks of sequence i, which starts at token t0, are numbers t0 / kC + min(i, t0 / len0) on, if it has len0 tokens or more: from
+// one such sequence to the next the minimum grows by one at least, so that as many as there can be lie between their first ones,
+// and sequences of fewer tokens take no numbers.
+__device__ __forceinline__ int first_number(const DeltaArgs& a, int t0, int i) {
+  return t0 / kC + (a.len0 == 0 ? i : min(i, t0 / a.len0));
+}
+long long chunk_numbers(const DeltaArgs& a) { return a.ntokens / kC + a.most; }
 
 // Whether the sequences' borders ascend within [0, ntokens], all of them: chunks are found by them.  By all threads.
 __device__ __forceinline__ bool ascending(const DeltaArgs& a) {
@@ -195,16 +200,17 @@ __global__ void __launch_bounds__(kInside, 2) k_gdn_inside(const __grid_constant
   InsideSmem<DK, DV>& sm = *reinterpret_cast<InsideSmem<DK, DV>*>(gdn_smem);
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0), lane = tid % 32, rep = a.H / a.G;
   const int number = blockIdx.x / a.H, h = blockIdx.x % a.H, g = h / rep;   // a chunk's heads side by side: their inputs share sectors
-  if (!ascending(a) || (smem_u32(gdn_smem) & 1023u) != 0) return;   // (the next launch reports it)
+  if (a.len0 > 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // short sequences' recurrence
+  if (!ascending(a) || (smem_u32(gdn_smem) & 1023u) != 0) return;   // (k_gdn_through reports it)
   int i = 0;
   for (int hi = a.nseq - 1; i < hi;) {         // the last sequence whose chunks start at or before this one
     const int mid = (i + hi + 1) / 2;
-    if ((long long)(a.cu[mid] / kC) + mid <= number) i = mid;
+    if (first_number(a, a.cu[mid], mid) <= number) i = mid;
     else hi = mid - 1;
   }
   const int s0 = a.cu[i], len = a.cu[i + 1] - s0;
-  const long long c0 = ((long long)number - (s0 / kC + i)) * kC;
-  if (c0 >= len) return;
+  const long long c0 = (long long)(number - first_number(a, s0, i)) * kC;
+  if (len < a.len0 || c0 < 0 || c0 >= len) return;
   const int t0 = s0 + (int)c0, n = min(kC, len - (int)c0);
   const Layout lay(a.H, a.G, DK, DV);
   uint8_t* chunk = static_cast<uint8_t*>(a.ws) + number * lay.chunk;
@@ -486,7 +492,31 @@ struct Hdr {
   uint64_t full[2], empty[2], s_ready, u_ready, u_decayed, u_written, s_done, o_done, o_free;
   uint32_t tmem;
   int dead;                                  // a wait gave up: no further wait waits, no copy or MMA is issued
+  int seq, counts[kThrough / 32];            // for chunk_sequence
 };
+
+// The n-th of the sequences that have chunks, where not all of them can; -1: there are fewer.  By all threads.
+__device__ __forceinline__ int chunk_sequence(const DeltaArgs& a, int n, Hdr& hd) {
+  if (a.most == a.nseq) return n;
+#pragma unroll 1
+  for (int x0 = 0; x0 < a.nseq; x0 += kThrough) {
+    const int x = x0 + threadIdx.x;
+    const bool is = x < a.nseq && a.cu[x + 1] - a.cu[x] >= a.len0;
+    const int count = __syncthreads_count(is);
+    if (n >= count) {
+      n -= count;
+      continue;
+    }
+    const uint32_t mine = __ballot_sync(kFull, is);
+    if (threadIdx.x % 32 == 0) hd.counts[threadIdx.x / 32] = __popc(mine);
+    __syncthreads();
+    for (int w = 0; w < threadIdx.x / 32; ++w) n -= hd.counts[w];
+    if (is && __popc(mine & ((1u << threadIdx.x % 32) - 1)) == n) hd.seq = x;
+    __syncthreads();
+    return hd.seq;
+  }
+  return -1;
+}
 
 // Shared memory: two stages, S^T as two terms side by side [dk x 2 P], U and the decayed U as two terms each [64 x 2 P].
 // A stage: for each 64 columns Q's and W hi's atoms, one A operand of 128 rows; W lo's, as rows 64-127 of one whose other rows are
@@ -524,17 +554,18 @@ __global__ void __launch_bounds__(kThrough, 1) k_gdn_through(const __grid_consta
   constexpr int X = P / 2;                     // state rows of a thread
   extern __shared__ __align__(1024) uint8_t gdn_smem[];
   Hdr& hd = *reinterpret_cast<Hdr*>(gdn_smem + St::hdr);
-  const int parts = a.dv / P, part = blockIdx.x % parts, unit = blockIdx.x / parts, i = unit / a.H, h = unit % a.H;
+  const int parts = a.dv / P, part = blockIdx.x % parts, unit = blockIdx.x / parts, h = unit % a.H;
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid / 32, 0), lane = tid % 32;
   if (!ascending(a) || (smem_u32(gdn_smem) & 1023u) != 0) {
     if (tid == 0) report(a.status, (smem_u32(gdn_smem) & 1023u) != 0 ? ERS_ECUDA : ERS_EINVAL);
     return;
   }
   DeltaSeq seq;
-  if (!delta_seq(a, i, h, &seq)) return;
+  const int i = chunk_sequence(a, unit / a.H, hd);
+  if (i < 0 || !delta_seq(a, i, h, &seq)) return;
   const int chunks = (seq.len + kC - 1) / kC, d0 = part * P;
   const Layout lay(a.H, a.G, DK, a.dv);
-  const uint8_t* first = static_cast<const uint8_t*>(a.ws) + (seq.t0 / kC + i) * lay.chunk;
+  const uint8_t* first = static_cast<const uint8_t*>(a.ws) + (size_t)first_number(a, seq.t0, i) * lay.chunk;
   const uint8_t *mine = first + (size_t)h * lay.head, *shared = first + (size_t)a.H * lay.head + (size_t)(h / (a.H / a.G)) * lay.group;
 
   if (warp == 9) tmem_alloc(&hd.tmem, Col::all);
@@ -759,32 +790,33 @@ cudaError_t launch_through(const DeltaArgs& a, cudaStream_t s) {
   static bool done[64] = {};
   const cudaError_t e = allow(k_gdn_through<DK, P>, Stage<DK, P>::smem, done, mu);
   if (e != cudaSuccess) return e;
-  k_gdn_through<DK, P><<<(unsigned)((long long)a.nseq * a.H * (a.dv / P)), kThrough, Stage<DK, P>::smem, s>>>(a);
+  k_gdn_through<DK, P><<<(unsigned)((long long)a.most * a.H * (a.dv / P)), kThrough, Stage<DK, P>::smem, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int DK, int DV>
-cudaError_t launch(const DeltaArgs& a, cudaStream_t s) {
+cudaError_t launch(const DeltaArgs& a, const DeltaArgs* few, cudaStream_t s) {
   static std::mutex mu;
   static bool done[64] = {};
   cudaError_t e = allow(k_gdn_inside<DK, DV>, sizeof(InsideSmem<DK, DV>), done, mu);
   if (e != cudaSuccess) return e;
-  k_gdn_inside<DK, DV><<<(unsigned)(chunk_numbers(a.ntokens, a.nseq) * a.H), kInside, sizeof(InsideSmem<DK, DV>), s>>>(a);
+  k_gdn_inside<DK, DV><<<(unsigned)(chunk_numbers(a) * a.H), kInside, sizeof(InsideSmem<DK, DV>), s>>>(a);
   e = cudaGetLastError();
+  if (e == cudaSuccess && few != nullptr) e = gdn_steps_beside(*few, s);
   if (e != cudaSuccess) return e;
   // 32 rows a CTA while every one of those has an SM for itself (2048 x 32 heads: 53 us, by 64 rows 81)
-  return (long long)a.nseq * a.H * (DV / 32) <= 152 ? launch_through<DK, 32>(a, s) : launch_through<DK, 64>(a, s);
+  return (long long)a.most * a.H * (DV / 32) <= 152 ? launch_through<DK, 32>(a, s) : launch_through<DK, 64>(a, s);
 }
 
 }  // namespace
 
 size_t gdn_tc_workspace(const DeltaArgs& a) {
-  return align256(Layout(a.H, a.G, a.dk, a.dv).chunk * chunk_numbers(a.ntokens, a.nseq));
+  return align256(Layout(a.H, a.G, a.dk, a.dv).chunk * chunk_numbers(a));
 }
 
-cudaError_t gdn_tc(const DeltaArgs& a, cudaStream_t s) {
-  if (a.dk == 64) return a.dv == 64 ? launch<64, 64>(a, s) : launch<64, 128>(a, s);
-  return a.dv == 64 ? launch<128, 64>(a, s) : launch<128, 128>(a, s);
+cudaError_t gdn_tc(const DeltaArgs& a, const DeltaArgs* few, cudaStream_t s) {
+  if (a.dk == 64) return a.dv == 64 ? launch<64, 64>(a, few, s) : launch<64, 128>(a, few, s);
+  return a.dv == 64 ? launch<128, 64>(a, few, s) : launch<128, 128>(a, few, s);
 }
 
 }  // namespace ers

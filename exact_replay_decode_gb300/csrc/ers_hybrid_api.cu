@@ -49,6 +49,7 @@ ers::DeltaArgs delta_args(const ers_linattn_dims* d, int32_t nseq, int64_t ntoke
   a.nseq = nseq;
   a.ntokens = ntokens;
   a.max_len = max_seqlen < ntokens ? max_seqlen : (int32_t)ntokens;
+  a.len1 = 0x7fffffff;
   return a;
 }
 

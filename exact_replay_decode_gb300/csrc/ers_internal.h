@@ -236,6 +236,8 @@ struct DeltaArgs {
   int H, G, dk, dv, io;
   float scale;
   int nseq, max_len;
+  int len0, len1;           // the launch's sequences: those of len0 to len1 tokens,
+  int most;                 // of which there are no more than this (chunks)
   long long ntokens;
   const int32_t* cu;        // prompts: [nseq + 1]
   const void* q;            // [T, G, dk]
@@ -259,7 +261,9 @@ struct DeltaArgs {
 cudaError_t gdn_fwd(const DeltaArgs& a, cudaStream_t s);      // prompts
 cudaError_t gdn_decode(const DeltaArgs& a, cudaStream_t s);   // one token per sequence
 size_t gdn_fwd_workspace(const DeltaArgs& a);                 // (by io, H, G, dk, dv, nseq, ntokens, max_len)
-cudaError_t gdn_tc(const DeltaArgs& a, cudaStream_t s);       // chunks on the tensor cores (bf16), ers_gdn_tc.cu
+// chunks on the tensor cores (bf16), ers_gdn_tc.cu, and, if few is not null, its sequences by the recurrence
+cudaError_t gdn_tc(const DeltaArgs& a, const DeltaArgs* few, cudaStream_t s);
+cudaError_t gdn_steps_beside(const DeltaArgs& a, cudaStream_t s);   // prompts by the recurrence, while the last launch runs
 size_t gdn_tc_workspace(const DeltaArgs& a);
 
 // attention over a paged cache of keys and values, ers_attn.cu

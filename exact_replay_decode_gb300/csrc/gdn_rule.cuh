@@ -14,7 +14,7 @@ struct DeltaSeq {
 };
 
 // Sequence i, head h.  False (reported by one thread) where an index leads outside the caller's memory:
-// nothing of that sequence may then be touched.
+// nothing of that sequence may then be touched.  False as well where another launch takes the sequence.
 __device__ __forceinline__ bool delta_seq(const DeltaArgs& a, int i, int h, DeltaSeq* s) {
   int32_t err = ERS_OK;
   s->t0 = i;
@@ -42,7 +42,7 @@ __device__ __forceinline__ bool delta_seq(const DeltaArgs& a, int i, int h, Delt
     }
   }
   if (err != ERS_OK && threadIdx.x == 0) report(a.status, err);
-  return err == ERS_OK;
+  return err == ERS_OK && s->len >= a.len0 && s->len <= a.len1;
 }
 
 }  // namespace ers

@@ -538,24 +538,28 @@ ERS_API ers_status ers_linattn_decode(const ers_linattn_dims* dims, const float*
  *     are: a final state may be copied into ers_gdn_cache.anchor, and its bf16 cast into read_copy).
  *   q, k [T, G, dk], v, o [T, H, dv] in the io dtype, g (log of the gate, <= 0), beta [T, H] fp32.  The rule forgets as long as
  *     beta |k|^2 <= 2; beyond that states grow, as they do in exact arithmetic.
- *   workspace: a 16-byte aligned buffer of the size that the query returns for the call's sizes (may be 0: then NULL will do;
- *     bf16 prompts by chunks: 1.3 KB for each token and head of 128 x 128).
+ *   max_seqlen: the longest sequence's length as the caller knows it: it chooses between launches, not what they compute (below).
+ *   workspace: a 16-byte aligned buffer of the size that the query returns for the call's sizes (may be 0: then NULL will do).  By
+ *     chunks of 64 tokens (below), (ntokens / 64 + n) (81 KB nheads + 32 KB ngroups) at dk = dv = 128, where n is the number of sequences, or
+ *     ntokens / 25 (33) if that is less: 1.3 KB a token and head of a long prompt, 11 GB for 131072 tokens x 64 heads of 8 groups.
  * ers_gdn_fwd: prompts from init_state [nseq, H, dv, dk] (NULL: zeros) to final_state (may be init_state itself).
  * ers_gdn_prefill / ers_gdn_decode: states in the pages of a pool, prompts or one token per sequence.
  * A NaN or infinity in a token may reach all of that head's outputs from that token on and its final state, and no others.
  * Sums of finite tokens beyond 3e38 are infinite.  By the recurrence they reach the outputs of their state row from that token on and
  *   the row's final state.  By chunks (below) also those of the row, or where products of keys overflow of the head, from the start of
  *   the token's chunk on (chunks count from the sequence's first token); earlier chunks, other rows, heads and sequences keep theirs.
- * Precision: states are fp32.  fp32 prompts, single tokens and bf16 prompts of up to 24 (32 of few heads) tokens round each step to
- *   nearest (final states are within 2e-7 of their size of the rule's).  Longer bf16 prompts are formed in chunks of 64 tokens from
+ * Precision: states are fp32.  fp32 prompts, single tokens and bf16 sequences of up to 24 tokens (32 where nseq nheads <= 64) go by the
+ *   recurrence, each step rounded to nearest (final states are within 2e-7 of their size of the rule's); whatever else the call holds,
+ *   and with the same bits.  Only where max_seqlen is in that range, or where nseq max_seqlen <= ntokens (so that all are that long), do
+ *   all of a call's sequences go by the one way that max_seqlen says.  Longer bf16 sequences are formed in chunks of 64 tokens from
  *   operands of 16 bits and more: final states are 3e-6 of their size off, and the outputs' own rounding to 8 bits hides it.
  *   A state is rounded to nearest once every 64 tokens (fp32 prompts: 8): what it holds from n tokens ago is off by no more than
  *   sqrt(n / 64) 2^-24 of itself beside that (1.3e-6 at 32768; fp32 prompts sqrt(n / 8) 2^-24).  Values
  *   under 2^-110 of the chunks' operands have fewer bits.
- *   How a prompt is split (nseq, max_seqlen) changes the order of sums; a log-gate under -200 counts as -200 there (0 in fp32 as well).
+ *   A log-gate under -200 counts as -200 there (0 in fp32 as well).
  * ntokens / 64 + nseq times nheads is at most 2^31 - 1 (ERS_EINVAL).
  * Device errors: ERS_ESLOT as for linear attention, and ERS_EINVAL (cu_seqlens not ascending within [0, ntokens]: of the recurrence,
- *   that sequence's, of chunks all sequences'): the outputs are then left unwritten; ERS_ETIMEOUT: they are undefined. */
+ *   that sequence's, of chunks all such sequences'): the outputs are then left unwritten; ERS_ETIMEOUT: they are undefined. */
 ERS_API size_t ers_gdn_fwd_workspace_size(const ers_linattn_dims* dims, int32_t nseq, int64_t ntokens, int32_t max_seqlen);
 ERS_API ers_status ers_gdn_fwd(const ers_linattn_dims* dims, int32_t nseq, int64_t ntokens, int32_t max_seqlen,
                                const int32_t* cu_seqlens, const void* q, const void* k, const void* v, const float* g,
