@@ -16,8 +16,9 @@
 // Precision: q, k and v are exact operands.  T' is taken as three bf16 terms (24 bits); W, S, M, U and the decayed U as
 // two (16 bits and more: each is off by at most 2^-17, in the mean 2^-18.7; a third term of all of them would double the products of the
 // serial loop).  The state itself is fp32 in registers, one rounded multiply-add a chunk by a factor of two floats (of one, whose
-// rounding is the same each time where the gate is, a state over 32768 tokens was 4e-5 off): final states are 3e-6 of their size
-// off, over 97 tokens as over 32768, and what they hold from n tokens ago sqrt(n / 64) 2^-24 more.
+// rounding is the same each time where the gate is, a state over 32768 tokens was 4e-5 off): final states are 2e-6 to
+// 5e-6 of their size off (three roundings in quadrature: 6.6e-6 at most), over 97 tokens as over 32768, and what they hold from n
+// tokens ago sqrt(n / 64) 2^-24 more.
 //
 // What bounds it (2048 tokens x 32 heads of 128 x 128: 50 and 54 us).  k_gdn_inside: the dependent phases of a CTA, 21000 cycles
 // with two a SM (loads 7400, of two products of 128 x 128 x 64 and the scores' 4200, T 4500, the rest made and stored); barriers

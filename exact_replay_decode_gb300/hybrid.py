@@ -39,8 +39,9 @@ def gdn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, 
     """The gated delta rule over packed prompts (ers_gdn_fwd).
 
     q, k [T,G,dk], v [T,H,dv] (bf16 or fp32; dk, dv 64 or 128), g (log-gates, <= 0), beta [T,H] fp32; cu_seqlens, init_state
-    and max_seqlen as in linattn_fwd.  Returns (o [T,H,dv], final_state [S,H,dv,dk] fp32); a final state may start a
-    GdnCache: anchor.copy_(state), read_copy.copy_(state)."""
+    and max_seqlen as in linattn_fwd (a short bf16 sequence has the recurrence's bits whatever max_seqlen and its neighbours are;
+    ers.h has the workspace that a call allocates).  Returns (o [T,H,dv], final_state [S,H,dv,dk] fp32); a final state may
+    start a GdnCache: anchor.copy_(state), read_copy.copy_(state)."""
     io = _io_from(q)
     T, G, dk = q.shape
     H, dv = v.shape[1], v.shape[2]

@@ -549,13 +549,12 @@ ERS_API ers_status ers_linattn_decode(const ers_linattn_dims* dims, const float*
  *   the row's final state.  By chunks (below) also those of the row, or where products of keys overflow of the head, from the start of
  *   the token's chunk on (chunks count from the sequence's first token); earlier chunks, other rows, heads and sequences keep theirs.
  * Precision: states are fp32.  fp32 prompts, single tokens and bf16 sequences of up to 24 tokens (32 where nseq nheads <= 64) go by the
- *   recurrence, each step rounded to nearest (final states are within 2e-7 of their size of the rule's); whatever else the call holds,
- *   and with the same bits.  Only where max_seqlen is in that range, or where nseq max_seqlen <= ntokens (so that all are that long), do
- *   all of a call's sequences go by the one way that max_seqlen says.  Longer bf16 sequences are formed in chunks of 64 tokens from
- *   operands of 16 bits and more: final states are 3e-6 of their size off, and the outputs' own rounding to 8 bits hides it.
- *   A state is rounded to nearest once every 64 tokens (fp32 prompts: 8): what it holds from n tokens ago is off by no more than
- *   sqrt(n / 64) 2^-24 of itself beside that (1.3e-6 at 32768; fp32 prompts sqrt(n / 8) 2^-24).  Values
- *   under 2^-110 of the chunks' operands have fewer bits.
+ *   recurrence, each step rounded to nearest, whatever else the call holds and with the same bits.  Only where max_seqlen is in that
+ *   range, or where nseq max_seqlen <= ntokens (so that all are that long), do all of a call's sequences go by the one way that
+ *   max_seqlen says.  Longer bf16 sequences are formed in chunks of 64 tokens from operands of 16 bits and more.
+ *   In the 2-norm, relative to the state: the recurrence's final states are within sqrt(2 n) 2^-24 of the rule's where they remember n
+ *   tokens (measured: 2e-7 to 4e-7 for some hundred, 1.7e-6 for 4096); those of chunks within 6.6e-6 + sqrt(n / 64) 2^-24 (2e-6 to
+ *   5e-6), which the outputs' own rounding to 8 bits hides.  Values under 2^-110 of the chunks' operands have fewer bits.
  *   A log-gate under -200 counts as -200 there (0 in fp32 as well).
  * ntokens / 64 + nseq times nheads is at most 2^31 - 1 (ERS_EINVAL).
  * Device errors: ERS_ESLOT as for linear attention, and ERS_EINVAL (cu_seqlens not ascending within [0, ntokens]: of the recurrence,

@@ -11,7 +11,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_gdn_rule import BF16, F32, _check, _ers, _gen, _inputs
+from test_gpu_gdn_rule import BF16, F32, _check, _ers, _gen, _inputs, _norm, _rule
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,22 @@ def test_weak_writes_over_a_long_memory(io, T):
     init = torch.randn(1, 2, 128, 128, device="cuda", generator=_gen(34)) * 0.3
     o, fin = _ers().gdn_fwd(*args, init_state=init)
     _check(o, fin, args, [T], init)
+
+
+@pytest.mark.parametrize("weak", ["none", "gates", "gates and writes"])
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("io,T", [(BF16, 1), (BF16, 24), (BF16, 97), (BF16, 1025), (BF16, 4096), (F32, 24), (F32, 300), (F32, 4096)], ids=str)
+def test_final_states_are_as_near_as_the_header_says(io, T, dk, weak):
+    """Chunks: three operands of 16 bits whose roundings, 2^-17 at most and 2^-18 in the mean, add up in quadrature (6.6e-6), and the
+    state's own rounding every 64 tokens.  The recurrence: for each token a rounded product and sum into the state, an eighth of
+    its factor's rounding, and the residual's own error, whose sum of dk products is as far off as sqrt(dk) 2^-24 / 2 of |S k|, which is
+    |S| / sqrt(dk) for keys that point anywhere: half a rounding of S.  Together less than two a token, in quadrature, for no
+    longer than the state remembers."""
+    args = list(_inputs(35, T, 4, 2, dk, 128, io, 1.0 if weak == "none" else 1.0 / T))
+    if weak == "gates and writes":
+        args[4] *= 4.0 / T
+    init = torch.randn(1, 4, 128, dk, device="cuda", generator=_gen(36)) * 0.3
+    _, fin = _ers().gdn_fwd(*args, init_state=init)
+    _, want, _, _ = _rule(*args, [T], init)
+    chunks = io == BF16 and T > 32
+    assert _norm(fin, want) <= ((6.6e-6 + math.sqrt(T / 64) * 2.0 ** -24) if chunks else (math.sqrt(2 * T) + 2) * 2.0 ** -24)
