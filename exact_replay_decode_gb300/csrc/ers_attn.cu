@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_commit(const __grid_constant_
 // as run at once (two a SM on the tensor cores, four of the fp32 kernel), and a quarter for each part that a row is joined
 // of (bf16; a tile of the fp32 kernel takes much longer than that).  By 1, 2, 4, 8, 16, 32 and 64 parts, us:
 //   1 x 32768 tokens 593, 310, 163, 89, 54, 41, 54 (38: 40)     8 x 8192, 4 drafts 156, 89, 57, 67, 79, 98, 138
-//   1 x 1000 26, 20, 16, 15, 16 (6: 12.5)                       64 x 4096, 16 drafts 186, 220, 265, 339 (171 by 1 since)
+//   1 x 1000 26, 20, 16, 15, 16 (6: 12.5)                       64 x 4096, 16 drafts 186, 220, 265, 339 (175 by 1 since)
 //   16 x 4096, 64 drafts 105, 148, 183, 237                     fp32, 4 x up to 1000, 7 drafts 129, 69, 40, 26, 21
 void attn_plan(AttnArgs* a, int max_len) {
   const bool tiles_of = a->io == ERS_DTYPE_BF16;

@@ -14,7 +14,7 @@
 // memory) run beside each other: one loads while the other computes.
 //
 // What bounds it: a tile moves 32 KB (D 128), 0.74 us of an SM's share of the memory, and its exponentials take 512 cycles of each
-// scheduler.  64 trees of 16 drafts over 2269 to 4096 tokens x 8 heads: 171 us, 126 of them the bytes' (the 512 CTAs come in
+// scheduler.  64 trees of 16 drafts over 2269 to 4096 tokens x 8 heads: 175 us, 126 of them the bytes' (the 512 CTAs come in
 // waves of 304; with a head's sequences side by side in place of a sequence's heads 185); one token over 32768 39 us in 37 parts (20 the bytes'; set-up, a part's first loads and the join are the rest);
 // 256 single tokens over 1024 214 us (160).  All loading threads polling in place of one cost 388 us in place of 185: they take
 // issue slots from the rows'.

@@ -20,7 +20,7 @@
 // 5e-6 of their size off (three roundings in quadrature: 6.6e-6 at most), over 97 tokens as over 32768, and what they hold from n
 // tokens ago sqrt(n / 64) 2^-24 more.
 //
-// What bounds it (2048 tokens x 32 heads of 128 x 128: 50 and 54 us).  k_gdn_inside: the dependent phases of a CTA, 21000 cycles
+// What bounds it (2048 tokens x 32 heads of 128 x 128: 51 and 55 us).  k_gdn_inside: the dependent phases of a CTA, 21000 cycles
 // with two a SM (loads 7400, of two products of 128 x 128 x 64 and the scores' 4200, T 4500, the rest made and stored); barriers
 // are most of its stalls.  k_gdn_through: the chain of a chunk, 2900 cycles of 32 state rows (4700 of 64): the state into terms 300,
 // W S^T 1300, U into terms 550, K^T U' and the state's step 760.  Where all parts of 32 rows have an SM they are taken

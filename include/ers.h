@@ -590,7 +590,9 @@ ERS_API ers_status ers_gdn_decode(const ers_linattn_dims* dims, const ers_linatt
  *   -2: the place is empty, its output zeros.  A draft attends to the slot's pos tokens, the drafts of its path and itself:
  *     o = sum_j softmax_j(scale q.k_j) v_j,  in fp32 with one rounding at the end (bf16: the weights are rounded to bf16 once,
  *   relative to the largest).  What is not attended to may hold anything: other drafts, what pages hold behind pos.
- *   A NaN or infinity in a draft's v makes the outputs of its path from there on NaN.  A row whose every product is -inf has zeros.
+ *   A NaN or infinity in a draft's v makes the outputs of its path from there on NaN, one in the v of the slot's tokens those of all
+ *   its drafts (of the heads that share it).  A row whose every product is -inf has zeros; products whose scale q.k is beyond 2e38
+ *   overflow (bf16: weights are powers of two of scale log2(e) q.k).
  *   max_len: the most tokens of any slot as the caller knows it (>= 0): it chooses how the work is split, never what is
  *   computed; a split changes the order of fp32 sums.  workspace: 16-byte aligned, of the size that the query returns.
  * ers_attn_append: rows of packed new tokens, k, v [ntokens, kv_heads, D] by cu_seqlens [nseq+1], go behind their
